@@ -26,6 +26,8 @@
  *     MEGAMOE_ERR_WORKSPACE   workspace_bytes is smaller than the matching *_workspace_bytes()
  *     MEGAMOE_ERR_LAUNCH      a kernel launch failed (hipGetLastError after the launch)
  *     MEGAMOE_ERR_DEVICE      the current device is not gfx950
+ *     MEGAMOE_ERR_ALIGN       a pointer is not aligned as its function asks (the scored router and
+ *                             the MXFP4 calls)
  * - Data errors on the device are defined away: a top-k id outside
  *   [expert_begin, expert_begin + num_experts) is "not local" and is dropped.
  * - Layouts are row-major.  NVFP4 tensors are three parts:
@@ -35,6 +37,11 @@
  *     gs     float             one FP32 global scale per tensor (per expert and matrix for
  *                               weights); the real value of element i is
  *                               e2m1(code_i) * e4m3(scale_block(i)) / gs.
+ *   MXFP4 tensors (OCP microscaling) are two parts:
+ *     codes  uint8 [rows, K/2]  as above;
+ *     scales uint8 [rows, K/32] one E8M0 block scale per 32 consecutive K elements: 2^(byte - 127),
+ *                               255 = NaN; the real value of element i is
+ *                               e2m1(code_i) * 2^(scale_block(i) - 127).
  * - Expert weights: W13 codes [E, 2I, H/2], scales [E, 2I, H/16], gs [E]; rows 0..I-1 are the
  *   gate projection and rows I..2I-1 the up projection.  W2 codes [E, H, I/2], scales
  *   [E, H, I/16], gs [E].  bf16 tensors are passed as raw 16-bit storage.
@@ -55,12 +62,24 @@ extern "C" {
 #define MEGAMOE_ERR_WORKSPACE (-3)
 #define MEGAMOE_ERR_LAUNCH (-4)
 #define MEGAMOE_ERR_DEVICE (-5)
+#define MEGAMOE_ERR_ALIGN (-6)
+
+/* Element types of the arguments that come in two. */
+#define MEGAMOE_DTYPE_BF16 0
+#define MEGAMOE_DTYPE_F32 1
+
+/* Scores of moe_router_scores. */
+#define MEGAMOE_SCORE_SOFTMAX 0
+#define MEGAMOE_SCORE_SIGMOID 1
 
 /* Largest number of local experts one call handles. */
 #define MEGAMOE_MAX_EXPERTS 1024
 
 /* Largest number of global experts the router takes. */
 #define MEGAMOE_ROUTER_MAX_EXPERTS 1024
+
+/* Largest number of expert groups of moe_router_scores. */
+#define MEGAMOE_ROUTER_MAX_GROUPS 64
 
 /* Slots of the per-workgroup h amax written by moe_grouped_gemm_l1_silu (every slot, every call). */
 #define MEGAMOE_L1_AMAX_PARTS 1280
@@ -126,6 +145,70 @@ int32_t moe_route_logits(const float* logits, int32_t T, int32_t num_experts_glo
                          int32_t* counts, int32_t* expert_offsets, int32_t* padded_offsets,
                          int32_t* row_token, int32_t* token_rows, int32_t* sched, void* workspace,
                          size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------------------------
+ * moe_router_scores - router logits -> top-k expert ids and weights by scores: sigmoid or
+ * softmax, a balance bias, expert groups, renormalised weights.
+ *
+ * For each token, with z its logits:
+ *   s_e = sigmoid(z_e), or softmax over all num_experts_global experts, in float64;
+ *   c_e = fl32(s_e) + bias_e in float32 (the choice; the bias steers the choice alone);
+ *   groups: the experts lie in n_group groups of num_experts_global / n_group consecutive ids; a
+ *     group's score is the float32 sum of its group_top largest choices (of those there are);
+ *     the topk_group best groups stay;
+ *   ids: the k largest choices of the groups that stay, in descending order; ties, of groups and of
+ *     experts, go to the lower index;
+ *   weights: fl32(scale * s / S), S = the sum of the k chosen scores with renormalize, else 1
+ *     (0 where S is 0).
+ * A logit of -inf or NaN, and a choice of -inf or NaN, make an expert unavailable: it is never
+ * chosen.  With fewer than k available, the remaining slots get id -1 and weight 0 (which
+ * moe_route_permute drops).  +inf counts as the largest float.
+ *
+ * logits             [T, num_experts_global], dtype MEGAMOE_DTYPE_F32 or MEGAMOE_DTYPE_BF16.
+ * bias               nullable float32 [num_experts_global].
+ * score              MEGAMOE_SCORE_SIGMOID or MEGAMOE_SCORE_SOFTMAX.
+ * n_group, topk_group  1 and 1 = no groups.      group_top  1 or 2.
+ * topk_ids int32 [T, k];  topk_weights float32 [T, k].
+ * Limits: 0 <= T, 1 <= num_experts_global <= MEGAMOE_ROUTER_MAX_EXPERTS, T*k < 2^31,
+ * n_group <= MEGAMOE_ROUTER_MAX_GROUPS and a divisor of num_experts_global, topk_group <= n_group,
+ * 1 <= k <= min(64, topk_group * num_experts_global / n_group), scale finite.
+ * ---------------------------------------------------------------------------------------- */
+int32_t moe_router_scores(const void* logits, int32_t dtype, int32_t T, int32_t num_experts_global, int32_t k,
+                          const float* bias, int32_t score, int32_t n_group, int32_t topk_group,
+                          int32_t group_top, int32_t renormalize, float scale, int32_t* topk_ids,
+                          float* topk_weights, void* stream);
+
+/* ------------------------------------------------------------------------------------------
+ * moe_route_scores - moe_router_scores, then moe_route_permute on the ids it wrote, in one call
+ * (as moe_route_logits for moe_router_topk).  Checks are those of both, all made before any launch.
+ * ---------------------------------------------------------------------------------------- */
+int32_t moe_route_scores(const void* logits, int32_t dtype, int32_t T, int32_t num_experts_global, int32_t k,
+                         const float* bias, int32_t score, int32_t n_group, int32_t topk_group,
+                         int32_t group_top, int32_t renormalize, float scale, int32_t expert_begin,
+                         int32_t num_experts, int32_t pad_multiple, int32_t block_m_override,
+                         int32_t* topk_ids, float* topk_weights, int32_t* counts, int32_t* expert_offsets,
+                         int32_t* padded_offsets, int32_t* row_token, int32_t* token_rows, int32_t* sched,
+                         void* workspace, size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------------------------
+ * moe_router_scores_bwd - gradient of moe_router_scores' weights with respect to the logits, for
+ * fixed ids (the choice itself has no gradient, nor has the bias).
+ *
+ * With g the gradient of the weights and n_j = s_j / S over the k slots: g'_j = scale * g_j, or
+ * with renormalize scale / S * (g_j - sum_i g_i n_i);
+ *   sigmoid: grad_e = g'_e s_e (1 - s_e);   softmax: grad_e = s_e (g'_e - sum_j g'_j s_j)
+ * with g'_e the sum over the slots that name e (0 for the others), in float64 with one rounding.
+ * Ids outside [0, num_experts_global) (the empty slots) take no part.
+ *
+ * logits, dtype, score, renormalize, scale   as given to moe_router_scores.
+ * topk_ids int32 [T, k];  grad_weights float32 [T, k];  grad_logits [T, num_experts_global] in
+ * dtype, every element written; it may be the logits' own memory.
+ * Limits as for moe_router_scores.
+ * ---------------------------------------------------------------------------------------- */
+int32_t moe_router_scores_bwd(const void* logits, int32_t dtype, int32_t T, int32_t num_experts_global,
+                              int32_t k, int32_t score, int32_t renormalize, float scale,
+                              const int32_t* topk_ids, const float* grad_weights, void* grad_logits,
+                              void* stream);
 
 /* ------------------------------------------------------------------------------------------
  * moe_route_permute - local filter, per-expert counts, offsets, stable permutation, tile table.
@@ -514,6 +597,79 @@ int32_t nvfp4_linear_gate_up_silu_nvfp4(const uint8_t* a_codes, const uint8_t* a
                                         const float* h_gs, uint8_t* h_codes, uint8_t* h_scales,
                                         float* h_amax_parts, void* workspace, size_t workspace_bytes,
                                         void* stream);
+
+/* ------------------------------------------------------------------------------------------
+ * mxfp4_quantize_act, mxfp4_dequantize - bf16 or float32 to MXFP4, and MXFP4 to bf16.
+ *
+ * Per block of 32: scale exponent e = floor(log2(amax)) - 2, at least -127 (byte 0, also for a
+ * block of zeros); an element's code is the E2M1 point nearest to x / 2^e, ties to the even code,
+ * saturating at +-6, sign copied from x.  Results are bit-exact with that definition.  A block with
+ * an infinity or a NaN gets scale 255 and zero codes, and decodes to NaN.  There is no global scale
+ * and no pass over the whole tensor.
+ *
+ * x            [rows, cols], dtype MEGAMOE_DTYPE_BF16 or MEGAMOE_DTYPE_F32.
+ * row_valid    nullable int32 [rows]: rows with row_valid[r] < 0 are not read and get zero codes and
+ *              scales (pass row_token to quantize permuted rows).
+ * codes        uint8 [rows, cols/2];  scales uint8 [rows, cols/32].
+ * out_bf16     bf16 [rows, cols]: the values, exact; beyond bf16's range (6 * 2^126 and up) infinite.
+ * Limits: rows >= 0, cols > 0 and a multiple of 32; x, codes and out_bf16 aligned to 16 bytes.
+ * ---------------------------------------------------------------------------------------- */
+int32_t mxfp4_quantize_act(const void* x, int32_t dtype, int64_t rows, int64_t cols,
+                           const int32_t* row_valid, uint8_t* codes, uint8_t* scales, void* stream);
+int32_t mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols,
+                         void* out_bf16, void* stream);
+
+/* ------------------------------------------------------------------------------------------
+ * mxfp4_linear, mxfp4_linear_gate_up_silu - dense MXFP4 products.
+ *
+ *   out[m, n] = bf16( sum_k a[m, k] * W[n, k] )
+ *   h[m, i]   = bf16( SiLU(g) * u ),  g / u = sum_k a[m, k] * W13[i or I+i, k]
+ * on gfx950's block-scaled matrix instructions: exact products, FP32 accumulation.  A NaN scale
+ * makes every output that reads its block NaN.
+ * a_codes/a_scales   MXFP4 A [M, K/2], [M, K/32] (e.g. from mxfp4_quantize_act).
+ * w_codes/w_scales   [N, K/2], [N, K/32];  w13 [2I, K/2], [2I, K/32], rows 0..I-1 gate, I..2I-1 up.
+ * out_bf16 bf16 [M, N];  h_bf16 bf16 [M, I].
+ * Limits: 0 <= M < 2^31, K >= 128 and a multiple of 128, N and I >= 16 and multiples of 16, below
+ * 2^30; codes and outputs aligned to 16 bytes, scales to 4.  With M == 0 the call enqueues nothing.
+ * ---------------------------------------------------------------------------------------- */
+int32_t mxfp4_linear(const uint8_t* a_codes, const uint8_t* a_scales, int64_t M, int32_t K,
+                     const uint8_t* w_codes, const uint8_t* w_scales, int32_t N, void* out_bf16, void* stream);
+int32_t mxfp4_linear_gate_up_silu(const uint8_t* a_codes, const uint8_t* a_scales, int64_t M, int32_t K,
+                                  const uint8_t* w13_codes, const uint8_t* w13_scales, int32_t I,
+                                  void* h_bf16, void* stream);
+
+/* ------------------------------------------------------------------------------------------
+ * moe_grouped_gemm_l1_silu_mxfp4, moe_grouped_gemm_l2_mxfp4 - the experts' products on MXFP4
+ * weights and activations: the operations of moe_grouped_gemm_l1_silu and moe_grouped_gemm_l2
+ * without global scales.  For each expert e and each of its rows r
+ * (padded_offsets[e] <= r < padded_offsets[e] + counts[e]):
+ *   h[r, i] = bf16( SiLU(g) * u ),  g / u = sum_k x[row_token[r], k] * W13[e, i or I+i, k]
+ *   y[r, n] = bf16( sum_k h[r, k] * W2[e, n, k] )
+ * Rows that hold no assignment are not written, experts with no rows are never read.
+ *
+ * x_codes/x_scales   MXFP4 x per token [T, H/2], [T, H/32].
+ * h_codes/h_scales   MXFP4 h [M_cap, I/2], [M_cap, I/32] (mxfp4_quantize_act of h with row_valid =
+ *              row_token).
+ * row_token, padded_offsets, counts   as written by moe_route_permute (its sched is not read).
+ * w13 [E, 2I, H/2], [E, 2I, H/32];  w2 [E, H, I/2], [E, H, I/32].
+ * M_cap        rows of h and y: megamoe_row_capacity(T, k, E, P).
+ * max_rows_per_expert  a bound on counts[e] the caller expects, or 0 if none: it may change which
+ *              kernels launch, never the results; a bound that is too low costs time only.
+ * h_bf16 bf16 [M_cap, I];  y_bf16 bf16 [M_cap, H].
+ * Limits: E as for moe_route_permute; the reduced dimension (H for L1, I for L2) a multiple of 128,
+ * the output dimension a multiple of 16; alignment as for mxfp4_linear.  With M_cap == 0 the row
+ * arrays may be NULL and the call enqueues nothing.
+ * ---------------------------------------------------------------------------------------- */
+int32_t moe_grouped_gemm_l1_silu_mxfp4(const uint8_t* x_codes, const uint8_t* x_scales,
+                                       const int32_t* row_token, const int32_t* padded_offsets,
+                                       const int32_t* counts, const uint8_t* w13_codes,
+                                       const uint8_t* w13_scales, int32_t E, int32_t H, int32_t I,
+                                       int64_t M_cap, int32_t max_rows_per_expert, void* h_bf16, void* stream);
+int32_t moe_grouped_gemm_l2_mxfp4(const uint8_t* h_codes, const uint8_t* h_scales,
+                                  const int32_t* padded_offsets, const int32_t* counts,
+                                  const uint8_t* w2_codes, const uint8_t* w2_scales, int32_t E, int32_t H,
+                                  int32_t I, int64_t M_cap, int32_t max_rows_per_expert, void* y_bf16,
+                                  void* stream);
 
 /* ------------------------------------------------------------------------------------------
  * moe_combine - routing-weighted combine of the expert outputs back into token order.

@@ -3,6 +3,7 @@
 #include <hip/hip_runtime.h>
 
 #include <atomic>
+#include <cmath>
 #include <cstring>
 
 #include "../../include/megamoe.h"
@@ -561,6 +562,151 @@ int32_t nvfp4_linear_gate_up_silu_nvfp4(const uint8_t* a_codes, const uint8_t* a
   ga.q_codes = h_codes;
   ga.q_scales = h_scales;
   return launch_status(launch_gemm_l1(ga, cls, s));
+}
+
+// ---- scored router -----------------------------------------------------------------------------
+
+static bool dtype_ok(int32_t d) { return d == MEGAMOE_DTYPE_BF16 || d == MEGAMOE_DTYPE_F32; }
+static bool score_ok(int32_t s) { return s == MEGAMOE_SCORE_SOFTMAX || s == MEGAMOE_SCORE_SIGMOID; }
+// The caller's pointers that kernels read or write in words wider than their elements.
+static bool aligned(const void* p, size_t to) { return reinterpret_cast<uintptr_t>(p) % to == 0; }
+
+static int32_t scores_args_ok(const void* logits, int32_t dtype, int32_t T, int32_t Eg, int32_t k, int32_t score,
+                              int32_t n_group, int32_t topk_group, int32_t group_top, float scale,
+                              const int32_t* topk_ids, const float* topk_weights) {
+  if (!router_shape_ok(T, Eg, k) || !dtype_ok(dtype) || !score_ok(score)) return MEGAMOE_ERR_SHAPE;
+  if (n_group < 1 || n_group > MEGAMOE_ROUTER_MAX_GROUPS || Eg % n_group != 0 || topk_group < 1 ||
+      topk_group > n_group || (group_top != 1 && group_top != 2) || k > topk_group * (Eg / n_group) ||
+      !std::isfinite(scale))
+    return MEGAMOE_ERR_SHAPE;
+  if (T > 0 && (!logits || !topk_ids || !topk_weights)) return MEGAMOE_ERR_NULL;
+  return MEGAMOE_OK;
+}
+
+int32_t moe_router_scores(const void* logits, int32_t dtype, int32_t T, int32_t num_experts_global, int32_t k,
+                          const float* bias, int32_t score, int32_t n_group, int32_t topk_group, int32_t group_top,
+                          int32_t renormalize, float scale, int32_t* topk_ids, float* topk_weights, void* stream) {
+  const int32_t rc = scores_args_ok(logits, dtype, T, num_experts_global, k, score, n_group, topk_group, group_top,
+                                    scale, topk_ids, topk_weights);
+  if (rc != MEGAMOE_OK) return rc;
+  const int32_t dev = check_device();
+  if (dev != MEGAMOE_OK) return dev;
+  const RouterScoreArgs a{logits, bias, T, num_experts_global, k, score, n_group, topk_group, group_top,
+                          renormalize != 0, scale, topk_ids, topk_weights};
+  return launch_status(launch_router_scores(a, dtype, static_cast<hipStream_t>(stream)));
+}
+
+int32_t moe_route_scores(const void* logits, int32_t dtype, int32_t T, int32_t num_experts_global, int32_t k,
+                         const float* bias, int32_t score, int32_t n_group, int32_t topk_group, int32_t group_top,
+                         int32_t renormalize, float scale, int32_t expert_begin, int32_t num_experts,
+                         int32_t pad_multiple, int32_t block_m_override, int32_t* topk_ids, float* topk_weights,
+                         int32_t* counts, int32_t* expert_offsets, int32_t* padded_offsets, int32_t* row_token,
+                         int32_t* token_rows, int32_t* sched, void* workspace, size_t workspace_bytes, void* stream) {
+  int32_t rc = scores_args_ok(logits, dtype, T, num_experts_global, k, score, n_group, topk_group, group_top, scale,
+                              topk_ids, topk_weights);
+  if (rc != MEGAMOE_OK) return rc;
+  rc = route_args_ok(T, k, expert_begin, num_experts, pad_multiple, block_m_override, topk_ids, counts,
+                     expert_offsets, padded_offsets, row_token, token_rows, sched, workspace, workspace_bytes);
+  if (rc != MEGAMOE_OK) return rc;
+  const int32_t dev = check_device();
+  if (dev != MEGAMOE_OK) return dev;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  const RouterScoreArgs a{logits, bias, T, num_experts_global, k, score, n_group, topk_group, group_top,
+                          renormalize != 0, scale, topk_ids, topk_weights};
+  rc = launch_status(launch_router_scores(a, dtype, s));
+  if (rc != MEGAMOE_OK) return rc;
+  return launch_status(launch_route(topk_ids, T, k, expert_begin, num_experts, pad_multiple, block_m_override, counts,
+                                    expert_offsets, padded_offsets, row_token,
+                                    megamoe_row_capacity(T, k, num_experts, pad_multiple), token_rows, sched,
+                                    static_cast<int32_t*>(workspace), s));
+}
+
+int32_t moe_router_scores_bwd(const void* logits, int32_t dtype, int32_t T, int32_t num_experts_global, int32_t k,
+                              int32_t score, int32_t renormalize, float scale, const int32_t* topk_ids,
+                              const float* grad_weights, void* grad_logits, void* stream) {
+  if (!router_shape_ok(T, num_experts_global, k) || !dtype_ok(dtype) || !score_ok(score) || !std::isfinite(scale))
+    return MEGAMOE_ERR_SHAPE;
+  if (T > 0 && (!logits || !topk_ids || !grad_weights || !grad_logits)) return MEGAMOE_ERR_NULL;
+  const int32_t dev = check_device();
+  if (dev != MEGAMOE_OK) return dev;
+  const RouterScoreBwdArgs a{logits, T, num_experts_global, k, score, renormalize != 0, scale, topk_ids, grad_weights,
+                             grad_logits};
+  return launch_status(launch_router_scores_bwd(a, dtype, static_cast<hipStream_t>(stream)));
+}
+
+// ---- MXFP4 ---------------------------------------------------------------------------------------
+
+static bool mx_matrix_ok(int64_t rows, int64_t cols) {
+  return rows >= 0 && cols > 0 && cols % 32 == 0 && rows <= ((int64_t)1 << 40) / cols;
+}
+
+int32_t mxfp4_quantize_act(const void* x, int32_t dtype, int64_t rows, int64_t cols, const int32_t* row_valid,
+                           uint8_t* codes, uint8_t* scales, void* stream) {
+  if (!mx_matrix_ok(rows, cols) || !dtype_ok(dtype)) return MEGAMOE_ERR_SHAPE;
+  if (rows > 0 && (!x || !codes || !scales)) return MEGAMOE_ERR_NULL;
+  if (!aligned(x, 16) || !aligned(codes, 16)) return MEGAMOE_ERR_ALIGN;
+  const int32_t dev = check_device();
+  if (dev != MEGAMOE_OK) return dev;
+  return launch_status(launch_mx_quant(x, dtype, rows, cols, row_valid, codes, scales,
+                                       static_cast<hipStream_t>(stream)));
+}
+
+int32_t mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols, void* out_bf16,
+                         void* stream) {
+  if (!mx_matrix_ok(rows, cols)) return MEGAMOE_ERR_SHAPE;
+  if (rows > 0 && (!codes || !scales || !out_bf16)) return MEGAMOE_ERR_NULL;
+  if (!aligned(codes, 16) || !aligned(out_bf16, 16)) return MEGAMOE_ERR_ALIGN;
+  const int32_t dev = check_device();
+  if (dev != MEGAMOE_OK) return dev;
+  return launch_status(launch_mx_dequant(codes, scales, rows, cols, out_bf16, static_cast<hipStream_t>(stream)));
+}
+
+// Checks and launch shared by the four MXFP4 products.  rows: rows of the output buffer.
+static int32_t mx_gemm(const MxGemmArgs& a, bool l1, int64_t rows, int32_t max_rows_per_expert, void* stream) {
+  if (a.E < 1 || a.E > MEGAMOE_MAX_EXPERTS || a.K < 128 || a.K % 128 != 0 || a.N < 16 || a.N % 16 != 0 ||
+      a.N >= (1 << 30) || rows < 0 || rows >= (int64_t)1 << 31 || max_rows_per_expert < 0)
+    return MEGAMOE_ERR_SHAPE;
+  if (!a.w_codes || !a.w_scales) return MEGAMOE_ERR_NULL;
+  if (rows > 0 && (!a.a_codes || !a.a_scales || !a.out)) return MEGAMOE_ERR_NULL;
+  if (!aligned(a.a_codes, 16) || !aligned(a.w_codes, 16) || !aligned(a.a_scales, 4) || !aligned(a.w_scales, 4) ||
+      !aligned(a.out, 16))
+    return MEGAMOE_ERR_ALIGN;
+  const int32_t dev = check_device();
+  if (dev != MEGAMOE_OK) return dev;
+  if (rows == 0) return MEGAMOE_OK;  // no rows: nothing to compute or write
+  return launch_status(launch_mx_gemm(a, l1, static_cast<hipStream_t>(stream)));
+}
+
+int32_t mxfp4_linear(const uint8_t* a_codes, const uint8_t* a_scales, int64_t M, int32_t K, const uint8_t* w_codes,
+                     const uint8_t* w_scales, int32_t N, void* out_bf16, void* stream) {
+  const MxGemmArgs a{a_codes, a_scales, nullptr, nullptr, nullptr, w_codes, w_scales, 1, K, N, M, out_bf16};
+  return mx_gemm(a, false, M, 0, stream);
+}
+
+int32_t mxfp4_linear_gate_up_silu(const uint8_t* a_codes, const uint8_t* a_scales, int64_t M, int32_t K,
+                                  const uint8_t* w13_codes, const uint8_t* w13_scales, int32_t I, void* h_bf16,
+                                  void* stream) {
+  const MxGemmArgs a{a_codes, a_scales, nullptr, nullptr, nullptr, w13_codes, w13_scales, 1, K, I, M, h_bf16};
+  return mx_gemm(a, true, M, 0, stream);
+}
+
+int32_t moe_grouped_gemm_l1_silu_mxfp4(const uint8_t* x_codes, const uint8_t* x_scales, const int32_t* row_token,
+                                       const int32_t* padded_offsets, const int32_t* counts,
+                                       const uint8_t* w13_codes, const uint8_t* w13_scales, int32_t E, int32_t H,
+                                       int32_t I, int64_t M_cap, int32_t max_rows_per_expert, void* h_bf16,
+                                       void* stream) {
+  if (!padded_offsets || !counts || (M_cap > 0 && !row_token)) return MEGAMOE_ERR_NULL;
+  const MxGemmArgs a{x_codes, x_scales, row_token, padded_offsets, counts, w13_codes, w13_scales, E, H, I, 0, h_bf16};
+  return mx_gemm(a, true, M_cap, max_rows_per_expert, stream);
+}
+
+int32_t moe_grouped_gemm_l2_mxfp4(const uint8_t* h_codes, const uint8_t* h_scales, const int32_t* padded_offsets,
+                                  const int32_t* counts, const uint8_t* w2_codes, const uint8_t* w2_scales, int32_t E,
+                                  int32_t H, int32_t I, int64_t M_cap, int32_t max_rows_per_expert, void* y_bf16,
+                                  void* stream) {
+  if (!padded_offsets || !counts) return MEGAMOE_ERR_NULL;
+  const MxGemmArgs a{h_codes, h_scales, nullptr, padded_offsets, counts, w2_codes, w2_scales, E, I, H, 0, y_bf16};
+  return mx_gemm(a, false, M_cap, max_rows_per_expert, stream);
 }
 
 }  // extern "C"

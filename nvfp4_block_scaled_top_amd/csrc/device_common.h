@@ -59,6 +59,21 @@ __device__ __forceinline__ uint32_t f32_to_bf16_bits(float f) {
   return (b + 0x7FFFu + ((b >> 16) & 1u)) >> 16;
 }
 
+// The same for any float: a NaN stays one (the rounding step could carry its mantissa away).
+__device__ __forceinline__ uint32_t f32_to_bf16_any(float f) {
+  return f != f ? 0x7FC0u : f32_to_bf16_bits(f);
+}
+
+// double -> bf16 bits with one rounding: to float toward an odd last bit (which keeps what lies below
+// it), then to nearest even.
+__device__ __forceinline__ uint32_t f64_to_bf16_bits(double d) {
+  const float f = (float)d;
+  uint32_t b = __float_as_uint(f);
+  const double back = (double)f;
+  if (back != d && !(b & 1u)) b += (d > back) == (f > 0.0f || (f == 0.0f && d > 0.0)) ? 1u : 0xFFFFFFFFu;
+  return f != f ? 0x7FC0u : f32_to_bf16_bits(__uint_as_float(b));
+}
+
 __device__ __forceinline__ float bf16_bits_to_f32(uint32_t h) { return __uint_as_float(h << 16); }
 
 // ---------------------------------------------------------------------------------------------

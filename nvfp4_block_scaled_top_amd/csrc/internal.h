@@ -45,6 +45,27 @@ hipError_t route_noalloc_scratch(int32_t** addr);
 hipError_t launch_router(const float* logits, int32_t T, int32_t Eg, int32_t k, int32_t* ids, float* weights,
                          hipStream_t stream);
 
+// ---- scored router ---------------------------------------------------------------------------
+struct RouterScoreArgs {
+  const void* logits;
+  const float* bias;  // [E] or NULL
+  int32_t T, E, k, score, n_group, topk_group, group_top, renormalize;
+  float scale;
+  int32_t* ids;
+  float* weights;
+  int32_t span = 0;  // lanes of a wave that hold one group (set by the launcher)
+};
+hipError_t launch_router_scores(const RouterScoreArgs& a, int dtype, hipStream_t stream);
+struct RouterScoreBwdArgs {
+  const void* logits;
+  int32_t T, E, k, score, renormalize;
+  float scale;
+  const int32_t* ids;
+  const float* grad_weights;
+  void* grad_logits;
+};
+hipError_t launch_router_scores_bwd(const RouterScoreBwdArgs& a, int dtype, hipStream_t stream);
+
 // Routing and the quantization of x in one launch (decode sizes: T*k <= 1024, T*H <= 2^16).
 bool route_quant_fusable(int32_t T, int32_t k, int64_t H);
 hipError_t launch_route_quant_small(const int32_t* topk_ids, int32_t T, int32_t k, int32_t e0, int32_t E, int32_t P,
@@ -120,6 +141,25 @@ struct FfnArgs {
 hipError_t launch_ffn_small(const FfnArgs& a, hipStream_t stream);
 // n floats at p set to v on the stream (graph-safe: a kernel, no memset node).
 hipError_t launch_fill_f32(float* p, int n, float v, hipStream_t stream);
+
+// ---- MXFP4 -----------------------------------------------------------------------------------
+hipError_t launch_mx_quant(const void* x, int dtype, int64_t rows, int64_t cols, const int32_t* row_valid,
+                           uint8_t* codes, uint8_t* scales, hipStream_t stream);
+hipError_t launch_mx_dequant(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols, void* out,
+                             hipStream_t stream);
+struct MxGemmArgs {
+  const uint8_t* a_codes;   // [*, K/2]; rows gathered through row_token when given
+  const uint8_t* a_scales;  // [*, K/32]
+  const int32_t* row_token;
+  const int32_t* padded_offsets;  // NULL with counts: one group of M rows
+  const int32_t* counts;
+  const uint8_t* w_codes;   // [E, N or 2N, K/2]
+  const uint8_t* w_scales;  // [E, N or 2N, K/32]
+  int32_t E, K, N;          // N = output columns (gate+up: weights have 2N rows)
+  int64_t M;                // rows of the one group without tables
+  void* out;                // bf16 [*, N]
+};
+hipError_t launch_mx_gemm(const MxGemmArgs& a, bool l1, hipStream_t stream);
 
 // ---- dense layers (one group of M rows) -------------------------------------------------------
 // int32 workspace layout: counts [1], padded offsets [2], tile table [sched_len(1)], then the

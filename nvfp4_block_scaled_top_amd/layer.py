@@ -293,3 +293,96 @@ class MoELayer:
         self.l2(w, stream)
         self.combine(self._rows(self.topk_weights, self.T), stream)
         return self._rows(self.out, self.T)
+
+
+@dataclasses.dataclass
+class MXMoEWeights:
+    """MXFP4 expert weights: codes and block scales only, no global scale."""
+    w13_codes: torch.Tensor   # uint8 [E, 2I, H/2]
+    w13_scales: torch.Tensor  # uint8 [E, 2I, H/32]
+    w2_codes: torch.Tensor    # uint8 [E, H, I/2]
+    w2_scales: torch.Tensor   # uint8 [E, H, I/32]
+
+    @property
+    def num_experts(self) -> int:
+        return self.w13_codes.shape[0]
+
+    @property
+    def hidden(self) -> int:
+        return self.w13_codes.shape[2] * 2
+
+    @property
+    def intermediate(self) -> int:
+        return self.w13_codes.shape[1] // 2
+
+    def nbytes_expert(self) -> int:
+        """MXFP4 bytes of one expert (codes + block scales)."""
+        return sum(t[0].numel() for t in (self.w13_codes, self.w13_scales, self.w2_codes, self.w2_scales))
+
+    @staticmethod
+    def empty(E: int, H: int, I: int, device="cuda") -> "MXMoEWeights":
+        u8 = dict(dtype=torch.uint8, device=device)
+        return MXMoEWeights(torch.empty(E, 2 * I, H // 2, **u8), torch.empty(E, 2 * I, H // 32, **u8),
+                            torch.empty(E, H, I // 2, **u8), torch.empty(E, H, I // 32, **u8))
+
+
+def quantize_expert_mx_into(weights: MXMoEWeights, e: int, w13: torch.Tensor, w2: torch.Tensor) -> None:
+    """MXFP4-quantize one expert's bf16 or float32 matrices on the GPU."""
+    mm.mxfp4_quantize_act(w13, weights.w13_codes[e], weights.w13_scales[e])
+    mm.mxfp4_quantize_act(w2, weights.w2_codes[e], weights.w2_scales[e])
+
+
+class MXMoELayer:
+    """The routed-expert layer on MXFP4 weights and activations, for T tokens, top-k, E local experts,
+    hidden H, intermediate I, pad P: route/permute, quantize x, L1 gate+up + SiLU, quantize h, L2
+    down, combine.  With block scales only, no step waits for a maximum over a whole tensor.
+    ``forward`` starts from top-k ids and weights, ``forward_scores`` from router logits."""
+
+    def __init__(self, T: int, k: int, E: int, H: int, I: int, P: int = 1, expert_begin: int = 0, device="cuda"):
+        self.T, self.k, self.E, self.H, self.I, self.P, self.expert_begin = T, k, E, H, I, P, expert_begin
+        self.M_cap = mm.megamoe_row_capacity(T, k, E, P)
+        i32 = dict(dtype=torch.int32, device=device)
+        u8 = dict(dtype=torch.uint8, device=device)
+        bf16 = dict(dtype=torch.bfloat16, device=device)
+        self.counts = torch.empty(E, **i32)
+        self.expert_offsets = torch.empty(E + 1, **i32)
+        self.padded_offsets = torch.empty(E + 1, **i32)
+        self.row_token = torch.empty(self.M_cap, **i32)
+        self.token_rows = torch.empty(T * k, **i32)
+        self.sched = torch.empty(mm.megamoe_sched_len(E), **i32)
+        self.route_ws = torch.empty(max(mm.megamoe_route_workspace_bytes(T, k, E), 4), **u8)
+        self.topk_ids = torch.empty(T, k, **i32)                      # written by forward_scores
+        self.topk_weights = torch.empty(T, k, dtype=torch.float32, device=device)
+        self.x_codes, self.x_scales = torch.empty(T, H // 2, **u8), torch.empty(T, H // 32, **u8)
+        self.h = torch.empty(self.M_cap, I, **bf16)
+        self.h_codes, self.h_scales = torch.empty(self.M_cap, I // 2, **u8), torch.empty(self.M_cap, I // 32, **u8)
+        self.y = torch.empty(self.M_cap, H, **bf16)
+        self.out = torch.empty(T, H, **bf16)
+
+    def experts(self, x: torch.Tensor, topk_weights: torch.Tensor, w: MXMoEWeights, stream=None) -> torch.Tensor:
+        """The steps after routing: x [T, H] bf16 -> out [T, H] bf16."""
+        mm.mxfp4_quantize_act(x, self.x_codes, self.x_scales, stream=stream)
+        mm.moe_grouped_gemm_l1_silu_mxfp4(self.x_codes, self.x_scales, self.row_token, self.padded_offsets, self.counts,
+                                          w.w13_codes, w.w13_scales, self.h, max_rows_per_expert=self.T, stream=stream)
+        mm.mxfp4_quantize_act(self.h, self.h_codes, self.h_scales, row_valid=self.row_token, stream=stream)
+        mm.moe_grouped_gemm_l2_mxfp4(self.h_codes, self.h_scales, self.padded_offsets, self.counts, w.w2_codes,
+                                     w.w2_scales, self.y, max_rows_per_expert=self.T, stream=stream)
+        mm.moe_combine(self.y, self.token_rows, topk_weights, self.out, stream=stream)
+        return self.out
+
+    def forward(self, x: torch.Tensor, topk_ids: torch.Tensor, topk_weights: torch.Tensor, w: MXMoEWeights,
+                stream=None) -> torch.Tensor:
+        """x bf16 [T, H], topk_ids int32 [T, k] global expert ids, topk_weights float32 [T, k]."""
+        mm.moe_route_permute(topk_ids, self.expert_begin, self.E, self.P, self.counts, self.expert_offsets,
+                             self.padded_offsets, self.row_token, self.token_rows, self.sched, self.route_ws,
+                             stream=stream)
+        return self.experts(x, topk_weights, w, stream)
+
+    def forward_scores(self, x: torch.Tensor, logits: torch.Tensor, w: MXMoEWeights, bias=None, stream=None,
+                       **router) -> torch.Tensor:
+        """x bf16 [T, H], logits float32 or bf16 [T, E_global]; router: the options of
+        moe_router_scores.  The chosen ids and weights are left in topk_ids / topk_weights."""
+        mm.moe_route_scores(logits, self.k, self.expert_begin, self.E, self.P, self.topk_ids, self.topk_weights,
+                            self.counts, self.expert_offsets, self.padded_offsets, self.row_token, self.token_rows,
+                            self.sched, self.route_ws, bias=bias, stream=stream, **router)
+        return self.experts(x, self.topk_weights, w, stream)

@@ -1,0 +1,181 @@
+"""The oracle of the scored router and the MXFP4 operators against brute force and differences, and
+the refusals of their entry points (host checks, no GPU needed)."""
+import os
+
+import numpy as np
+import pytest
+import torch
+
+from nvfp4_block_scaled_top_amd import layer, megamoe as mm
+from oracle import mxfp4_oracle as X
+
+
+@pytest.fixture(scope="module")
+def lib():
+    if not os.path.exists(mm.library_path()):
+        from nvfp4_block_scaled_top_amd import build_lib
+        build_lib.build()
+    return mm.lib()
+
+
+FAKE = 0x1000  # never dereferenced: every call below fails its host-side checks
+ODD = FAKE + 2
+
+
+def test_oracle_quantizer_is_nearest_point():
+    rng = np.random.default_rng(0)
+    x = rng.standard_normal((64, 96)) * np.exp2(rng.integers(-20, 20, (64, 1)).astype(float))
+    x[0] = 0.0
+    x[1, :32] = np.tile([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0, 6.0], 4)  # every tie at scale 1
+    codes, scales = X.quantize(x)
+    v = X.decode(codes, scales)
+    unit = np.repeat(np.ldexp(1.0, scales.astype(int) - 127), 32, -1)
+    points = np.concatenate([X.E2M1, -X.E2M1])
+    best = np.abs(np.abs(x)[..., None] / unit[..., None] - X.E2M1).min(-1)
+    assert np.array_equal(np.abs(np.abs(x) - np.abs(v)) / unit, best)
+    assert np.isin(v / unit, points).all() and np.all((v == 0) | (np.sign(v) == np.sign(x)))
+    assert v[1, :8].tolist() == [0.0, 1.0, 1.0, 2.0, 2.0, 4.0, 4.0, 6.0]
+    amax = np.abs(x).reshape(64, 3, 32).max(-1)
+    assert np.array_equal(scales[1:], (np.floor(np.log2(amax[1:])) - 2 + 127).astype(np.uint8))
+    assert not scales[0].any() and not codes[0].any()
+
+
+def test_oracle_quantizer_extremes():
+    x = np.zeros((4, 32))
+    x[0, 3], x[1, 5] = np.inf, np.nan
+    x[2, 0] = 2.0 ** -133          # the smallest bf16: below half a step of the smallest scale
+    x[3, 0], x[3, 1] = 2.0 ** -126, -3 * 2.0 ** -128
+    codes, scales = X.quantize(x)
+    assert scales[:, 0].tolist() == [255, 255, 0, 0]
+    assert not codes[:3].any()
+    assert X.decode(codes, scales)[3, :2].tolist() == [2.0 ** -126, -3 * 2.0 ** -128]
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("renormalize", [True, False])
+def test_oracle_router_gradient_by_differences(score, renormalize):
+    rng = np.random.default_rng(3)
+    z = rng.standard_normal((5, 24))
+    ids, _ = X.router(z, 4, None, score, 4, 2, 2, renormalize, 2.5)
+    grad = rng.standard_normal((5, 4))
+
+    def loss(zz):
+        s = X.scores(zz, score)
+        p = np.take_along_axis(s, ids, 1)
+        w = 2.5 * (p / p.sum(1, keepdims=True) if renormalize else p)
+        return (w * grad).sum(1)
+
+    got = X.router_bwd(z, ids, grad, score, renormalize, 2.5)
+    h = 1e-5
+    for e in range(24):
+        d = np.zeros((5, 24))
+        d[:, e] = h
+        diff = (loss(z + d) - loss(z - d)) / (2 * h)
+        # central difference: third derivatives of order 10 times h^2 / 6, and the sums' rounding over h
+        assert np.abs(diff - got[:, e]).max() <= 1e-8
+
+
+def test_oracle_router_masks():
+    z = np.zeros((3, 8))
+    z[0] = -np.inf
+    z[1, 2:] = np.nan
+    z[2, 4:] = -np.inf
+    ids, w = X.router(z, 3, score="softmax", n_group=2, topk_group=1, group_top=2)
+    assert ids.tolist() == [[-1, -1, -1], [0, 1, -1], [0, 1, 2]]
+    assert w[0].tolist() == [0, 0, 0] and w[1].tolist() == [0.5, 0.5, 0]
+
+
+def test_scores_reject_bad_args(lib):
+    f = lib.moe_router_scores
+
+    def call(logits=FAKE, dtype=1, T=4, E=384, k=6, bias=None, score=1, n_group=8, topk_group=4, group_top=2, scale=1.0,
+             ids=FAKE, w=FAKE):
+        return f(logits, dtype, T, E, k, bias, score, n_group, topk_group, group_top, 1, scale, ids, w, None)
+
+    assert call(dtype=2) == -2 and call(dtype=-1) == -2
+    assert call(score=2) == -2
+    assert call(T=-1) == -2 and call(k=0) == -2 and call(k=65) == -2
+    assert call(E=1032) == -2 and call(E=0) == -2
+    assert call(n_group=7) == -2                  # does not divide 384
+    assert call(n_group=0) == -2 and call(n_group=96, topk_group=1) == -2
+    assert call(topk_group=9) == -2 and call(topk_group=0) == -2
+    assert call(E=16, n_group=8, topk_group=2, k=5) == -2  # more than the kept groups hold
+    assert call(group_top=3) == -2 and call(group_top=0) == -2
+    assert call(scale=float("inf")) == -2 and call(scale=float("nan")) == -2
+    assert call(logits=None) == -1 and call(ids=None) == -1 and call(w=None) == -1
+    b = lib.moe_router_scores_bwd
+    assert b(FAKE, 3, 4, 384, 6, 1, 1, 1.0, FAKE, FAKE, FAKE, None) == -2
+    assert b(FAKE, 1, 4, 384, 6, 5, 1, 1.0, FAKE, FAKE, FAKE, None) == -2
+    assert b(FAKE, 1, 4, 384, 0, 1, 1, 1.0, FAKE, FAKE, FAKE, None) == -2
+    assert b(FAKE, 1, 4, 384, 6, 1, 1, float("nan"), FAKE, FAKE, FAKE, None) == -2
+    assert b(FAKE, 1, 4, 384, 6, 1, 1, 1.0, FAKE, None, FAKE, None) == -1
+    assert b(FAKE, 1, 4, 384, 6, 1, 1, 1.0, FAKE, FAKE, None, None) == -1
+    r = lib.moe_route_scores
+    ok = [FAKE] * 6
+    assert r(FAKE, 1, 4, 384, 6, None, 1, 7, 1, 2, 1, 1.0, 0, 48, 1, 0, FAKE, FAKE, *ok, FAKE, 4096, None) == -2
+    assert r(FAKE, 1, 4, 384, 6, None, 1, 8, 4, 2, 1, 1.0, 0, 0, 1, 0, FAKE, FAKE, *ok, FAKE, 4096, None) == -2
+    assert r(FAKE, 1, 4, 384, 6, None, 1, 8, 4, 2, 1, 1.0, 0, 48, 1, 0, FAKE, FAKE, *ok, FAKE, 4, None) == -3
+    assert r(None, 1, 4, 384, 6, None, 1, 8, 4, 2, 1, 1.0, 0, 48, 1, 0, FAKE, FAKE, *ok, FAKE, 4096, None) == -1
+
+
+def test_mxfp4_reject_bad_args(lib):
+    q, d = lib.mxfp4_quantize_act, lib.mxfp4_dequantize
+    assert q(FAKE, 0, 4, 48, None, FAKE, FAKE, None) == -2     # cols % 32
+    assert q(FAKE, 0, 4, 0, None, FAKE, FAKE, None) == -2
+    assert q(FAKE, 0, -1, 64, None, FAKE, FAKE, None) == -2
+    assert q(FAKE, 2, 4, 64, None, FAKE, FAKE, None) == -2     # dtype
+    assert q(FAKE, 0, 1 << 40, 64, None, FAKE, FAKE, None) == -2
+    assert q(None, 0, 4, 64, None, FAKE, FAKE, None) == -1
+    assert q(ODD, 0, 4, 64, None, FAKE, FAKE, None) == -6
+    assert q(FAKE, 0, 4, 64, None, ODD, FAKE, None) == -6
+    assert d(FAKE, FAKE, 4, 40, FAKE, None) == -2
+    assert d(FAKE, None, 4, 64, FAKE, None) == -1
+    assert d(FAKE, FAKE, 4, 64, ODD, None) == -6
+    for lin, n in ((lib.mxfp4_linear, 64), (lib.mxfp4_linear_gate_up_silu, 64)):
+        assert lin(FAKE, FAKE, 4, 192, FAKE, FAKE, n, FAKE, None) == -2   # K % 128
+        assert lin(FAKE, FAKE, 4, 0, FAKE, FAKE, n, FAKE, None) == -2
+        assert lin(FAKE, FAKE, 4, 256, FAKE, FAKE, 24, FAKE, None) == -2  # N % 16
+        assert lin(FAKE, FAKE, 4, 256, FAKE, FAKE, 0, FAKE, None) == -2
+        assert lin(FAKE, FAKE, 1 << 31, 256, FAKE, FAKE, n, FAKE, None) == -2
+        assert lin(FAKE, FAKE, -1, 256, FAKE, FAKE, n, FAKE, None) == -2
+        assert lin(FAKE, FAKE, 4, 256, FAKE, None, n, FAKE, None) == -1
+        assert lin(FAKE, FAKE, 4, 256, FAKE, FAKE, n, None, None) == -1
+        assert lin(FAKE, ODD, 4, 256, FAKE, FAKE, n, FAKE, None) == -6
+        assert lin(FAKE, FAKE, 4, 256, FAKE, FAKE, n, ODD, None) == -6
+    l1, l2 = lib.moe_grouped_gemm_l1_silu_mxfp4, lib.moe_grouped_gemm_l2_mxfp4
+    a7, a6 = [FAKE] * 7, [FAKE] * 6
+    assert l1(*a7, 8, 192, 128, 64, 0, FAKE, None) == -2       # H % 128
+    assert l1(*a7, 8, 256, 120, 64, 0, FAKE, None) == -2       # I % 16
+    assert l1(*a7, 0, 256, 128, 64, 0, FAKE, None) == -2 and l1(*a7, 1025, 256, 128, 64, 0, FAKE, None) == -2
+    assert l1(*a7, 8, 256, 128, -1, 0, FAKE, None) == -2 and l1(*a7, 8, 256, 128, 64, -1, FAKE, None) == -2
+    assert l1(*a7, 8, 256, 128, 64, 0, None, None) == -1
+    assert l1(FAKE, FAKE, None, *[FAKE] * 4, 8, 256, 128, 64, 0, FAKE, None) == -1
+    assert l1(*a7, 8, 256, 128, 64, 0, ODD, None) == -6
+    assert l2(*a6, 8, 256, 96, 64, 0, FAKE, None) == -2        # I % 128
+    assert l2(*a6, 8, 248, 128, 64, 0, FAKE, None) == -2
+    assert l2(FAKE, FAKE, FAKE, None, FAKE, FAKE, 8, 256, 128, 64, 0, FAKE, None) == -1
+    assert l2(*a6, 8, 256, 128, 64, 0, None, None) == -1
+
+
+def test_binding_refuses_wrong_tensors():
+    """The binding's own checks come before the library: type, shape, device."""
+    z = torch.zeros(4, 8)
+    ids, w = torch.zeros(4, 2, dtype=torch.int32), torch.zeros(4, 2)
+    with pytest.raises(mm.MegaMoEError, match="GPU"):
+        mm.moe_router_scores(z, 2, ids, w)
+    with pytest.raises(mm.MegaMoEError, match="score"):
+        mm.moe_router_scores(z, 2, ids, w, score="tanh")
+    with pytest.raises(mm.MegaMoEError, match="logits is"):
+        mm.moe_router_scores(z.double(), 2, ids, w)
+    u8 = lambda *s: torch.zeros(*s, dtype=torch.uint8)  # noqa: E731
+    with pytest.raises(mm.MegaMoEError, match="GPU"):
+        mm.mxfp4_quantize_act(z.bfloat16(), u8(4, 4), u8(4, 1))
+    with pytest.raises(mm.MegaMoEError, match="x is"):
+        mm.mxfp4_quantize_act(z.half(), u8(4, 4), u8(4, 1))
+
+
+def test_mx_layer_weight_shapes():
+    w = layer.MXMoEWeights.empty(4, 256, 128, device="cpu")
+    assert (w.num_experts, w.hidden, w.intermediate) == (4, 256, 128)
+    assert w.w13_scales.shape == (4, 256, 8) and w.w2_scales.shape == (4, 256, 4)
+    assert w.nbytes_expert() == 256 * 256 // 2 + 256 * 8 + 256 * 128 // 2 + 256 * 4
