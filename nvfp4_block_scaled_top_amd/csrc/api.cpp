@@ -674,7 +674,7 @@ static int32_t mx_gemm(const MxGemmArgs& a, bool l1, int64_t rows, int32_t max_r
   const int32_t dev = check_device();
   if (dev != MEGAMOE_OK) return dev;
   if (rows == 0) return MEGAMOE_OK;  // no rows: nothing to compute or write
-  return launch_status(launch_mx_gemm(a, l1, static_cast<hipStream_t>(stream)));
+  return launch_status(launch_mx_gemm(a, l1, max_rows_per_expert, static_cast<hipStream_t>(stream)));
 }
 
 int32_t mxfp4_linear(const uint8_t* a_codes, const uint8_t* a_scales, int64_t M, int32_t K, const uint8_t* w_codes,

@@ -158,8 +158,10 @@ struct MxGemmArgs {
   int32_t E, K, N;          // N = output columns (gate+up: weights have 2N rows)
   int64_t M;                // rows of the one group without tables
   void* out;                // bf16 [*, N]
+  bool cover_large = false;  // the tile kernel is not launched: the small kernel takes every expert
 };
-hipError_t launch_mx_gemm(const MxGemmArgs& a, bool l1, hipStream_t stream);
+// max_rows: the caller's bound on an expert's rows, 0 = none.
+hipError_t launch_mx_gemm(const MxGemmArgs& a, bool l1, int64_t max_rows, hipStream_t stream);
 
 // ---- dense layers (one group of M rows) -------------------------------------------------------
 // int32 workspace layout: counts [1], padded offsets [2], tile table [sched_len(1)], then the
