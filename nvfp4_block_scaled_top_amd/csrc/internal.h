@@ -159,6 +159,7 @@ struct MxGemmArgs {
   int64_t M;                // rows of the one group without tables
   void* out;                // bf16 [*, N]
   bool cover_large = false;  // the tile kernel is not launched: the small kernel takes every expert
+  bool cover_small = false;  // the small kernel is not launched: the tile kernel takes every expert
 };
 // max_rows: the caller's bound on an expert's rows, 0 = none.
 hipError_t launch_mx_gemm(const MxGemmArgs& a, bool l1, int64_t max_rows, hipStream_t stream);

@@ -22,14 +22,6 @@ constexpr int kMxDevices = 64;
 
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 
-constexpr int kMxGemmThreads = 256;
-
-__device__ __forceinline__ f32x4 mx_mfma16(u32x4 a, u32x4 b, f32x4 c, uint32_t sa, uint32_t sb) {
-  const i32x8 av{(int)a[0], (int)a[1], (int)a[2], (int)a[3], 0, 0, 0, 0};
-  const i32x8 bv{(int)b[0], (int)b[1], (int)b[2], (int)b[3], 0, 0, 0, 0};
-  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(av, bv, c, 4, 4, 0, (int)sa, 0, (int)sb);
-}
-
 __device__ __forceinline__ f32x16 mx_mfma32_lo(u32x4 a, u32x4 b, f32x16 c, uint32_t sa, uint32_t sb) {
   const i32x8 av{(int)a[0], (int)a[1], (int)a[2], (int)a[3], 0, 0, 0, 0};
   const i32x8 bv{(int)b[0], (int)b[1], (int)b[2], (int)b[3], 0, 0, 0, 0};
@@ -45,60 +37,276 @@ __device__ __forceinline__ float mx_silu(float g) {
   return g * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-g * 1.4426950408889634f));
 }
 
+// Workgroup barrier that no LDS access is moved across.  Vector memory loads stay in flight.
+__device__ __forceinline__ void mx_barrier() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
 // Rows of expert e and their first row; without tables there is one group of all p.M rows.
 __device__ __forceinline__ int mx_count(const MxGemmArgs& p, int e) { return p.counts ? p.counts[e] : (int)p.M; }
 
 // ============================================================================================
-// Experts (or a dense call) of at most kMxSmallRows rows.
+// Experts (or a dense call) of at most kMxSmallRows rows: the weights' bytes are the work.
+//
+// Work unit: a group, 16 weight rows over the whole of K for one m-tile; the groups of all m-tiles
+// are laid end to end and every workgroup takes an equal range (one workgroup of 4 waves a CU).
+// The 4 waves split K; each streams its part of the weight rows through an LDS ring of its own, 16 rows
+// x 512 elements (256 bytes a row, 16 scale bytes) a slot, by direct global -> LDS loads: no barrier, no
+// registers, and some 70 KB in flight a CU.  A slot is requested again as soon as its operands are in
+// registers.  The ring runs on across groups and m-tiles.
+//
+// The token rows' part of K stays in LDS while the groups of their m-tile pass.  Both operands keep
+// 16-byte piece c of row R (one MXFP4 block) at slot c ^ R of the row's 256 bytes, so that 16 rows are
+// read without bank conflicts.  Lane (r, g) takes blocks 4g .. 4g+3 of its row, one an MFMA step: its
+// four scale bytes are one word, and the instruction picks the byte.
+//
+// At the end of a group the waves leave their partial sums in LDS (two buffers, by the group's parity) and
+// one of them adds the four in wave order and stores.
 // ============================================================================================
 constexpr int kMxSmallRows = 16;
+constexpr int kMxSplit = 4;                        // waves, K split
+constexpr int kMxChunk = 512;                      // K elements of a slot
+constexpr int kMxSlotCodes = 16 * kMxChunk / 2;
+constexpr int kMxSlot = kMxSlotCodes + 16 * kMxChunk / 32;
+constexpr int kMxMaxSlots = 8;
+constexpr int kMxLds = 160 * 1024;
+constexpr int kMxRed = 2 * kMxSplit * kWave * 16;
+constexpr int kMxGrid = 256;                       // one workgroup a CU
+
+// Waits until at most `after` (<= K) later slots' loads are outstanding for this wave.
+template <int K>
+__device__ __forceinline__ void mx_wait_slots(int after) {
+  if constexpr (K > 0) {
+    if (after < K) {
+      mx_wait_slots<K - 1>(after);
+      return;
+    }
+  }
+  wait_vmcnt<5 * K>();
+}
+
+template <int S>
+__device__ __forceinline__ f32x4 mx_mfma16(u32x4 a, u32x4 b, f32x4 c, uint32_t sa, uint32_t sb) {
+  const i32x8 av{(int)a[0], (int)a[1], (int)a[2], (int)a[3], 0, 0, 0, 0};
+  const i32x8 bv{(int)b[0], (int)b[1], (int)b[2], (int)b[3], 0, 0, 0, 0};
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(av, bv, c, 4, 4, S, (int)sa, S, (int)sb);
+}
+
+// A place in the list of groups: expert e of cnt rows, m-tile mt of it, 16-row weight block j.
+struct MxPlace {
+  int e, cnt, mt, j;
+};
+
+__device__ __forceinline__ int mx_small_tiles(const MxGemmArgs& p, int cnt, int mrows) {
+  return cnt <= kMxSmallRows || p.cover_large ? (cnt + mrows - 1) / mrows : 0;
+}
+
+// The first m-tile of an expert from e0 on that has any; p.E if none.
+__device__ __forceinline__ void mx_seek(const MxGemmArgs& p, int e0, int mrows, MxPlace& at) {
+  at.e = p.E;
+  at.mt = 0;
+  for (int c = e0; c < p.E && at.e == p.E; c += kWave) {
+    const int cnt = c + lane_id() < p.E ? mx_count(p, c + lane_id()) : 0;
+    const uint64_t any = __ballot(mx_small_tiles(p, cnt, mrows) > 0);
+    if (any) {
+      const int l = __ffsll((unsigned long long)any) - 1;
+      at.e = c + l;
+      at.cnt = __builtin_amdgcn_readlane(cnt, l);
+    }
+  }
+}
 
 template <bool kL1>
-__global__ __launch_bounds__(kMxGemmThreads) void mx_small_kernel(MxGemmArgs p) {
+__global__ __launch_bounds__(kMxSplit* kWave, 1) void mx_small_kernel(MxGemmArgs p, int slots, int mrows) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t s_mx[];
   const int lane = lane_id(), r = lane & 15, g = lane >> 4;
-  const int K = p.K, Kh = K / 2, Ks = K / 32;
-  const int unit = kL1 ? 8 : 16;  // output columns of a 16-row weight block
-  const int nt = (p.N + unit - 1) / unit;
-  const int wave = (int)(blockIdx.x * (kMxGemmThreads / kWave)) + (int)(threadIdx.x / kWave);
-  const int nwaves = (int)gridDim.x * (kMxGemmThreads / kWave);
-  const int64_t Nw = kL1 ? 2 * (int64_t)p.N : p.N;
-  int64_t t0 = 0;  // tiles of the experts before e
-  for (int e = 0; e < p.E; ++e) {
-    const int cnt = mx_count(p, e);
-    if (cnt > kMxSmallRows && !p.cover_large) continue;  // the tile kernel's
-    const int64_t tiles = (int64_t)((cnt + 15) / 16) * nt;
-    int64_t t = (wave - t0 % nwaves + nwaves) % nwaves;  // first tile of e that this wave takes
-    for (; t < tiles; t += nwaves) {
-      const int mt = (int)(t / nt), j = (int)(t % nt);
-      const int left = cnt - 16 * mt;
-      const int64_t row0 = (p.padded_offsets ? p.padded_offsets[e] : 0) + 16 * (int64_t)mt;
-      // A lane outside the tile reads a valid row of it instead; what it feeds is not stored.
-      const int64_t tr = row0 + (r < left ? r : 0);
-      const int64_t ar = p.row_token ? p.row_token[tr] : tr;
-      int col = j * unit + (kL1 ? (r >> 2) * 2 + (r & 1) : r);  // weight row of lane row r
-      if (col >= p.N) col = p.N - 1;
-      const int64_t wr = e * Nw + (kL1 && (r & 2) ? p.N + col : col);
-      const uint8_t* a = p.a_codes + ar * Kh + 16 * g;
-      const uint8_t* as = p.a_scales + ar * Ks + g;
-      const uint8_t* w = p.w_codes + wr * Kh + 16 * g;
-      const uint8_t* ws = p.w_scales + wr * Ks + g;
-      f32x4 c{0.f, 0.f, 0.f, 0.f};
-      for (int k = 0; k < K / 128; ++k)
-        c = mx_mfma16(*reinterpret_cast<const u32x4*>(w + 64 * k), *reinterpret_cast<const u32x4*>(a + 64 * k), c,
-                      ws[4 * k], as[4 * k]);
-      // lane: token row r of the tile, weight rows 4g .. 4g+3
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int nch = (p.K + kMxChunk - 1) / kMxChunk, nblk = p.K / 32;
+  const int64_t Kh = p.K / 2, Ks = p.K / 32;
+  const int a_chunk = mrows * (kMxChunk / 2 + kMxChunk / 32);  // LDS bytes of a chunk of the token rows
+  uint8_t* const s_a = s_mx;
+  f32x4* const s_red = reinterpret_cast<f32x4*>(s_mx + nch * a_chunk);
+  uint8_t* const s_ring = s_mx + nch * a_chunk + kMxRed + wave * slots * kMxSlot;
+  const int c0 = wave * nch / kMxSplit, c1 = (wave + 1) * nch / kMxSplit;  // this wave's chunks
+  constexpr int unit = kL1 ? 8 : 16;  // output columns of a group
+  const int nt = p.N / unit;
+
+  // This workgroup's groups [gb, ge); XCD b % 8 takes one contiguous eighth.
+  int64_t tiles = 0;
+  if (p.counts == nullptr) {
+    tiles = (p.M + mrows - 1) / mrows;
+  } else {
+    int mine = 0;
+    for (int e = lane; e < p.E; e += kWave) mine += mx_small_tiles(p, p.counts[e], mrows);
+    tiles = wave_sum_i32(mine);
+  }
+  const int64_t groups = tiles * nt;
+  const int64_t part = (blockIdx.x % 8) * (kMxGrid / 8) + blockIdx.x / 8;
+  const int64_t gb = part * groups / kMxGrid, ge = (part + 1) * groups / kMxGrid;
+  if (gb >= ge) return;  // the whole workgroup
+
+  MxPlace cur;  // of the group that is computed
+  {
+    int64_t m = gb / nt;
+    cur.j = (int)(gb % nt);
+    if (p.counts == nullptr) {
+      cur.e = 0;
+      cur.cnt = (int)p.M;
+      cur.mt = (int)m;
+    } else {
+      for (mx_seek(p, 0, mrows, cur);; mx_seek(p, cur.e + 1, mrows, cur)) {
+        const int n = mx_small_tiles(p, cur.cnt, mrows);
+        if (m < n || cur.e >= p.E) break;
+        m -= n;
+      }
+      cur.mt = (int)m;
+    }
+  }
+  const auto next = [&](MxPlace& at) {
+    if (++at.j < nt) return;
+    at.j = 0;
+    if ((at.mt + 1) * mrows < at.cnt) {
+      ++at.mt;
+    } else {
+      mx_seek(p, at.e + 1, mrows, at);
+    }
+  };
+
+  // ---- the weight stream -------------------------------------------------------------------------
+  MxPlace ld = cur;
+  int ld_c = c0, ld_slot = 0;
+  int64_t ld_left = (ge - gb) * (c1 - c0);  // slots still to be requested
+  const uint8_t *w_src, *ws_src;
+  // Loads of 4 rows a 1 KB: lane l brings a piece of row 4q + l / 16, whose LDS place is l % 16.
+  const auto row_of = [&](int R) -> int64_t {  // weight row of row R of the group
+    if constexpr (kL1) return ((int64_t)ld.e * 2 + ((R >> 1) & 1)) * p.N + ld.j * 8 + (R >> 2) * 2 + (R & 1);
+    else return (int64_t)ld.e * p.N + ld.j * 16 + R;
+  };
+  const auto set_src = [&]() {
+    w_src = p.w_codes + row_of(lane >> 4) * Kh;
+    ws_src = p.w_scales + row_of(lane >> 2) * Ks;
+  };
+  const int64_t quad = (kL1 ? 2 : 4) * Kh;  // from row R to row R + 4 of the group
+  const auto request = [&]() {
+    const uint32_t base = lds_addr(s_ring + ld_slot * kMxSlot);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      // a piece beyond K (in the last chunk): the chunk's first instead; the compute skips it
+      const int piece = (lane & 15) ^ (4 * q + (lane >> 4));
+      const int b = ld_c * 16 + (ld_c * 16 + piece < nblk ? piece : 0);
+      dma16nt(w_src + q * quad + 16 * b, base + 1024 * q);
+    }
+    const int b4 = ld_c * 4 + (ld_c * 4 + (lane & 3) < nblk / 4 ? lane & 3 : 0);
+    dma4(ws_src + 4 * b4, base + kMxSlotCodes);
+    ld_slot = ld_slot + 1 == slots ? 0 : ld_slot + 1;
+    --ld_left;
+    if (++ld_c == c1) {
+      ld_c = c0;
+      if (ld_left > 0) {
+        next(ld);
+        set_src();
+      }
+    }
+  };
+
+  // This wave's chunks of the m-tile's rows into LDS (rows past the last are left as they are: a row
+  // is one column of the product, and theirs are not stored).
+  const auto load_rows = [&](const MxPlace& at, int64_t row0, int left) {
+    const auto src_row = [&](int R) -> int64_t {
+      const int64_t t = row0 + (R < left ? R : 0);
+      return p.row_token ? p.row_token[t] : t;
+    };
+    const uint8_t* a[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) a[q] = 4 * q < left ? p.a_codes + src_row(4 * q + (lane >> 4)) * Kh : p.a_codes;
+    const uint8_t* as = p.a_scales + src_row(lane >> 2) * Ks;
+    for (int c = c0; c < c1; ++c) {
+      const uint32_t base = lds_addr(s_a + c * a_chunk);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        if (4 * q >= left) continue;
+        const int piece = (lane & 15) ^ (4 * q + (lane >> 4));
+        dma16(a[q] + 16 * (c * 16 + (c * 16 + piece < nblk ? piece : 0)), base + 1024 * q);
+      }
+      const int b4 = c * 4 + (c * 4 + (lane & 3) < nblk / 4 ? lane & 3 : 0);
+      if ((lane >> 2) < mrows) dma4(as + 4 * b4, base + mrows * (kMxChunk / 2));
+    }
+  };
+
+  int64_t row0 = 0;
+  int left = 0;
+  const auto enter = [&]() {  // the rows of cur's m-tile
+    row0 = (p.padded_offsets ? p.padded_offsets[cur.e] : 0) + (int64_t)cur.mt * mrows;
+    left = min(cur.cnt - cur.mt * mrows, mrows);
+    load_rows(cur, row0, left);
+  };
+  enter();
+  set_src();
+  for (int i = 0; i < slots && ld_left > 0; ++i) request();
+
+  int slot = 0;
+  const int rl = r & (mrows - 1);
+  for (int64_t gi = gb; gi < ge; ++gi) {
+    f32x4 acc{0.f, 0.f, 0.f, 0.f};
+    for (int c = c0; c < c1; ++c) {
+      const int64_t ahead = (ge - gi) * (c1 - c0) - (c - c0) - 1 - ld_left;  // slots requested after this one
+      mx_wait_slots<kMxMaxSlots - 1>((int)ahead);
+      asm volatile("" ::: "memory");
+      const uint8_t* w = s_ring + slot * kMxSlot;
+      const uint8_t* a = s_a + c * a_chunk;
+      u32x4 wv[4], av[4];
+#pragma unroll
+      for (int st = 0; st < 4; ++st) {
+        wv[st] = *reinterpret_cast<const u32x4*>(w + r * 256 + 16 * ((4 * g + st) ^ r));
+        av[st] = *reinterpret_cast<const u32x4*>(a + rl * 256 + 16 * ((4 * g + st) ^ rl));
+      }
+      uint32_t wsc = *reinterpret_cast<const uint32_t*>(w + kMxSlotCodes + r * 16 + 4 * g);
+      uint32_t asc = *reinterpret_cast<const uint32_t*>(a + mrows * (kMxChunk / 2) + rl * 16 + 4 * g);
+      __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): the slot's operands are in registers
+      asm volatile("" ::: "memory");
+      slot = slot + 1 == slots ? 0 : slot + 1;
+      if (ld_left > 0) request();
+      if (c * 4 + 4 > nblk / 4 && c * 4 + g >= nblk / 4) {  // beyond K
+        wsc = asc = 0x7F7F7F7Fu;
+#pragma unroll
+        for (int st = 0; st < 4; ++st) av[st] = u32x4{0u, 0u, 0u, 0u};
+      }
+      acc = mx_mfma16<0>(wv[0], av[0], acc, wsc, asc);
+      acc = mx_mfma16<1>(wv[1], av[1], acc, wsc, asc);
+      acc = mx_mfma16<2>(wv[2], av[2], acc, wsc, asc);
+      acc = mx_mfma16<3>(wv[3], av[3], acc, wsc, asc);
+    }
+    f32x4* const red = s_red + (gi & 1) * kMxSplit * kWave;
+    red[wave * kWave + lane] = acc;
+    __builtin_amdgcn_s_waitcnt(0xC07F);  // the partial sums are written; weight loads stay in flight
+    mx_barrier();
+    if (wave == (int)(gi % kMxSplit)) {
+      f32x4 z = red[lane];
+#pragma unroll
+      for (int k = 1; k < kMxSplit; ++k) z += red[k * kWave + lane];
+      // lane: token row r of the m-tile, weight rows 4g .. 4g+3
       if (r < left) {
         uint16_t* out = static_cast<uint16_t*>(p.out) + (row0 + r) * (int64_t)p.N;
         if constexpr (kL1) {
-          for (int i = 0; i < 2; ++i)
-            if (j * 8 + 2 * g + i < p.N) out[j * 8 + 2 * g + i] = (uint16_t)f32_to_bf16_any(mx_silu(c[i]) * c[i + 2]);
+          *reinterpret_cast<uint32_t*>(out + cur.j * 8 + 2 * g) =
+              f32_to_bf16_any(mx_silu(z[0]) * z[2]) | f32_to_bf16_any(mx_silu(z[1]) * z[3]) << 16;
         } else {
-          for (int i = 0; i < 4; ++i)
-            if (j * 16 + 4 * g + i < p.N) out[j * 16 + 4 * g + i] = (uint16_t)f32_to_bf16_any(c[i]);
+          *reinterpret_cast<u32x2*>(out + cur.j * 16 + 4 * g) =
+              u32x2{f32_to_bf16_any(z[0]) | f32_to_bf16_any(z[1]) << 16,
+                    f32_to_bf16_any(z[2]) | f32_to_bf16_any(z[3]) << 16};
         }
       }
     }
-    t0 += tiles;
+    if (gi + 1 < ge) {
+      const int e = cur.e, mt = cur.mt;
+      next(cur);
+      if (cur.e != e || cur.mt != mt) {
+        enter();
+        wait_vmcnt<0>();  // the new rows, and with them every weight slot requested so far
+      }
+    }
   }
 }
 
@@ -122,7 +330,6 @@ __global__ __launch_bounds__(kMxGemmThreads) void mx_small_kernel(MxGemmArgs p) 
 // columns, so both meet in one lane.
 // ============================================================================================
 constexpr int kMxWaves = 8, kMxThreads = kMxWaves * kWave;
-constexpr int kMxGrid = 256;   // one workgroup a CU
 constexpr int kMxBn = 256;     // weight rows of a tile
 constexpr int kMxBm = 256;     // token rows of a full tile
 constexpr int kMxSlots = 4, kMxAhead = kMxSlots - 1;
@@ -141,7 +348,7 @@ struct MxShape {
   static constexpr int kStage = kAScales + BM * 4;
 };
 constexpr int kMxRing = kMxSlots * MxShape<kMxBm>::kStage;
-static_assert(kMxRing + 4 * (MEGAMOE_MAX_EXPERTS + 1) <= 160 * 1024, "the ring and the tables fit");
+static_assert(kMxRing + 4 * (MEGAMOE_MAX_EXPERTS + 1) <= kMxLds, "the ring and the tables fit");
 
 // Waits for this wave's loads but those of the last `after` stages, and for its LDS reads.
 template <class S, int K>
@@ -155,13 +362,6 @@ __device__ __forceinline__ void mx_wait_stages(int after) {
     }
   }
   __builtin_amdgcn_s_waitcnt((n & 15) | ((n >> 4) << 14) | (0x7 << 4));  // vmcnt(n) lgkmcnt(0)
-}
-
-// Workgroup barrier that no LDS access is moved across.  Vector memory loads stay in flight.
-__device__ __forceinline__ void mx_barrier() {
-  asm volatile("" ::: "memory");
-  __builtin_amdgcn_s_barrier();
-  asm volatile("" ::: "memory");
 }
 
 template <bool kL1, int BM>
@@ -315,7 +515,7 @@ __global__ __launch_bounds__(kMxThreads, 1) void mx_tile_kernel(MxGemmArgs p) {
     int carry = 0;
     for (int c = 0; c < E; c += kWave) {
       const int cnt = c + lane < E ? mx_count(p, c + lane) : 0;
-      int incl = cnt > kMxSmallRows ? (cnt + kMxBm - 1) / kMxBm : 0;
+      int incl = cnt > kMxSmallRows || p.cover_small ? (cnt + kMxBm - 1) / kMxBm : 0;
       const int own = incl;
 #pragma unroll
       for (int o = 1; o < kWave; o <<= 1) {
@@ -351,40 +551,72 @@ __global__ __launch_bounds__(kMxThreads, 1) void mx_tile_kernel(MxGemmArgs p) {
   }
 }
 
+// The dynamic LDS limit of a kernel, raised once a device.
+template <typename F>
+static hipError_t mx_allow_lds(F* kernel, std::atomic<bool> (&done)[kMxDevices]) {
+  int dev = 0;
+  hipError_t err = hipGetDevice(&dev);
+  if (err != hipSuccess) return err;
+  if (dev < kMxDevices && done[dev].load(std::memory_order_acquire)) return hipSuccess;
+  err = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, kMxLds);
+  if (err == hipSuccess && dev < kMxDevices) done[dev].store(true, std::memory_order_release);
+  return err;
+}
+
+// Token rows of the small kernel's m-tiles and its ring slots for this K: 16 rows, or 8 or 4 where 16 (or
+// 8) rows of K elements would leave fewer than 4 slots.  0 slots: K is too long for the small kernel.
+struct MxSmallPlan {
+  int mrows, slots;
+  size_t lds;
+};
+static MxSmallPlan mx_small_plan(int K) {
+  const int64_t nch = (K + kMxChunk - 1) / kMxChunk;
+  for (int mrows = kMxSmallRows; mrows >= 4; mrows /= 2) {
+    const int64_t fixed = nch * mrows * (kMxChunk / 2 + kMxChunk / 32) + kMxRed;
+    int64_t slots = (kMxLds - fixed) / (kMxSplit * kMxSlot);
+    if (slots > kMxMaxSlots) slots = kMxMaxSlots;
+    if (fixed < kMxLds && slots >= 4) return {mrows, (int)slots, (size_t)(fixed + kMxSplit * slots * kMxSlot)};
+  }
+  return {0, 0, 0};
+}
+
 template <bool kL1>
-static hipError_t launch_mx(const MxGemmArgs& a, bool small, bool large, hipStream_t stream) {
+static hipError_t launch_mx(const MxGemmArgs& a, const MxSmallPlan& plan, bool small, bool large, hipStream_t stream) {
+  static std::atomic<bool> small_done[kMxDevices], tile_done[kMxDevices];
+  hipError_t err = hipSuccess;
   if (small) {
-    hipLaunchKernelGGL(mx_small_kernel<kL1>, dim3(2048), dim3(kMxGemmThreads), 0, stream, a);
-    const hipError_t err = hipGetLastError();
+    err = mx_allow_lds(mx_small_kernel<kL1>, small_done);
+    if (err != hipSuccess) return err;
+    hipLaunchKernelGGL(mx_small_kernel<kL1>, dim3(kMxGrid), dim3(kMxSplit * kWave), plan.lds, stream, a, plan.slots,
+                       plan.mrows);
+    err = hipGetLastError();
     if (err != hipSuccess) return err;
   }
   if (large) {
-    const size_t lds = kMxRing + sizeof(int) * ((size_t)a.E + 1);
-    static std::atomic<bool> set[2][kMxDevices];  // the kernel's dynamic LDS limit, raised once a device
-    int dev = 0;
-    hipError_t err = hipGetDevice(&dev);
+    err = mx_allow_lds(mx_tile_kernel<kL1>, tile_done);
     if (err != hipSuccess) return err;
-    if (dev >= kMxDevices || !set[kL1][dev].load(std::memory_order_acquire)) {
-      err = hipFuncSetAttribute(reinterpret_cast<const void*>(mx_tile_kernel<kL1>),
-                                hipFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
-      if (err != hipSuccess) return err;
-      if (dev < kMxDevices) set[kL1][dev].store(true, std::memory_order_release);
-    }
-    hipLaunchKernelGGL(mx_tile_kernel<kL1>, dim3(kMxGrid), dim3(kMxThreads), lds, stream, a);
-    return hipGetLastError();
+    hipLaunchKernelGGL(mx_tile_kernel<kL1>, dim3(kMxGrid), dim3(kMxThreads),
+                       kMxRing + sizeof(int) * ((size_t)a.E + 1), stream, a);
+    err = hipGetLastError();
   }
-  return hipSuccess;
+  return err;
 }
 
 hipError_t launch_mx_gemm(const MxGemmArgs& a0, bool l1, int64_t max_rows, hipStream_t stream) {
   MxGemmArgs a = a0;
+  const MxSmallPlan plan = mx_small_plan(a.K);
   // A dense call knows its rows.  A grouped one launches both kernels unless the caller's bound says
   // that no expert has more than the small kernel's rows; it then covers every expert, should the
-  // bound be wrong.
-  const bool small = a.counts != nullptr || a.M <= kMxSmallRows;
-  const bool large = a.counts != nullptr ? !(max_rows > 0 && max_rows <= kMxSmallRows) : a.M > kMxSmallRows;
+  // bound be wrong.  With a K beyond the small kernel's the tile kernel takes everything.
+  bool small = a.counts != nullptr || a.M <= kMxSmallRows;
+  bool large = a.counts != nullptr ? !(max_rows > 0 && max_rows <= kMxSmallRows) : a.M > kMxSmallRows;
+  if (plan.slots == 0) {
+    small = false;
+    large = true;
+  }
   a.cover_large = !large;
-  return l1 ? launch_mx<true>(a, small, large, stream) : launch_mx<false>(a, small, large, stream);
+  a.cover_small = !small;
+  return l1 ? launch_mx<true>(a, plan, small, large, stream) : launch_mx<false>(a, plan, small, large, stream);
 }
 
 }  // namespace megamoe

@@ -363,20 +363,32 @@ def nvfp4_linear_gate_up_silu_nvfp4(a_codes, a_scales, a_gs, w13_codes, w13_scal
 
 # ---- scored router -----------------------------------------------------------------------------
 
-def _arg(name: str, t: torch.Tensor, dtypes, shape) -> int:
+# The checks below run on every call, beside kernels of a few microseconds: one device query and one raw
+# stream query a call, and five cheap tests a tensor (8.5 us a call instead of 10.5 for the router).
+
+def _arg(name: str, t: torch.Tensor, dtypes, shape, dev: int) -> int:
     """Device pointer of a tensor that must have one of these types and this shape, be contiguous and
-    lie on the current device (the one the kernels are launched on)."""
+    lie on device `dev`, the current one (the one the kernels are launched on)."""
+    if t.dtype in dtypes and t.shape == shape and t.get_device() == dev and dev >= 0 and t.is_contiguous():
+        return t.data_ptr()
     if t.dtype not in dtypes:
         raise MegaMoEError(f"{name} is {t.dtype}, expected one of {list(dtypes)}")
     if t.shape != shape:
         raise MegaMoEError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     if not t.is_cuda:
         raise MegaMoEError("tensors passed to libmegamoe must be on the GPU")
-    if t.get_device() != torch.cuda.current_device():
+    if t.get_device() != dev:
         raise MegaMoEError(f"{name} is on another device than the current one")
-    if not t.is_contiguous():
-        raise MegaMoEError("tensors passed to libmegamoe must be contiguous")
-    return t.data_ptr()
+    raise MegaMoEError("tensors passed to libmegamoe must be contiguous")
+
+
+def _on(t: torch.Tensor, stream):
+    """Current device and raw stream for a call on t's device (-1 and no stream if t is not on a GPU:
+    _arg then refuses it)."""
+    if not t.is_cuda:
+        return -1, None
+    dev = torch.cuda.current_device()
+    return dev, torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
 _U8 = (torch.uint8,)
@@ -385,12 +397,12 @@ _F32 = (torch.float32,)
 _BF16 = (torch.bfloat16, torch.int16)
 
 
-def _score_args(logits, k, bias, score, n_group, topk_group, group_top, renormalize, scale):
+def _score_args(logits, k, bias, score, n_group, topk_group, group_top, renormalize, scale, dev):
     T, Eg = logits.shape
     if score not in SCORES:
         raise MegaMoEError(f"score is {score!r}, expected one of {list(SCORES)}")
-    return (_arg("logits", logits, DTYPES, (T, Eg)), DTYPES[logits.dtype], T, Eg, k,
-            None if bias is None else _arg("bias", bias, _F32, (Eg,)), SCORES[score], n_group, topk_group, group_top,
+    return (_arg("logits", logits, DTYPES, (T, Eg), dev), DTYPES[logits.dtype], T, Eg, k,
+            None if bias is None else _arg("bias", bias, _F32, (Eg,), dev), SCORES[score], n_group, topk_group, group_top,
             int(renormalize), scale)
 
 
@@ -399,9 +411,10 @@ def moe_router_scores(logits, k, topk_ids, topk_weights, bias=None, score="sigmo
     """Top-k ids and weights by sigmoid or softmax scores, with a balance bias, expert groups and
     renormalised weights.  logits [T, E] float32 or bf16."""
     T = logits.shape[0]
+    dev, st = _on(logits, stream)
     _check("moe_router_scores", lib().moe_router_scores(
-        *_score_args(logits, k, bias, score, n_group, topk_group, group_top, renormalize, scale),
-        _arg("topk_ids", topk_ids, _INT, (T, k)), _arg("topk_weights", topk_weights, _F32, (T, k)), _stream(stream)))
+        *_score_args(logits, k, bias, score, n_group, topk_group, group_top, renormalize, scale, dev),
+        _arg("topk_ids", topk_ids, _INT, (T, k), dev), _arg("topk_weights", topk_weights, _F32, (T, k), dev), st))
 
 
 def moe_route_scores(logits, k, expert_begin, num_experts, pad_multiple, topk_ids, topk_weights, counts,
@@ -410,11 +423,12 @@ def moe_route_scores(logits, k, expert_begin, num_experts, pad_multiple, topk_id
                      block_m_override=0, stream=None):
     """moe_router_scores, then moe_route_permute on its ids."""
     T = logits.shape[0]
+    dev, st = _on(logits, stream)
     _check("moe_route_scores", lib().moe_route_scores(
-        *_score_args(logits, k, bias, score, n_group, topk_group, group_top, renormalize, scale), expert_begin,
-        num_experts, pad_multiple, block_m_override, _arg("topk_ids", topk_ids, _INT, (T, k)),
-        _arg("topk_weights", topk_weights, _F32, (T, k)), _ptr(counts), _ptr(expert_offsets), _ptr(padded_offsets),
-        _ptr(row_token), _ptr(token_rows), _ptr(sched), _ptr(workspace), _nbytes(workspace), _stream(stream)))
+        *_score_args(logits, k, bias, score, n_group, topk_group, group_top, renormalize, scale, dev), expert_begin,
+        num_experts, pad_multiple, block_m_override, _arg("topk_ids", topk_ids, _INT, (T, k), dev),
+        _arg("topk_weights", topk_weights, _F32, (T, k), dev), _ptr(counts), _ptr(expert_offsets), _ptr(padded_offsets),
+        _ptr(row_token), _ptr(token_rows), _ptr(sched), _ptr(workspace), _nbytes(workspace), st))
 
 
 def moe_router_scores_bwd(logits, topk_ids, grad_weights, grad_logits, score="sigmoid", renormalize=True, scale=1.0,
@@ -424,10 +438,11 @@ def moe_router_scores_bwd(logits, topk_ids, grad_weights, grad_logits, score="si
     k = topk_ids.shape[1]
     if score not in SCORES:
         raise MegaMoEError(f"score is {score!r}, expected one of {list(SCORES)}")
+    dev, st = _on(logits, stream)
     _check("moe_router_scores_bwd", lib().moe_router_scores_bwd(
-        _arg("logits", logits, DTYPES, (T, Eg)), DTYPES[logits.dtype], T, Eg, k, SCORES[score], int(renormalize),
-        scale, _arg("topk_ids", topk_ids, _INT, (T, k)), _arg("grad_weights", grad_weights, _F32, (T, k)),
-        _arg("grad_logits", grad_logits, (logits.dtype,), (T, Eg)), _stream(stream)))
+        _arg("logits", logits, DTYPES, (T, Eg), dev), DTYPES[logits.dtype], T, Eg, k, SCORES[score], int(renormalize),
+        scale, _arg("topk_ids", topk_ids, _INT, (T, k), dev), _arg("grad_weights", grad_weights, _F32, (T, k), dev),
+        _arg("grad_logits", grad_logits, (logits.dtype,), (T, Eg), dev), st))
 
 
 # ---- MXFP4 -------------------------------------------------------------------------------------
@@ -435,36 +450,40 @@ def moe_router_scores_bwd(logits, topk_ids, grad_weights, grad_logits, score="si
 def mxfp4_quantize_act(x, codes, scales, row_valid=None, stream=None):
     """x [rows, cols] bf16 (also viewed as int16) or float32 -> codes [rows, cols/2], scales [rows, cols/32]."""
     rows, cols = x.shape
+    dev, st = _on(x, stream)
     _check("mxfp4_quantize_act", lib().mxfp4_quantize_act(
-        _arg("x", x, DTYPES, (rows, cols)), DTYPES[x.dtype], rows, cols,
-        None if row_valid is None else _arg("row_valid", row_valid, _INT, (rows,)),
-        _arg("codes", codes, _U8, (rows, cols // 2)), _arg("scales", scales, _U8, (rows, cols // 32)),
-        _stream(stream)))
+        _arg("x", x, DTYPES, (rows, cols), dev), DTYPES[x.dtype], rows, cols,
+        None if row_valid is None else _arg("row_valid", row_valid, _INT, (rows,), dev),
+        _arg("codes", codes, _U8, (rows, cols // 2), dev), _arg("scales", scales, _U8, (rows, cols // 32), dev),
+        st))
 
 
 def mxfp4_dequantize(codes, scales, out_bf16, stream=None):
     rows, cols = out_bf16.shape
+    dev, st = _on(codes, stream)
     _check("mxfp4_dequantize", lib().mxfp4_dequantize(
-        _arg("codes", codes, _U8, (rows, cols // 2)), _arg("scales", scales, _U8, (rows, cols // 32)), rows, cols,
-        _arg("out_bf16", out_bf16, _BF16, (rows, cols)), _stream(stream)))
+        _arg("codes", codes, _U8, (rows, cols // 2), dev), _arg("scales", scales, _U8, (rows, cols // 32), dev), rows, cols,
+        _arg("out_bf16", out_bf16, _BF16, (rows, cols), dev), st))
 
 
 def mxfp4_linear(a_codes, a_scales, w_codes, w_scales, out_bf16, stream=None):
     M, Kh = a_codes.shape
     N = w_codes.shape[0]
+    dev, st = _on(a_codes, stream)
     _check("mxfp4_linear", lib().mxfp4_linear(
-        _arg("a_codes", a_codes, _U8, (M, Kh)), _arg("a_scales", a_scales, _U8, (M, Kh // 16)), M, 2 * Kh,
-        _arg("w_codes", w_codes, _U8, (N, Kh)), _arg("w_scales", w_scales, _U8, (N, Kh // 16)), N,
-        _arg("out_bf16", out_bf16, _BF16, (M, N)), _stream(stream)))
+        _arg("a_codes", a_codes, _U8, (M, Kh), dev), _arg("a_scales", a_scales, _U8, (M, Kh // 16), dev), M, 2 * Kh,
+        _arg("w_codes", w_codes, _U8, (N, Kh), dev), _arg("w_scales", w_scales, _U8, (N, Kh // 16), dev), N,
+        _arg("out_bf16", out_bf16, _BF16, (M, N), dev), st))
 
 
 def mxfp4_linear_gate_up_silu(a_codes, a_scales, w13_codes, w13_scales, h_bf16, stream=None):
     M, Kh = a_codes.shape
     I = h_bf16.shape[1]
+    dev, st = _on(a_codes, stream)
     _check("mxfp4_linear_gate_up_silu", lib().mxfp4_linear_gate_up_silu(
-        _arg("a_codes", a_codes, _U8, (M, Kh)), _arg("a_scales", a_scales, _U8, (M, Kh // 16)), M, 2 * Kh,
-        _arg("w13_codes", w13_codes, _U8, (2 * I, Kh)), _arg("w13_scales", w13_scales, _U8, (2 * I, Kh // 16)), I,
-        _arg("h_bf16", h_bf16, _BF16, (M, I)), _stream(stream)))
+        _arg("a_codes", a_codes, _U8, (M, Kh), dev), _arg("a_scales", a_scales, _U8, (M, Kh // 16), dev), M, 2 * Kh,
+        _arg("w13_codes", w13_codes, _U8, (2 * I, Kh), dev), _arg("w13_scales", w13_scales, _U8, (2 * I, Kh // 16), dev), I,
+        _arg("h_bf16", h_bf16, _BF16, (M, I), dev), st))
 
 
 def moe_grouped_gemm_l1_silu_mxfp4(x_codes, x_scales, row_token, padded_offsets, counts, w13_codes, w13_scales,
@@ -474,20 +493,22 @@ def moe_grouped_gemm_l1_silu_mxfp4(x_codes, x_scales, row_token, padded_offsets,
     T, Hh = x_codes.shape
     E, I2, _ = w13_codes.shape
     M_cap, I = h_bf16.shape
+    dev, st = _on(x_codes, stream)
     _check("moe_grouped_gemm_l1_silu_mxfp4", lib().moe_grouped_gemm_l1_silu_mxfp4(
-        _arg("x_codes", x_codes, _U8, (T, Hh)), _arg("x_scales", x_scales, _U8, (T, Hh // 16)),
-        _arg("row_token", row_token, _INT, (M_cap,)), _arg("padded_offsets", padded_offsets, _INT, (E + 1,)),
-        _arg("counts", counts, _INT, (E,)), _arg("w13_codes", w13_codes, _U8, (E, 2 * I, Hh)),
-        _arg("w13_scales", w13_scales, _U8, (E, 2 * I, Hh // 16)), E, 2 * Hh, I, M_cap, max_rows_per_expert,
-        _arg("h_bf16", h_bf16, _BF16, (M_cap, I)), _stream(stream)))
+        _arg("x_codes", x_codes, _U8, (T, Hh), dev), _arg("x_scales", x_scales, _U8, (T, Hh // 16), dev),
+        _arg("row_token", row_token, _INT, (M_cap,), dev), _arg("padded_offsets", padded_offsets, _INT, (E + 1,), dev),
+        _arg("counts", counts, _INT, (E,), dev), _arg("w13_codes", w13_codes, _U8, (E, 2 * I, Hh), dev),
+        _arg("w13_scales", w13_scales, _U8, (E, 2 * I, Hh // 16), dev), E, 2 * Hh, I, M_cap, max_rows_per_expert,
+        _arg("h_bf16", h_bf16, _BF16, (M_cap, I), dev), st))
 
 
 def moe_grouped_gemm_l2_mxfp4(h_codes, h_scales, padded_offsets, counts, w2_codes, w2_scales, y_bf16,
                               max_rows_per_expert=0, stream=None):
     M_cap, Ih = h_codes.shape
     E, H, _ = w2_codes.shape
+    dev, st = _on(h_codes, stream)
     _check("moe_grouped_gemm_l2_mxfp4", lib().moe_grouped_gemm_l2_mxfp4(
-        _arg("h_codes", h_codes, _U8, (M_cap, Ih)), _arg("h_scales", h_scales, _U8, (M_cap, Ih // 16)),
-        _arg("padded_offsets", padded_offsets, _INT, (E + 1,)), _arg("counts", counts, _INT, (E,)),
-        _arg("w2_codes", w2_codes, _U8, (E, H, Ih)), _arg("w2_scales", w2_scales, _U8, (E, H, Ih // 16)), E, H,
-        2 * Ih, M_cap, max_rows_per_expert, _arg("y_bf16", y_bf16, _BF16, (M_cap, H)), _stream(stream)))
+        _arg("h_codes", h_codes, _U8, (M_cap, Ih), dev), _arg("h_scales", h_scales, _U8, (M_cap, Ih // 16), dev),
+        _arg("padded_offsets", padded_offsets, _INT, (E + 1,), dev), _arg("counts", counts, _INT, (E,), dev),
+        _arg("w2_codes", w2_codes, _U8, (E, H, Ih), dev), _arg("w2_scales", w2_scales, _U8, (E, H, Ih // 16), dev), E, H,
+        2 * Ih, M_cap, max_rows_per_expert, _arg("y_bf16", y_bf16, _BF16, (M_cap, H), dev), st))

@@ -143,6 +143,7 @@ SHAPES = [  # M, N, K
     (0, 64, 256), (1, 16, 128), (1, 7168, 2048), (5, 48, 384), (16, 256, 7168), (17, 272, 640), (32, 512, 1024),
     (33, 128, 128), (64, 80, 2176), (100, 4096, 512), (129, 528, 1152), (255, 256, 256), (256, 256, 512),
     (257, 1040, 896), (513, 2048, 1024), (1000, 304, 2048), (8, 4096, 16384),
+    (13, 48, 9088), (9, 32, 20480), (3, 16, 40448), (5, 32, 40576),  # long reductions, few rows
 ]
 
 
