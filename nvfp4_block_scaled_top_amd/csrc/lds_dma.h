@@ -27,6 +27,15 @@ __device__ __forceinline__ void dma16nt(const uint8_t* src, uint32_t lds) {
   lds = __builtin_amdgcn_readfirstlane(lds);
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off nt" ::"s"(lds), "v"(src) : "memory", "m0");
 }
+// The same from a wave-uniform base and a 32-bit lane offset.
+__device__ __forceinline__ void dma16s(const uint8_t* base, uint32_t off, uint32_t lds) {
+  lds = __builtin_amdgcn_readfirstlane(lds);
+  const uint64_t b = reinterpret_cast<uint64_t>(base);
+  const uint64_t sb = (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)b) |
+                      (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(b >> 32)) << 32;
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(sb)
+               : "memory", "m0");
+}
 __device__ __forceinline__ void dma4(const uint8_t* src, uint32_t lds) {
   lds = __builtin_amdgcn_readfirstlane(lds);
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(lds), "v"(src) : "memory", "m0");

@@ -22,17 +22,6 @@ constexpr int kMxDevices = 64;
 
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 
-__device__ __forceinline__ f32x16 mx_mfma32_lo(u32x4 a, u32x4 b, f32x16 c, uint32_t sa, uint32_t sb) {
-  const i32x8 av{(int)a[0], (int)a[1], (int)a[2], (int)a[3], 0, 0, 0, 0};
-  const i32x8 bv{(int)b[0], (int)b[1], (int)b[2], (int)b[3], 0, 0, 0, 0};
-  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(av, bv, c, 4, 4, 0, (int)sa, 0, (int)sb);
-}
-__device__ __forceinline__ f32x16 mx_mfma32_hi(u32x4 a, u32x4 b, f32x16 c, uint32_t sa, uint32_t sb) {
-  const i32x8 av{(int)a[0], (int)a[1], (int)a[2], (int)a[3], 0, 0, 0, 0};
-  const i32x8 bv{(int)b[0], (int)b[1], (int)b[2], (int)b[3], 0, 0, 0, 0};
-  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(av, bv, c, 4, 4, 1, (int)sa, 1, (int)sb);
-}
-
 __device__ __forceinline__ float mx_silu(float g) {
   return g * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-g * 1.4426950408889634f));
 }
@@ -43,6 +32,11 @@ __device__ __forceinline__ void mx_barrier() {
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
 }
+
+template <int V>
+struct IntTag {
+  static constexpr int value = V;
+};
 
 // Rows of expert e and their first row; without tables there is one group of all p.M rows.
 __device__ __forceinline__ int mx_count(const MxGemmArgs& p, int e) { return p.counts ? p.counts[e] : (int)p.M; }
@@ -314,204 +308,66 @@ __global__ __launch_bounds__(kMxSplit* kWave, 1) void mx_small_kernel(MxGemmArgs
 // Experts of more rows: 256 weight rows x BM token rows a tile, BM = 256, or 128 or 64 for an
 // expert's last rows when they fit; one persistent workgroup of 8 waves a CU.
 //
-// Stages of 128 K elements go from global memory straight into an LDS ring (no registers); a wave
-// waits for its own loads (vmcnt), one barrier makes everyone's visible, and the stage three ahead
-// is requested right after it, into the slot that the barrier has just freed.  A stage holds, per
-// operand, 64 code bytes a row (16-byte chunk c of row R in slot c ^ mx_swz(R), so that the 16-byte
-// reads of consecutive rows hit distinct banks) and 4 scale bytes a row.
+// Stages of 256 K elements go from global memory straight into one of two LDS slots (no registers): at
+// the top of a stage a wave waits for its own loads, one barrier makes everyone's visible and says that
+// the other slot is free, the next stage is requested into it, and the stage is computed meanwhile.
+// The stages run on across tiles: a tile's last stage requests the next tile's first, whose rows and
+// expert were found while this tile was computed.
+//
+// A stage holds 128 code bytes a row of either operand (a load instruction covers 8 rows; with 128
+// contiguous bytes a row it takes 19 cycles, with 64 bytes 28), block c of row R at slot
+// c ^ mx_swz(R), which the 16-byte reads of 32 rows meet without bank conflicts.  Scales come in
+// stages of 512 elements, 16 bytes a row: 64 rows cost a load instruction 97 cycles whatever it
+// brings of each.
 //
 // The 32x32x64 form is used: it sustains 9.2 PFLOP/s from registers (6.6 on random data, where the
 // chip lowers its clock), the 16x16x128 form 6.9 (5.5).  Lane (r, h) of a 32-row fragment takes blocks
-// 2h and 2h + 1 of its row, one a step, so its two scale bytes are neighbours: one 2-byte read, and
-// the instruction picks the byte.  Both operands use the same order, so every block is met once.
+// 4h .. 4h+3 of the stage, one a step: its four scale bytes are one word, and the instruction picks
+// the byte.  Both operands use the same order, so every block is met once.
 //
 // A wave computes 64 token rows x 32 * WB weight rows (WB = 4, 2, 1 for BM = 256, 128, 64).  Gate+up:
 // the first half of a wave's weight rows are gate rows, the second half the up rows of the same h
 // columns, so both meet in one lane.
 // ============================================================================================
 constexpr int kMxWaves = 8, kMxThreads = kMxWaves * kWave;
-constexpr int kMxBn = 256;     // weight rows of a tile
-constexpr int kMxBm = 256;     // token rows of a full tile
-constexpr int kMxSlots = 4, kMxAhead = kMxSlots - 1;
-constexpr int kMxBand = 8;     // m-tiles walked together, for L2 reuse of the weights
+constexpr int kMxBn = 256;                       // weight rows of a tile
+constexpr int kMxBm = 256;                       // token rows of a full tile
+constexpr int kMxBand = 8;                       // m-tiles walked together, for L2 reuse of the weights
+constexpr int kMxStageK = 256, kMxRowBytes = kMxStageK / 2;
+constexpr int kMxACodes = kMxBn * kMxRowBytes;   // within a slot: the weights' codes, then the tokens'
+constexpr int kMxStage = kMxACodes + kMxBm * kMxRowBytes;
+constexpr int kMxAScales = kMxBn * 16;           // within a scale buffer
+constexpr int kMxScaleBuf = kMxAScales + kMxBm * 16;
+constexpr int kMxScales = 2 * kMxStage;          // LDS: two slots, two scale buffers, the tables
+constexpr int kMxTables = kMxScales + 2 * kMxScaleBuf;
+static_assert(kMxTables + 4 * (MEGAMOE_MAX_EXPERTS + 1) + 8 * kMxBm <= kMxLds, "the LDS layout fits");
 
-__device__ __forceinline__ constexpr int mx_swz(int R) { return ((R >> 1) ^ (R >> 3)) & 3; }
+__device__ __forceinline__ constexpr int mx_swz(int R) { return (R >> 1) & 7; }
 
-template <int BM>
-struct MxShape {
-  static constexpr int kWM = BM / 64, kWN = kMxWaves / kWM;
-  static constexpr int kWB = kMxBn / kWN / 32;                     // 32-row weight blocks a wave
-  static constexpr int kACodeDma = BM >= 128 ? BM / 128 : 1;       // 16-row loads a wave (BM = 64: two waves load the same)
-  static constexpr int kDma = kACodeDma + 2 + 1;                   // loads a wave and stage
-  static constexpr int kACodes = kMxBn * 64, kWScales = kACodes + BM * 64;
-  static constexpr int kAScales = kWScales + kMxBn * 4;
-  static constexpr int kStage = kAScales + BM * 4;
+// One output tile: BM = 64 * wb token rows from row0 on (left of them real), n-tile nt.
+struct MxTile {
+  int e, nt, wb, left;
+  int64_t row0;
 };
-constexpr int kMxRing = kMxSlots * MxShape<kMxBm>::kStage;
-static_assert(kMxRing + 4 * (MEGAMOE_MAX_EXPERTS + 1) <= kMxLds, "the ring and the tables fit");
 
-// Waits for this wave's loads but those of the last `after` stages, and for its LDS reads.
-template <class S, int K>
-__device__ __forceinline__ void mx_wait_stages(int after) {
-  constexpr int n = K * S::kDma;
-  static_assert(n < 64, "vmcnt range");
-  if constexpr (K > 0) {
-    if (after < K) {
-      mx_wait_stages<S, K - 1>(after);
-      return;
-    }
-  }
-  __builtin_amdgcn_s_waitcnt((n & 15) | ((n >> 4) << 14) | (0x7 << 4));  // vmcnt(n) lgkmcnt(0)
-}
-
-template <bool kL1, int BM>
-__device__ __forceinline__ void mx_tile(const MxGemmArgs& p, uint8_t* smem, int e, int64_t row0, int left, int nt) {
-  using S = MxShape<BM>;
-  constexpr int WB = S::kWB;
-  const int K = p.K, nks = K / 128;
-  const int64_t Kh = K / 2, Ks = K / 32;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), lane = lane_id();
-  const int wm = wave / S::kWN, wn = wave % S::kWN;
-  const int r = lane & 31, h = lane >> 5;
-
-  // Rows past the tile's end read its first row, columns past the last one the last column's weights:
-  // what they feed is not stored.
-  auto a_row = [&](int R) -> int64_t {
-    const int64_t t = row0 + (R < left ? R : 0);
-    return p.row_token ? p.row_token[t] : t;
-  };
-  auto w_row = [&](int R) -> int64_t {
-    if constexpr (kL1) {
-      const int w = R / (32 * WB), x = R % (32 * WB);
-      int c = nt * (kMxBn / 2) + w * 16 * WB + x % (16 * WB);
-      c = c < p.N ? c : p.N - 1;
-      return (int64_t)e * 2 * p.N + (x < 16 * WB ? c : p.N + c);
-    } else {
-      const int c = nt * kMxBn + R;
-      return (int64_t)e * p.N + (c < p.N ? c : p.N - 1);
-    }
-  };
-  // Code loads cover 16 rows: lane l brings chunk (l % 4) ^ mx_swz(row) of row l / 4.
-  const uint8_t* a_src[S::kACodeDma];
-  int a_lds[S::kACodeDma];
-#pragma unroll
-  for (int j = 0; j < S::kACodeDma; ++j) {
-    const int R0 = (16 * S::kACodeDma * wave + 16 * j) % BM, R = R0 + lane / 4;
-    a_src[j] = p.a_codes + a_row(R) * Kh + 16 * ((lane & 3) ^ mx_swz(R));
-    a_lds[j] = S::kACodes + R0 * 64;
-  }
-  const uint8_t* w_src[2];
-#pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    const int R = 32 * wave + 16 * j + lane / 4;
-    w_src[j] = p.w_codes + w_row(R) * Kh + 16 * ((lane & 3) ^ mx_swz(R));
-  }
-  // Scale loads cover 64 rows: waves 0-3 the weights', waves 4-7 the tokens' (repeated when BM < 256).
-  const int s_row0 = wave < 4 ? 64 * wave : 64 * ((wave - 4) % (BM / 64));
-  const uint8_t* s_src = wave < 4 ? p.w_scales + w_row(s_row0 + lane) * Ks : p.a_scales + a_row(s_row0 + lane) * Ks;
-  const int s_lds = (wave < 4 ? S::kWScales : S::kAScales) + 4 * s_row0;
-
-  auto issue = [&](int ks) {
-    const uint32_t base = lds_addr(smem + (ks % kMxSlots) * S::kStage);
-    const int off = ks * 64;
-#pragma unroll
-    for (int j = 0; j < 2; ++j) dma16(w_src[j] + off, base + (32 * wave + 16 * j) * 64);
-#pragma unroll
-    for (int j = 0; j < S::kACodeDma; ++j) dma16(a_src[j] + off, base + a_lds[j]);
-    dma4(s_src + 4 * ks, base + s_lds);
-  };
-
-  f32x16 acc[2][WB];
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
-#pragma unroll
-    for (int f = 0; f < WB; ++f)
-#pragma unroll
-      for (int q = 0; q < 16; ++q) acc[i][f][q] = 0.f;
-
-  const int swz = mx_swz(r);  // of rows 32 i + r too
-  for (int ks = 0; ks < kMxAhead && ks < nks; ++ks) issue(ks);
-  for (int ks = 0; ks < nks; ++ks) {
-    const int after = nks - 1 - ks;
-    mx_wait_stages<S, kMxAhead - 1>(after < kMxAhead - 1 ? after : kMxAhead - 1);
-    mx_barrier();
-    if (ks + kMxAhead < nks) issue(ks + kMxAhead);
-    const uint8_t* st = smem + (ks % kMxSlots) * S::kStage;
-    u32x4 w[WB][2], a[2][2];
-    uint32_t wsc[WB], asc[2];
-#pragma unroll
-    for (int f = 0; f < WB; ++f) {
-      const int R = (wn * WB + f) * 32 + r;
-#pragma unroll
-      for (int s = 0; s < 2; ++s) w[f][s] = *reinterpret_cast<const u32x4*>(st + R * 64 + 16 * ((2 * h + s) ^ swz));
-      wsc[f] = *reinterpret_cast<const uint16_t*>(st + S::kWScales + R * 4 + 2 * h);
-    }
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int R = wm * 64 + 32 * i + r;
-#pragma unroll
-      for (int s = 0; s < 2; ++s)
-        a[i][s] = *reinterpret_cast<const u32x4*>(st + S::kACodes + R * 64 + 16 * ((2 * h + s) ^ swz));
-      asc[i] = *reinterpret_cast<const uint16_t*>(st + S::kAScales + R * 4 + 2 * h);
-    }
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-      for (int f = 0; f < WB; ++f) acc[i][f] = mx_mfma32_lo(w[f][0], a[i][0], acc[i][f], wsc[f], asc[i]);
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-      for (int f = 0; f < WB; ++f) acc[i][f] = mx_mfma32_hi(w[f][1], a[i][1], acc[i][f], wsc[f], asc[i]);
-  }
-
-  // Accumulator q of block (i, f): weight row 32 f + 8 (q / 4) + 4 h + q % 4 of the wave, token row 32 i + r.
-  uint16_t* out = static_cast<uint16_t*>(p.out);
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int R = wm * 64 + 32 * i + r;
-    if (R >= left) continue;
-    uint16_t* o = out + (row0 + R) * (int64_t)p.N;
-    if constexpr (kL1) {
-      const int c0 = nt * (kMxBn / 2) + wn * 16 * WB;
-#pragma unroll
-      for (int f = 0; f < (WB + 1) / 2; ++f)
-#pragma unroll
-        for (int q4 = 0; q4 < (WB == 1 ? 2 : 4); ++q4) {
-          const int c = c0 + 32 * f + 8 * q4 + 4 * h;
-          if (c >= p.N) continue;
-          uint32_t b[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float gt = acc[i][f][4 * q4 + j];
-            const float up = WB == 1 ? acc[i][0][(4 * q4 + j + 8) & 15] : acc[i][(f + WB / 2) % WB][4 * q4 + j];
-            b[j] = f32_to_bf16_any(mx_silu(gt) * up);
-          }
-          *reinterpret_cast<u32x2*>(o + c) = u32x2{b[0] | b[1] << 16, b[2] | b[3] << 16};
-        }
-    } else {
-#pragma unroll
-      for (int f = 0; f < WB; ++f)
-#pragma unroll
-        for (int q4 = 0; q4 < 4; ++q4) {
-          const int c = nt * kMxBn + (wn * WB + f) * 32 + 8 * q4 + 4 * h;
-          if (c >= p.N) continue;
-          uint32_t b[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) b[j] = f32_to_bf16_any(acc[i][f][4 * q4 + j]);
-          *reinterpret_cast<u32x2*>(o + c) = u32x2{b[0] | b[1] << 16, b[2] | b[3] << 16};
-        }
-    }
-  }
-  __syncthreads();  // every wave is done with the ring before the next tile's loads refill it
+template <int S>
+__device__ __forceinline__ f32x16 mx_mfma32(u32x4 a, u32x4 b, f32x16 c, uint32_t sa, uint32_t sb) {
+  const i32x8 av{(int)a[0], (int)a[1], (int)a[2], (int)a[3], 0, 0, 0, 0};
+  const i32x8 bv{(int)b[0], (int)b[1], (int)b[2], (int)b[3], 0, 0, 0, 0};
+  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(av, bv, c, 4, 4, S, (int)sa, S, (int)sb);
 }
 
 template <bool kL1>
 __global__ __launch_bounds__(kMxThreads, 1) void mx_tile_kernel(MxGemmArgs p) {
-  extern __shared__ __attribute__((aligned(16))) uint8_t s_mx[];  // ring, then the m-tile prefix [E + 1]
-  int* const pref = reinterpret_cast<int*>(s_mx + kMxRing);
-  const int E = p.E;
-  if (threadIdx.x < kWave) {  // exclusive prefix of the experts' m-tiles
-    const int lane = lane_id();
+  extern __shared__ __attribute__((aligned(16))) uint8_t s_mx[];
+  int* const s_row = reinterpret_cast<int*>(s_mx + kMxTables);  // [2][kMxBm] tokens of a tile's rows
+  int* const pref = s_row + 2 * kMxBm;                          // m-tiles before each expert [E + 1]
+  const int E = p.E, K = p.K, nks = (K + kMxStageK - 1) / kMxStageK, nblk = K / 32;
+  const int64_t Kh = K / 2, Ks = K / 32;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), lane = lane_id();
+  const int r = lane & 31, h = lane >> 5;
+  const bool wide_scales = K % 512 == 0;  // whole 16-byte scale pieces
+  if (wave == 0) {  // exclusive prefix of the experts' m-tiles
     int carry = 0;
     for (int c = 0; c < E; c += kWave) {
       const int cnt = c + lane < E ? mx_count(p, c + lane) : 0;
@@ -528,26 +384,243 @@ __global__ __launch_bounds__(kMxThreads, 1) void mx_tile_kernel(MxGemmArgs p) {
     if (lane == 0) pref[E] = carry;
   }
   __syncthreads();
-  const int ntn = (p.N + (kL1 ? kMxBn / 2 : kMxBn) - 1) / (kL1 ? kMxBn / 2 : kMxBn);
+  constexpr int cols = kL1 ? kMxBn / 2 : kMxBn;  // output columns of a tile
+  const int ntn = (p.N + cols - 1) / cols;
   const int64_t total = (int64_t)pref[E] * ntn;
-  // Workgroup b runs on XCD b % 8: the 32 workgroups of an XCD take 32 tiles in a row, which share
-  // rows and weights in its L2.
-  for (int64_t t = (blockIdx.x % 8) * (kMxGrid / 8) + blockIdx.x / 8; t < total; t += kMxGrid) {
-    int lo = 0, hi = E;  // pref[lo] * ntn <= t < pref[hi] * ntn
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if ((int64_t)pref[mid] * ntn <= t) lo = mid; else hi = mid;
-    }
-    const int e = lo, mts = pref[e + 1] - pref[e];
-    const int64_t local = t - (int64_t)pref[e] * ntn;
+
+  // Tile t of the list: its expert by two steps of 64 comparisons (at most 1024 experts).
+  const auto find = [&](int64_t t) {
+    const int step = (E + kWave - 1) / kWave;
+    const int at = lane * step;
+    const int chunk = __popcll(__ballot(at < E && (int64_t)pref[at < E ? at : 0] * ntn <= t)) - 1;
+    const int at2 = chunk * step + lane;
+    const int e = chunk * step - 1 +
+                  __popcll(__ballot(lane < step && at2 < E && (int64_t)pref[at2 < E ? at2 : 0] * ntn <= t));
+    const int first = pref[e], mts = pref[e + 1] - first;
+    const int64_t local = t - (int64_t)first * ntn;
     const int band = (int)(local / ((int64_t)kMxBand * ntn)), in = (int)(local % ((int64_t)kMxBand * ntn));
     const int width = min(kMxBand, mts - band * kMxBand);
-    const int nt = in / width, mt = band * kMxBand + in % width;
-    const int left = mx_count(p, e) - mt * kMxBm;
-    const int64_t row0 = (p.padded_offsets ? p.padded_offsets[e] : 0) + (int64_t)mt * kMxBm;
-    if (left > 128) mx_tile<kL1, 256>(p, s_mx, e, row0, left, nt);
-    else if (left > 64) mx_tile<kL1, 128>(p, s_mx, e, row0, left, nt);
-    else mx_tile<kL1, 64>(p, s_mx, e, row0, left, nt);
+    const int mt = band * kMxBand + in % width;
+    MxTile x;
+    x.e = __builtin_amdgcn_readfirstlane(e);
+    x.nt = __builtin_amdgcn_readfirstlane(in / width);
+    x.left = __builtin_amdgcn_readfirstlane(mx_count(p, e) - mt * kMxBm);
+    x.wb = x.left > 128 ? 4 : x.left > 64 ? 2 : 1;
+    x.row0 = (p.padded_offsets ? p.padded_offsets[x.e] : 0) +
+             (int64_t)__builtin_amdgcn_readfirstlane(mt) * kMxBm;
+    return x;
+  };
+  // Rows past the tile's end read its last row, columns past the last one the last columns' weights:
+  // what they feed is not stored.  The tokens of a gathered tile's rows are brought to s_row[parity]
+  // by loads that a later barrier makes visible.
+  const auto fetch_rows = [&](const MxTile& x, int parity) {
+    if (kL1 && p.row_token != nullptr && wave < 4) {
+      const int R = 64 * wave + lane;
+      dma4(reinterpret_cast<const uint8_t*>(p.row_token + x.row0 + (R < x.left ? R : x.left - 1)),
+           lds_addr(reinterpret_cast<uint8_t*>(s_row + parity * kMxBm + 64 * wave)));
+    }
+  };
+  const auto a_row = [&](const MxTile& x, int parity, int R) -> int {
+    if (kL1 && p.row_token != nullptr) return s_row[parity * kMxBm + R];
+    return (int)x.row0 + (R < x.left ? R : x.left - 1);
+  };
+  // Weight row, within the expert, of row R of a tile (R: of 8 rows in a row, whose columns follow each
+  // other; N is a multiple of 8).
+  const auto w_row = [&](const MxTile& x, int R) -> int {
+    if constexpr (kL1) {
+      const int half = 16 * x.wb, in = R & (2 * half - 1);
+      const int c = x.nt * cols + (R - in) / 2 + (in & (half - 1));
+      return (c < p.N ? c : p.N - 8 + (c & 7)) + (in >= half ? p.N : 0);
+    } else {
+      const int c = x.nt * cols + R;
+      return c < p.N ? c : p.N - 8 + (c & 7);
+    }
+  };
+  int issued = 0, scale_issued = 0;  // parities of the slots
+  const auto issue = [&](const MxTile& x, int parity, int ks) {
+    int ln = lane;
+    asm volatile("" : "+v"(ln));  // addresses are computed here, not kept in registers across the stages
+    const int blk0 = (ln & 7) ^ mx_swz(ln / 8);  // block that this lane brings of an even 8-row piece (^ 4: odd)
+    const uint32_t w_lane = (uint32_t)(ln / 8) * (uint32_t)Kh;
+    const uint32_t base = lds_addr(s_mx + (issued & 1) * kMxStage);
+    ++issued;
+    // Lane l of a load brings a block of row l / 8 to place l % 8; a block beyond K (in the last stage)
+    // is replaced by one of the stage's first half, and the compute skips it.
+    const bool whole = (ks + 1) * 8 <= nblk;
+    const uint32_t c0 = 16u * (whole ? blk0 : blk0 & 3), c1 = 16u * (whole ? blk0 ^ 4 : blk0 & 3);
+    const int64_t wn0 = (int64_t)x.e * (kL1 ? 2 : 1) * p.N;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int R0 = 32 * wave + 8 * j;
+      dma16s(p.w_codes + (wn0 + w_row(x, R0)) * Kh + kMxRowBytes * ks, w_lane + (j & 1 ? c1 : c0),
+             base + R0 * kMxRowBytes);
+    }
+    for (int j = 0; j < x.wb; ++j) {
+      const int R0 = 8 * (x.wb * wave + j);
+      const uint8_t* src = p.a_codes + (uint64_t)(uint32_t)a_row(x, parity, R0 + ln / 8) * (uint32_t)Kh;
+      dma16(src + kMxRowBytes * ks + ((x.wb * wave + j) & 1 ? c1 : c0), base + kMxACodes + R0 * kMxRowBytes);
+    }
+    if (ks & 1) return;
+    const uint32_t sbase = lds_addr(s_mx + kMxScales + (scale_issued & 1) * kMxScaleBuf);
+    ++scale_issued;
+    // waves 0-3: scales of 64 weight rows each; the next wb waves: of 64 token rows each
+    if (wave >= 4 + x.wb) return;
+    const int R0 = 64 * (wave & 3);
+    const uint32_t to = sbase + (wave < 4 ? 0 : kMxAScales) + 16 * R0;
+    if (wide_scales) {
+      const uint8_t* src = wave < 4
+                               ? p.w_scales + wn0 * Ks + (uint64_t)(uint32_t)w_row(x, R0 + ln) * (uint32_t)Ks
+                               : p.a_scales + (uint64_t)(uint32_t)a_row(x, parity, R0 + ln) * (uint32_t)Ks;
+      dma16(src + 8 * ks, to);
+    } else {
+      // K not a multiple of 512: words, 16 rows a load; a word beyond K is replaced by the first
+      const int word = ks * 2 + (ln & 3);
+      const uint32_t off = 4u * (4 * word < nblk ? word : ks * 2);
+      for (int j = 0; j < 4; ++j) {
+        const int R = R0 + 16 * j + ln / 4;
+        const uint8_t* src = wave < 4 ? p.w_scales + wn0 * Ks + (uint64_t)(uint32_t)w_row(x, R) * (uint32_t)Ks
+                                      : p.a_scales + (uint64_t)(uint32_t)a_row(x, parity, R) * (uint32_t)Ks;
+        dma4(src + off, to + 256 * j);
+      }
+    }
+  };
+
+  // XCD b % 8 takes 32 tiles in a row of every 256: they share rows and weights in its L2.
+  int64_t t = (blockIdx.x % 8) * (kMxGrid / 8) + blockIdx.x / 8;
+  if (t >= total) return;  // the whole workgroup
+  MxTile cur = find(t), nxt = cur;
+  int parity = 0;  // of cur's rows in s_row
+  fetch_rows(cur, parity);
+  wait_vmcnt<0>();
+  mx_barrier();
+  issue(cur, parity, 0);
+  int stage = 0, sstage = 0;
+  bool first = true;
+
+  const auto run_tile = [&](auto wb_tag) {
+    constexpr int WB = decltype(wb_tag)::value;
+    constexpr int WM = WB, WN = kMxWaves / WM;
+    const int wm = wave / WN, wn = wave % WN;
+    const bool more = t + kMxGrid < total;
+    f32x16 acc[2][WB];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int f = 0; f < WB; ++f)
+#pragma unroll
+        for (int q = 0; q < 16; ++q) acc[i][f][q] = 0.f;
+    const int swz = mx_swz(r);  // of rows 32 i + r too
+    for (int ks = 0; ks < nks; ++ks) {
+      // A tile's first stage was waited for before the last tile's stores were issued.
+      if (ks > 0 || first) __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0) lgkmcnt(0)
+      else __builtin_amdgcn_s_waitcnt(0xC07F);                  // lgkmcnt(0)
+      mx_barrier();
+      if (ks == 0 && more) {
+        nxt = find(t + kMxGrid);
+        fetch_rows(nxt, parity ^ 1);
+        if (nks == 1) {  // no later stage waits for these rows
+          wait_vmcnt<0>();
+          mx_barrier();
+        }
+      }
+      if (ks + 1 < nks) issue(cur, parity, ks + 1);
+      else if (more) issue(nxt, parity ^ 1, 0);
+      const uint8_t* st = s_mx + (stage & 1) * kMxStage;
+      const uint8_t* ss = s_mx + kMxScales + (sstage & 1) * kMxScaleBuf + 8 * (ks & 1) + 4 * h;
+      const uint8_t* wp = st + (wn * WB * 32 + r) * kMxRowBytes;
+      const uint8_t* ap = st + kMxACodes + (wm * 64 + r) * kMxRowBytes;
+      uint32_t wsc[WB], asc[2];
+#pragma unroll
+      for (int f = 0; f < WB; ++f) wsc[f] = *reinterpret_cast<const uint32_t*>(ss + ((wn * WB + f) * 32 + r) * 16);
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        asc[i] = *reinterpret_cast<const uint32_t*>(ss + kMxAScales + (wm * 64 + 32 * i + r) * 16);
+      const bool beyond = (ks + 1) * 8 > nblk && h == 1;  // blocks 4 .. 7 of a stage that has only four
+      if ((ks + 1) * 8 > nblk && h == 1) {
+#pragma unroll
+        for (int f = 0; f < WB; ++f) wsc[f] = 0x7F7F7F7Fu;
+        asc[0] = asc[1] = 0x7F7F7F7Fu;
+      }
+      const auto read_w = [&](int f, int s) {
+        return *reinterpret_cast<const u32x4*>(wp + f * 32 * kMxRowBytes + 16 * ((4 * h + s) ^ swz));
+      };
+      const auto read_a = [&](int i, int s) {
+        u32x4 v = *reinterpret_cast<const u32x4*>(ap + i * 32 * kMxRowBytes + 16 * ((4 * h + s) ^ swz));
+        return beyond ? u32x4{0u, 0u, 0u, 0u} : v;
+      };
+      u32x4 w[2][WB], a[2][2];
+#pragma unroll
+      for (int f = 0; f < WB; ++f) w[0][f] = read_w(f, 0);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) a[0][i] = read_a(i, 0);
+      const auto step = [&](auto s_tag) {
+        constexpr int S = decltype(s_tag)::value;
+        if constexpr (S < 3) {
+#pragma unroll
+          for (int f = 0; f < WB; ++f) w[(S + 1) & 1][f] = read_w(f, S + 1);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) a[(S + 1) & 1][i] = read_a(i, S + 1);
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int f = 0; f < WB; ++f) acc[i][f] = mx_mfma32<S>(w[S & 1][f], a[S & 1][i], acc[i][f], wsc[f], asc[i]);
+      };
+      step(IntTag<0>{});
+      step(IntTag<1>{});
+      step(IntTag<2>{});
+      step(IntTag<3>{});
+      ++stage;
+      if ((ks & 1) || ks + 1 == nks) ++sstage;
+    }
+    if (more) wait_vmcnt<0>();  // the next tile's first stage, ahead of the stores
+
+    // Accumulator q of block (i, f): weight row 32 f + 8 (q / 4) + 4 h + q % 4 of the wave, token row 32 i + r.
+    uint16_t* out = static_cast<uint16_t*>(p.out);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int R = wm * 64 + 32 * i + r;
+      if (R >= cur.left) continue;
+      uint16_t* o = out + (cur.row0 + R) * (int64_t)p.N;
+      if constexpr (kL1) {
+        const int c0 = cur.nt * cols + wn * 16 * WB;
+#pragma unroll
+        for (int f = 0; f < (WB + 1) / 2; ++f)
+#pragma unroll
+          for (int q4 = 0; q4 < (WB == 1 ? 2 : 4); ++q4) {
+            const int c = c0 + 32 * f + 8 * q4 + 4 * h;
+            if (c >= p.N) continue;
+            uint32_t b[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const float gt = acc[i][f][4 * q4 + j];
+              const float up = WB == 1 ? acc[i][0][(4 * q4 + j + 8) & 15] : acc[i][(f + WB / 2) % WB][4 * q4 + j];
+              b[j] = f32_to_bf16_any(mx_silu(gt) * up);
+            }
+            *reinterpret_cast<u32x2*>(o + c) = u32x2{b[0] | b[1] << 16, b[2] | b[3] << 16};
+          }
+      } else {
+#pragma unroll
+        for (int f = 0; f < WB; ++f)
+#pragma unroll
+          for (int q4 = 0; q4 < 4; ++q4) {
+            const int c = cur.nt * cols + (wn * WB + f) * 32 + 8 * q4 + 4 * h;
+            if (c >= p.N) continue;
+            uint32_t b[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) b[j] = f32_to_bf16_any(acc[i][f][4 * q4 + j]);
+            *reinterpret_cast<u32x2*>(o + c) = u32x2{b[0] | b[1] << 16, b[2] | b[3] << 16};
+          }
+      }
+    }
+    first = false;
+  };
+  for (; t < total; t += kMxGrid) {
+    if (cur.wb == 4) run_tile(IntTag<4>{});
+    else if (cur.wb == 2) run_tile(IntTag<2>{});
+    else run_tile(IntTag<1>{});
+    cur = nxt;
+    parity ^= 1;
   }
 }
 
@@ -596,7 +669,7 @@ static hipError_t launch_mx(const MxGemmArgs& a, const MxSmallPlan& plan, bool s
     err = mx_allow_lds(mx_tile_kernel<kL1>, tile_done);
     if (err != hipSuccess) return err;
     hipLaunchKernelGGL(mx_tile_kernel<kL1>, dim3(kMxGrid), dim3(kMxThreads),
-                       kMxRing + sizeof(int) * ((size_t)a.E + 1), stream, a);
+                       kMxTables + sizeof(int) * ((size_t)2 * kMxBm + a.E + 1), stream, a);
     err = hipGetLastError();
   }
   return err;
