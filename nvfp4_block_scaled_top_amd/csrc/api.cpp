@@ -666,6 +666,9 @@ static int32_t mx_gemm(const MxGemmArgs& a, bool l1, int64_t rows, int32_t max_r
   if (a.E < 1 || a.E > MEGAMOE_MAX_EXPERTS || a.K < 128 || a.K % 128 != 0 || a.N < 16 || a.N % 16 != 0 ||
       a.N >= (1 << 30) || rows < 0 || rows >= (int64_t)1 << 31 || max_rows_per_expert < 0)
     return MEGAMOE_ERR_SHAPE;
+  // row offsets are 32-bit counts of 16 bytes (a token tensor has no more rows than the output)
+  if (rows * (a.K / 2) >= (int64_t)1 << 36 || (l1 ? 2 : 1) * (int64_t)a.N * (a.K / 2) >= (int64_t)1 << 36)
+    return MEGAMOE_ERR_SHAPE;
   if (!a.w_codes || !a.w_scales) return MEGAMOE_ERR_NULL;
   if (rows > 0 && (!a.a_codes || !a.a_scales || !a.out)) return MEGAMOE_ERR_NULL;
   if (!aligned(a.a_codes, 16) || !aligned(a.w_codes, 16) || !aligned(a.a_scales, 4) || !aligned(a.w_scales, 4) ||

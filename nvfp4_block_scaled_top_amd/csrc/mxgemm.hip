@@ -340,7 +340,7 @@ constexpr int kMxAScales = kMxBn * 16;           // within a scale buffer
 constexpr int kMxScaleBuf = kMxAScales + kMxBm * 16;
 constexpr int kMxScales = 2 * kMxStage;          // LDS: two slots, two scale buffers, the tables
 constexpr int kMxTables = kMxScales + 2 * kMxScaleBuf;
-static_assert(kMxTables + 4 * (MEGAMOE_MAX_EXPERTS + 1) + 8 * kMxBm <= kMxLds, "the LDS layout fits");
+static_assert(kMxTables + 4 * (MEGAMOE_MAX_EXPERTS + 1) + 4 * kMxBm <= kMxLds, "the LDS layout fits");
 
 __device__ __forceinline__ constexpr int mx_swz(int R) { return (R >> 1) & 7; }
 
@@ -349,6 +349,9 @@ struct MxTile {
   int e, nt, wb, left;
   int64_t row0;
 };
+
+// What a load brings for a block beyond K: zero codes, and scales of 1.
+__device__ const uint32_t g_mx_pad[8] = {0u, 0u, 0u, 0u, 0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu};
 
 template <int S>
 __device__ __forceinline__ f32x16 mx_mfma32(u32x4 a, u32x4 b, f32x16 c, uint32_t sa, uint32_t sb) {
@@ -360,12 +363,11 @@ __device__ __forceinline__ f32x16 mx_mfma32(u32x4 a, u32x4 b, f32x16 c, uint32_t
 template <bool kL1>
 __global__ __launch_bounds__(kMxThreads, 1) void mx_tile_kernel(MxGemmArgs p) {
   extern __shared__ __attribute__((aligned(16))) uint8_t s_mx[];
-  int* const s_row = reinterpret_cast<int*>(s_mx + kMxTables);  // [2][kMxBm] tokens of a tile's rows
-  int* const pref = s_row + 2 * kMxBm;                          // m-tiles before each expert [E + 1]
+  int* const s_row = reinterpret_cast<int*>(s_mx + kMxTables);  // tokens of the next tile's rows
+  int* const pref = s_row + kMxBm;                              // m-tiles before each expert [E + 1]
   const int E = p.E, K = p.K, nks = (K + kMxStageK - 1) / kMxStageK, nblk = K / 32;
   const int64_t Kh = K / 2, Ks = K / 32;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), lane = lane_id();
-  const int r = lane & 31, h = lane >> 5;
   const bool wide_scales = K % 512 == 0;  // whole 16-byte scale pieces
   if (wave == 0) {  // exclusive prefix of the experts' m-tiles
     int carry = 0;
@@ -386,101 +388,122 @@ __global__ __launch_bounds__(kMxThreads, 1) void mx_tile_kernel(MxGemmArgs p) {
   __syncthreads();
   constexpr int cols = kL1 ? kMxBn / 2 : kMxBn;  // output columns of a tile
   const int ntn = (p.N + cols - 1) / cols;
-  const int64_t total = (int64_t)pref[E] * ntn;
+  const int64_t total = (int64_t)__builtin_amdgcn_readfirstlane(pref[E]) * ntn;
 
   // Tile t of the list: its expert by two steps of 64 comparisons (at most 1024 experts).
-  const auto find = [&](int64_t t) {
+  const auto find = [&](int64_t t) __attribute__((always_inline)) {
     const int step = (E + kWave - 1) / kWave;
     const int at = lane * step;
     const int chunk = __popcll(__ballot(at < E && (int64_t)pref[at < E ? at : 0] * ntn <= t)) - 1;
     const int at2 = chunk * step + lane;
-    const int e = chunk * step - 1 +
-                  __popcll(__ballot(lane < step && at2 < E && (int64_t)pref[at2 < E ? at2 : 0] * ntn <= t));
-    const int first = pref[e], mts = pref[e + 1] - first;
+    const int e = __builtin_amdgcn_readfirstlane(
+        chunk * step - 1 + __popcll(__ballot(lane < step && at2 < E && (int64_t)pref[at2 < E ? at2 : 0] * ntn <= t)));
+    const int first = __builtin_amdgcn_readfirstlane(pref[e]);
+    const int mts = __builtin_amdgcn_readfirstlane(pref[e + 1]) - first;
     const int64_t local = t - (int64_t)first * ntn;
     const int band = (int)(local / ((int64_t)kMxBand * ntn)), in = (int)(local % ((int64_t)kMxBand * ntn));
     const int width = min(kMxBand, mts - band * kMxBand);
     const int mt = band * kMxBand + in % width;
-    MxTile x;
-    x.e = __builtin_amdgcn_readfirstlane(e);
-    x.nt = __builtin_amdgcn_readfirstlane(in / width);
-    x.left = __builtin_amdgcn_readfirstlane(mx_count(p, e) - mt * kMxBm);
+    MxTile x;  // wave-uniform, in scalar registers
+    x.e = e;
+    x.nt = in / width;
+    x.left = __builtin_amdgcn_readfirstlane(mx_count(p, e)) - mt * kMxBm;
     x.wb = x.left > 128 ? 4 : x.left > 64 ? 2 : 1;
-    x.row0 = (p.padded_offsets ? p.padded_offsets[x.e] : 0) +
-             (int64_t)__builtin_amdgcn_readfirstlane(mt) * kMxBm;
+    x.row0 = (int64_t)(p.padded_offsets ? __builtin_amdgcn_readfirstlane(p.padded_offsets[e]) : 0) + (int64_t)mt * kMxBm;
     return x;
   };
   // Rows past the tile's end read its last row, columns past the last one the last columns' weights:
-  // what they feed is not stored.  The tokens of a gathered tile's rows are brought to s_row[parity]
-  // by loads that a later barrier makes visible.
-  const auto fetch_rows = [&](const MxTile& x, int parity) {
+  // what they feed is not stored.  The tokens of a gathered tile's rows are brought to s_row by loads
+  // that a later barrier makes visible.
+  const auto fetch_rows = [&](const MxTile& x) __attribute__((always_inline)) {
     if (kL1 && p.row_token != nullptr && wave < 4) {
       const int R = 64 * wave + lane;
       dma4(reinterpret_cast<const uint8_t*>(p.row_token + x.row0 + (R < x.left ? R : x.left - 1)),
-           lds_addr(reinterpret_cast<uint8_t*>(s_row + parity * kMxBm + 64 * wave)));
+           lds_addr(reinterpret_cast<uint8_t*>(s_row + 64 * wave)));
     }
   };
-  const auto a_row = [&](const MxTile& x, int parity, int R) -> int {
-    if (kL1 && p.row_token != nullptr) return s_row[parity * kMxBm + R];
-    return (int)x.row0 + (R < x.left ? R : x.left - 1);
-  };
-  // Weight row, within the expert, of row R of a tile (R: of 8 rows in a row, whose columns follow each
-  // other; N is a multiple of 8).
-  const auto w_row = [&](const MxTile& x, int R) -> int {
-    if constexpr (kL1) {
-      const int half = 16 * x.wb, in = R & (2 * half - 1);
-      const int c = x.nt * cols + (R - in) / 2 + (in & (half - 1));
-      return (c < p.N ? c : p.N - 8 + (c & 7)) + (in >= half ? p.N : 0);
-    } else {
-      const int c = x.nt * cols + R;
-      return c < p.N ? c : p.N - 8 + (c & 7);
-    }
+  // Waves 0-3 bring the stages: wave w weight rows 64 w .. 64 w + 63 and the w-th quarter of the token
+  // rows.  (They share the SIMDs with waves 4-7, which multiply meanwhile.)  What a load adds to its
+  // tensor's address is kept in units of 16 bytes for the codes and of 4 for the scales (operands of an
+  // expert are below 64 GB), the eight weight loads' in the lanes of one register: with all of it
+  // computed anew, 40 instructions a load, a stage's loads took 3800 cycles to issue.
+  uint32_t w_off = 0, a_off[8] = {0, 0, 0, 0, 0, 0, 0, 0}, ws_off = 0, as_off = 0;
+  const auto set_loads = [&](const MxTile& x) __attribute__((always_inline)) {
+    if (wave >= 4) return;
+    int ln = lane;
+    asm volatile("" : "+v"(ln));  // nothing of this is kept in registers across the tile
+    const auto a_row = [&](int R) -> uint32_t {
+      if (kL1 && p.row_token != nullptr) return (uint32_t)s_row[R];
+      return (uint32_t)((int)x.row0 + (R < x.left ? R : x.left - 1));
+    };
+    const auto w_row = [&](int R) -> uint32_t {  // within the expert; N is a multiple of 8
+      if constexpr (kL1) {
+        const int half = 16 * x.wb, in = R & (2 * half - 1);
+        const int c = x.nt * cols + (R - in) / 2 + (in & (half - 1));
+        return (uint32_t)((c < p.N ? c : p.N - 8 + (c & 7)) + (in >= half ? p.N : 0));
+      } else {
+        const int c = x.nt * cols + R;
+        return (uint32_t)(c < p.N ? c : p.N - 8 + (c & 7));
+      }
+    };
+    w_off = w_row(64 * wave + 8 * (ln & 7)) * (uint32_t)(Kh / 16);
+    ws_off = w_row(64 * wave + ln) * (uint32_t)(Ks / 4);
+    as_off = a_row(64 * wave + ln) * (uint32_t)(Ks / 4);
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      a_off[j] = a_row((8 * (2 * x.wb * wave + j) + ln / 8) & (kMxBm - 1)) * (uint32_t)(Kh / 16);
   };
   int issued = 0, scale_issued = 0;  // parities of the slots
-  const auto issue = [&](const MxTile& x, int parity, int ks) {
-    int ln = lane;
-    asm volatile("" : "+v"(ln));  // addresses are computed here, not kept in registers across the stages
-    const int blk0 = (ln & 7) ^ mx_swz(ln / 8);  // block that this lane brings of an even 8-row piece (^ 4: odd)
-    const uint32_t w_lane = (uint32_t)(ln / 8) * (uint32_t)Kh;
-    const uint32_t base = lds_addr(s_mx + (issued & 1) * kMxStage);
+  const auto issue = [&](const MxTile& x, int ks) __attribute__((always_inline)) {
+    const int slot = issued & 1, sslot = scale_issued & 1;
     ++issued;
-    // Lane l of a load brings a block of row l / 8 to place l % 8; a block beyond K (in the last stage)
-    // is replaced by one of the stage's first half, and the compute skips it.
-    const bool whole = (ks + 1) * 8 <= nblk;
-    const uint32_t c0 = 16u * (whole ? blk0 : blk0 & 3), c1 = 16u * (whole ? blk0 ^ 4 : blk0 & 3);
+    if (!(ks & 1)) ++scale_issued;
+    if (wave >= 4) return;
+    int ln = lane;
+    asm volatile("" : "+v"(ln));  // what follows from the lane is computed here, not held through the tile
+    const uint32_t base = lds_addr(s_mx + slot * kMxStage);
     const int64_t wn0 = (int64_t)x.e * (kL1 ? 2 : 1) * p.N;
+    const uint8_t* const wb = p.w_codes + wn0 * Kh + kMxRowBytes * ks;
+    const uint8_t* const pad = reinterpret_cast<const uint8_t*>(g_mx_pad);
+    // Lane l of a load brings a block of row l / 8 to place l % 8.
+    const int blk0 = (ln & 7) ^ mx_swz(ln / 8);  // of an even 8-row piece (^ 4: odd)
+    const uint32_t w_lane = (uint32_t)(ln / 8) * (uint32_t)Kh;
+    const bool whole = (ks + 1) * 8 <= nblk;  // else the last stage, of four blocks
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int R0 = 32 * wave + 8 * j;
-      dma16s(p.w_codes + (wn0 + w_row(x, R0)) * Kh + kMxRowBytes * ks, w_lane + (j & 1 ? c1 : c0),
-             base + R0 * kMxRowBytes);
+    for (int j = 0; j < 8; ++j) {
+      const int blk = j & 1 ? blk0 ^ 4 : blk0;
+      const uint8_t* src = wb + ((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)w_off, j) << 4);
+      const uint32_t to = base + (64 * wave + 8 * j) * kMxRowBytes;
+      if (whole) dma16s(src, w_lane + 16 * blk, to);
+      else dma16(blk < 4 ? src + w_lane + 16 * blk : pad, to);
     }
-    for (int j = 0; j < x.wb; ++j) {
-      const int R0 = 8 * (x.wb * wave + j);
-      const uint8_t* src = p.a_codes + (uint64_t)(uint32_t)a_row(x, parity, R0 + ln / 8) * (uint32_t)Kh;
-      dma16(src + kMxRowBytes * ks + ((x.wb * wave + j) & 1 ? c1 : c0), base + kMxACodes + R0 * kMxRowBytes);
+    const uint8_t* const ab = p.a_codes + kMxRowBytes * ks;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if (j < 2 * x.wb) {
+        const int blk = j & 1 ? blk0 ^ 4 : blk0;
+        const uint8_t* src = ab + 16 * blk + (uint64_t)a_off[j] * 16;
+        dma16(whole || blk < 4 ? src : pad, base + kMxACodes + 8 * (2 * x.wb * wave + j) * kMxRowBytes);
+      }
     }
     if (ks & 1) return;
-    const uint32_t sbase = lds_addr(s_mx + kMxScales + (scale_issued & 1) * kMxScaleBuf);
-    ++scale_issued;
-    // waves 0-3: scales of 64 weight rows each; the next wb waves: of 64 token rows each
-    if (wave >= 4 + x.wb) return;
-    const int R0 = 64 * (wave & 3);
-    const uint32_t to = sbase + (wave < 4 ? 0 : kMxAScales) + 16 * R0;
+    // the scales of 64 weight rows, and of 64 token rows
+    const uint32_t to = lds_addr(s_mx + kMxScales + sslot * kMxScaleBuf) + 16 * 64 * wave;
+    const uint8_t* const ws = p.w_scales + wn0 * Ks + 8 * ks;
+    const uint8_t* const as = p.a_scales + 8 * ks;
     if (wide_scales) {
-      const uint8_t* src = wave < 4
-                               ? p.w_scales + wn0 * Ks + (uint64_t)(uint32_t)w_row(x, R0 + ln) * (uint32_t)Ks
-                               : p.a_scales + (uint64_t)(uint32_t)a_row(x, parity, R0 + ln) * (uint32_t)Ks;
-      dma16(src + 8 * ks, to);
+      dma16(ws + (uint64_t)ws_off * 4, to);
+      if (wave < x.wb) dma16(as + (uint64_t)as_off * 4, to + kMxAScales);
     } else {
-      // K not a multiple of 512: words, 16 rows a load; a word beyond K is replaced by the first
-      const int word = ks * 2 + (ln & 3);
-      const uint32_t off = 4u * (4 * word < nblk ? word : ks * 2);
+      // K not a multiple of 512: words, 16 rows a load
+      const int word = ln & 3;
+      const bool in = 4 * (ks * 2 + word) < nblk;
+#pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const int R = R0 + 16 * j + ln / 4;
-        const uint8_t* src = wave < 4 ? p.w_scales + wn0 * Ks + (uint64_t)(uint32_t)w_row(x, R) * (uint32_t)Ks
-                                      : p.a_scales + (uint64_t)(uint32_t)a_row(x, parity, R) * (uint32_t)Ks;
-        dma4(src + off, to + 256 * j);
+        const uint64_t wo = (uint64_t)(uint32_t)__shfl((int)ws_off, 16 * j + ln / 4, kWave) * 4 + 4 * word;
+        const uint64_t ao = (uint64_t)(uint32_t)__shfl((int)as_off, 16 * j + ln / 4, kWave) * 4 + 4 * word;
+        dma4(in ? ws + wo : pad + 16, to + 256 * j);
+        if (wave < x.wb) dma4(in ? as + ao : pad + 16, to + kMxAScales + 256 * j);
       }
     }
   };
@@ -489,15 +512,15 @@ __global__ __launch_bounds__(kMxThreads, 1) void mx_tile_kernel(MxGemmArgs p) {
   int64_t t = (blockIdx.x % 8) * (kMxGrid / 8) + blockIdx.x / 8;
   if (t >= total) return;  // the whole workgroup
   MxTile cur = find(t), nxt = cur;
-  int parity = 0;  // of cur's rows in s_row
-  fetch_rows(cur, parity);
+  fetch_rows(cur);
   wait_vmcnt<0>();
   mx_barrier();
-  issue(cur, parity, 0);
+  set_loads(cur);
+  issue(cur, 0);
   int stage = 0, sstage = 0;
   bool first = true;
 
-  const auto run_tile = [&](auto wb_tag) {
+  const auto run_tile = [&](auto wb_tag) __attribute__((always_inline)) {
     constexpr int WB = decltype(wb_tag)::value;
     constexpr int WM = WB, WN = kMxWaves / WM;
     const int wm = wave / WN, wn = wave % WN;
@@ -509,7 +532,6 @@ __global__ __launch_bounds__(kMxThreads, 1) void mx_tile_kernel(MxGemmArgs p) {
       for (int f = 0; f < WB; ++f)
 #pragma unroll
         for (int q = 0; q < 16; ++q) acc[i][f][q] = 0.f;
-    const int swz = mx_swz(r);  // of rows 32 i + r too
     for (int ks = 0; ks < nks; ++ks) {
       // A tile's first stage was waited for before the last tile's stores were issued.
       if (ks > 0 || first) __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0) lgkmcnt(0)
@@ -517,14 +539,18 @@ __global__ __launch_bounds__(kMxThreads, 1) void mx_tile_kernel(MxGemmArgs p) {
       mx_barrier();
       if (ks == 0 && more) {
         nxt = find(t + kMxGrid);
-        fetch_rows(nxt, parity ^ 1);
+        fetch_rows(nxt);
         if (nks == 1) {  // no later stage waits for these rows
           wait_vmcnt<0>();
           mx_barrier();
         }
       }
-      if (ks + 1 < nks) issue(cur, parity, ks + 1);
-      else if (more) issue(nxt, parity ^ 1, 0);
+      const bool last = ks + 1 == nks;
+      if (last && more) set_loads(nxt);
+      if (!last || more) issue(last ? nxt : cur, last ? 0 : ks + 1);
+      int ln = lane;
+      asm volatile("" : "+v"(ln));  // a few instructions a stage instead of registers
+      const int r = ln & 31, h = ln >> 5, swz = mx_swz(r);  // (of rows 32 i + r too)
       const uint8_t* st = s_mx + (stage & 1) * kMxStage;
       const uint8_t* ss = s_mx + kMxScales + (sstage & 1) * kMxScaleBuf + 8 * (ks & 1) + 4 * h;
       const uint8_t* wp = st + (wn * WB * 32 + r) * kMxRowBytes;
@@ -535,18 +561,11 @@ __global__ __launch_bounds__(kMxThreads, 1) void mx_tile_kernel(MxGemmArgs p) {
 #pragma unroll
       for (int i = 0; i < 2; ++i)
         asc[i] = *reinterpret_cast<const uint32_t*>(ss + kMxAScales + (wm * 64 + 32 * i + r) * 16);
-      const bool beyond = (ks + 1) * 8 > nblk && h == 1;  // blocks 4 .. 7 of a stage that has only four
-      if ((ks + 1) * 8 > nblk && h == 1) {
-#pragma unroll
-        for (int f = 0; f < WB; ++f) wsc[f] = 0x7F7F7F7Fu;
-        asc[0] = asc[1] = 0x7F7F7F7Fu;
-      }
       const auto read_w = [&](int f, int s) {
         return *reinterpret_cast<const u32x4*>(wp + f * 32 * kMxRowBytes + 16 * ((4 * h + s) ^ swz));
       };
       const auto read_a = [&](int i, int s) {
-        u32x4 v = *reinterpret_cast<const u32x4*>(ap + i * 32 * kMxRowBytes + 16 * ((4 * h + s) ^ swz));
-        return beyond ? u32x4{0u, 0u, 0u, 0u} : v;
+        return *reinterpret_cast<const u32x4*>(ap + i * 32 * kMxRowBytes + 16 * ((4 * h + s) ^ swz));
       };
       u32x4 w[2][WB], a[2][2];
 #pragma unroll
@@ -561,10 +580,12 @@ __global__ __launch_bounds__(kMxThreads, 1) void mx_tile_kernel(MxGemmArgs p) {
 #pragma unroll
           for (int i = 0; i < 2; ++i) a[(S + 1) & 1][i] = read_a(i, S + 1);
         }
+        __builtin_amdgcn_sched_barrier(0);  // the next step's reads before this step's products
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
           for (int f = 0; f < WB; ++f) acc[i][f] = mx_mfma32<S>(w[S & 1][f], a[S & 1][i], acc[i][f], wsc[f], asc[i]);
+        __builtin_amdgcn_sched_barrier(0);
       };
       step(IntTag<0>{});
       step(IntTag<1>{});
@@ -576,43 +597,49 @@ __global__ __launch_bounds__(kMxThreads, 1) void mx_tile_kernel(MxGemmArgs p) {
     if (more) wait_vmcnt<0>();  // the next tile's first stage, ahead of the stores
 
     // Accumulator q of block (i, f): weight row 32 f + 8 (q / 4) + 4 h + q % 4 of the wave, token row 32 i + r.
-    uint16_t* out = static_cast<uint16_t*>(p.out);
+    // The wave's 32 token rows of a block go through its eighth of the slot that the tile's last stage was
+    // read from (the barrier: by everyone), so that the rows are stored in 16-byte pieces that follow each
+    // other: with the accumulators' own 8-byte pieces a 256 x 256 tile took 20 us to store.
+    mx_barrier();
+    int ln = lane;
+    asm volatile("" : "+v"(ln));  // addresses are computed here, not held through the stages
+    constexpr int kRow = (kL1 ? 32 : 64) * WB, kPieces = kRow / 16;  // bytes of a wave's output row
+    uint8_t* const o_lds = s_mx + ((stage + 1) & 1) * kMxStage + wave * (kMxStage / kMxWaves);
+    const auto put = [&](int piece, u32x2 v) {  // 4 columns: half h of a 16-byte piece of row r
+      *reinterpret_cast<u32x2*>(o_lds + (ln & 31) * kRow + 16 * (piece ^ (ln & (kPieces - 1))) + 8 * (ln >> 5)) = v;
+    };
+    const int c0 = cur.nt * cols + wn * kRow / 2;
+    const auto store_rows = [&](auto i_tag) __attribute__((always_inline)) {
+      constexpr int i = decltype(i_tag)::value;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int R = wm * 64 + 32 * i + r;
-      if (R >= cur.left) continue;
-      uint16_t* o = out + (cur.row0 + R) * (int64_t)p.N;
-      if constexpr (kL1) {
-        const int c0 = cur.nt * cols + wn * 16 * WB;
+      for (int f = 0; f < (kL1 ? (WB + 1) / 2 : WB); ++f)
 #pragma unroll
-        for (int f = 0; f < (WB + 1) / 2; ++f)
+        for (int q4 = 0; q4 < (kL1 && WB == 1 ? 2 : 4); ++q4) {
+          uint32_t b[4];
 #pragma unroll
-          for (int q4 = 0; q4 < (WB == 1 ? 2 : 4); ++q4) {
-            const int c = c0 + 32 * f + 8 * q4 + 4 * h;
-            if (c >= p.N) continue;
-            uint32_t b[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const float gt = acc[i][f][4 * q4 + j];
+          for (int j = 0; j < 4; ++j) {
+            const float z = acc[i][f][4 * q4 + j];
+            if constexpr (kL1) {
               const float up = WB == 1 ? acc[i][0][(4 * q4 + j + 8) & 15] : acc[i][(f + WB / 2) % WB][4 * q4 + j];
-              b[j] = f32_to_bf16_any(mx_silu(gt) * up);
+              b[j] = f32_to_bf16_any(mx_silu(z) * up);
+            } else {
+              b[j] = f32_to_bf16_any(z);
             }
-            *reinterpret_cast<u32x2*>(o + c) = u32x2{b[0] | b[1] << 16, b[2] | b[3] << 16};
           }
-      } else {
+          put(4 * f + q4, u32x2{b[0] | b[1] << 16, b[2] | b[3] << 16});
+        }
 #pragma unroll
-        for (int f = 0; f < WB; ++f)
-#pragma unroll
-          for (int q4 = 0; q4 < 4; ++q4) {
-            const int c = cur.nt * cols + (wn * WB + f) * 32 + 8 * q4 + 4 * h;
-            if (c >= p.N) continue;
-            uint32_t b[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) b[j] = f32_to_bf16_any(acc[i][f][4 * q4 + j]);
-            *reinterpret_cast<u32x2*>(o + c) = u32x2{b[0] | b[1] << 16, b[2] | b[3] << 16};
-          }
+      for (int k = 0; k < kPieces / 2; ++k) {
+        const int rr = k * (kWave / kPieces) + ln / kPieces, piece = ln % kPieces;
+        const int R = wm * 64 + 32 * i + rr, c = c0 + 8 * piece;
+        const u32x4 v = *reinterpret_cast<const u32x4*>(o_lds + rr * kRow + 16 * (piece ^ (rr & (kPieces - 1))));
+        if (R < cur.left && c < p.N)
+          __builtin_nontemporal_store(
+              v, reinterpret_cast<u32x4*>(static_cast<uint16_t*>(p.out) + (cur.row0 + R) * (int64_t)p.N + c));
       }
-    }
+    };
+    store_rows(IntTag<0>{});
+    store_rows(IntTag<1>{});
     first = false;
   };
   for (; t < total; t += kMxGrid) {
@@ -620,7 +647,6 @@ __global__ __launch_bounds__(kMxThreads, 1) void mx_tile_kernel(MxGemmArgs p) {
     else if (cur.wb == 2) run_tile(IntTag<2>{});
     else run_tile(IntTag<1>{});
     cur = nxt;
-    parity ^= 1;
   }
 }
 
@@ -669,7 +695,7 @@ static hipError_t launch_mx(const MxGemmArgs& a, const MxSmallPlan& plan, bool s
     err = mx_allow_lds(mx_tile_kernel<kL1>, tile_done);
     if (err != hipSuccess) return err;
     hipLaunchKernelGGL(mx_tile_kernel<kL1>, dim3(kMxGrid), dim3(kMxThreads),
-                       kMxTables + sizeof(int) * ((size_t)2 * kMxBm + a.E + 1), stream, a);
+                       kMxTables + sizeof(int) * ((size_t)kMxBm + a.E + 1), stream, a);
     err = hipGetLastError();
   }
   return err;
