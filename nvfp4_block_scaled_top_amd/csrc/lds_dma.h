@@ -27,13 +27,22 @@ __device__ __forceinline__ void dma16nt(const uint8_t* src, uint32_t lds) {
   lds = __builtin_amdgcn_readfirstlane(lds);
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off nt" ::"s"(lds), "v"(src) : "memory", "m0");
 }
-// The same from a wave-uniform base and a 32-bit lane offset.
+// The same from a wave-uniform base and a 32-bit lane offset, without and with the non-temporal hint.
+__device__ __forceinline__ uint64_t scalar_addr(const uint8_t* base) {
+  const uint64_t b = reinterpret_cast<uint64_t>(base);
+  return (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)b) |
+         (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(b >> 32)) << 32;
+}
 __device__ __forceinline__ void dma16s(const uint8_t* base, uint32_t off, uint32_t lds) {
   lds = __builtin_amdgcn_readfirstlane(lds);
-  const uint64_t b = reinterpret_cast<uint64_t>(base);
-  const uint64_t sb = (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)b) |
-                      (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(b >> 32)) << 32;
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(sb)
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off),
+               "s"(scalar_addr(base))
+               : "memory", "m0");
+}
+__device__ __forceinline__ void dma16snt(const uint8_t* base, uint32_t off, uint32_t lds) {
+  lds = __builtin_amdgcn_readfirstlane(lds);
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2 nt" ::"s"(lds), "v"(off),
+               "s"(scalar_addr(base))
                : "memory", "m0");
 }
 __device__ __forceinline__ void dma4(const uint8_t* src, uint32_t lds) {

@@ -58,6 +58,12 @@ __device__ __forceinline__ int mx_count(const MxGemmArgs& p, int e) { return p.c
 //
 // At the end of a group the waves leave their partial sums in LDS (two buffers, by the group's parity) and
 // one of them adds the four in wave order and stores.
+//
+// Where the token rows of the whole K fit LDS four times beside the rings (K up to 2048), K is not split:
+// every wave takes groups of its own and keeps its own copy of the token rows, and nothing is shared
+// or waited for.  With K = 2048 split in four a wave has one slot between two barriers: the down projection
+// of a 512-token prompt (384 experts, 7168 x 2048) took 814 us, and takes 632 (4.8 TB/s) without the split; with
+// K = 7168 the split spreads 16 rows' 61 KB over the four waves, which LDS would not hold four times.
 // ============================================================================================
 constexpr int kMxSmallRows = 16;
 constexpr int kMxSplit = 4;                        // waves, K split
@@ -112,7 +118,7 @@ __device__ __forceinline__ void mx_seek(const MxGemmArgs& p, int e0, int mrows, 
   }
 }
 
-template <bool kL1>
+template <bool kL1, bool kSplit>
 __global__ __launch_bounds__(kMxSplit* kWave, 1) void mx_small_kernel(MxGemmArgs p, int slots, int mrows) {
   extern __shared__ __attribute__((aligned(16))) uint8_t s_mx[];
   const int lane = lane_id(), r = lane & 15, g = lane >> 4;
@@ -120,14 +126,14 @@ __global__ __launch_bounds__(kMxSplit* kWave, 1) void mx_small_kernel(MxGemmArgs
   const int nch = (p.K + kMxChunk - 1) / kMxChunk, nblk = p.K / 32;
   const int64_t Kh = p.K / 2, Ks = p.K / 32;
   const int a_chunk = mrows * (kMxChunk / 2 + kMxChunk / 32);  // LDS bytes of a chunk of the token rows
-  uint8_t* const s_a = s_mx;
+  uint8_t* const s_a = s_mx + (kSplit ? 0 : wave * nch * a_chunk);
   f32x4* const s_red = reinterpret_cast<f32x4*>(s_mx + nch * a_chunk);
-  uint8_t* const s_ring = s_mx + nch * a_chunk + kMxRed + wave * slots * kMxSlot;
-  const int c0 = wave * nch / kMxSplit, c1 = (wave + 1) * nch / kMxSplit;  // this wave's chunks
+  uint8_t* const s_ring = s_mx + (kSplit ? nch * a_chunk + kMxRed : kMxSplit * nch * a_chunk) + wave * slots * kMxSlot;
+  const int c0 = kSplit ? wave * nch / kMxSplit : 0, c1 = kSplit ? (wave + 1) * nch / kMxSplit : nch;  // this wave's chunks
   constexpr int unit = kL1 ? 8 : 16;  // output columns of a group
   const int nt = p.N / unit;
 
-  // This workgroup's groups [gb, ge); XCD b % 8 takes one contiguous eighth.
+  // The groups [gb, ge) of this workgroup, or of this wave; XCD b % 8 takes one contiguous eighth.
   int64_t tiles = 0;
   if (p.counts == nullptr) {
     tiles = (p.M + mrows - 1) / mrows;
@@ -137,9 +143,10 @@ __global__ __launch_bounds__(kMxSplit* kWave, 1) void mx_small_kernel(MxGemmArgs
     tiles = wave_sum_i32(mine);
   }
   const int64_t groups = tiles * nt;
-  const int64_t part = (blockIdx.x % 8) * (kMxGrid / 8) + blockIdx.x / 8;
-  const int64_t gb = part * groups / kMxGrid, ge = (part + 1) * groups / kMxGrid;
-  if (gb >= ge) return;  // the whole workgroup
+  const int64_t wg = (blockIdx.x % 8) * (kMxGrid / 8) + blockIdx.x / 8;
+  const int64_t part = kSplit ? wg : wg * kMxSplit + wave, parts = kSplit ? kMxGrid : kMxGrid * kMxSplit;
+  const int64_t gb = part * groups / parts, ge = (part + 1) * groups / parts;
+  if (gb >= ge) return;  // with the split, the whole workgroup
 
   MxPlace cur;  // of the group that is computed
   {
@@ -272,14 +279,19 @@ __global__ __launch_bounds__(kMxSplit* kWave, 1) void mx_small_kernel(MxGemmArgs
       acc = mx_mfma16<2>(wv[2], av[2], acc, wsc, asc);
       acc = mx_mfma16<3>(wv[3], av[3], acc, wsc, asc);
     }
-    f32x4* const red = s_red + (gi & 1) * kMxSplit * kWave;
-    red[wave * kWave + lane] = acc;
-    __builtin_amdgcn_s_waitcnt(0xC07F);  // the partial sums are written; weight loads stay in flight
-    mx_barrier();
-    if (wave == (int)(gi % kMxSplit)) {
-      f32x4 z = red[lane];
+    f32x4 z = acc;
+    if constexpr (kSplit) {
+      f32x4* const red = s_red + (gi & 1) * kMxSplit * kWave;
+      red[wave * kWave + lane] = acc;
+      __builtin_amdgcn_s_waitcnt(0xC07F);  // the partial sums are written; weight loads stay in flight
+      mx_barrier();
+      if (wave == (int)(gi % kMxSplit)) {
+        z = red[lane];
 #pragma unroll
-      for (int k = 1; k < kMxSplit; ++k) z += red[k * kWave + lane];
+        for (int k = 1; k < kMxSplit; ++k) z += red[k * kWave + lane];
+      }
+    }
+    if (!kSplit || wave == (int)(gi % kMxSplit)) {
       // lane: token row r of the m-tile, weight rows 4g .. 4g+3
       if (r < left) {
         uint16_t* out = static_cast<uint16_t*>(p.out) + (row0 + r) * (int64_t)p.N;
@@ -347,6 +359,7 @@ __device__ __forceinline__ constexpr int mx_swz(int R) { return (R >> 1) & 7; }
 // One output tile: BM = 64 * wb token rows from row0 on (left of them real), n-tile nt.
 struct MxTile {
   int e, nt, wb, left;
+  bool once;  // the expert's only m-tile: its weights are read once
   int64_t row0;
 };
 
@@ -409,6 +422,7 @@ __global__ __launch_bounds__(kMxThreads, 1) void mx_tile_kernel(MxGemmArgs p) {
     x.nt = in / width;
     x.left = __builtin_amdgcn_readfirstlane(mx_count(p, e)) - mt * kMxBm;
     x.wb = x.left > 128 ? 4 : x.left > 64 ? 2 : 1;
+    x.once = mts == 1;
     x.row0 = (int64_t)(p.padded_offsets ? __builtin_amdgcn_readfirstlane(p.padded_offsets[e]) : 0) + (int64_t)mt * kMxBm;
     return x;
   };
@@ -474,7 +488,10 @@ __global__ __launch_bounds__(kMxThreads, 1) void mx_tile_kernel(MxGemmArgs p) {
       const int blk = j & 1 ? blk0 ^ 4 : blk0;
       const uint8_t* src = wb + ((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)w_off, j) << 4);
       const uint32_t to = base + (64 * wave + 8 * j) * kMxRowBytes;
-      if (whole) dma16s(src, w_lane + 16 * blk, to);
+      // Weights read once bypass the caches: 96 experts of 100 rows (2048 -> 7168) take 202 us instead of
+      // 217; weights that the m-tiles of an expert share do not (16381 x 4096 x 7168: 321 us instead of 308).
+      if (whole && x.once) dma16snt(src, w_lane + 16 * blk, to);
+      else if (whole) dma16s(src, w_lane + 16 * blk, to);
       else dma16(blk < 4 ? src + w_lane + 16 * blk : pad, to);
     }
     const uint8_t* const ab = p.a_codes + kMxRowBytes * ks;
@@ -662,32 +679,37 @@ static hipError_t mx_allow_lds(F* kernel, std::atomic<bool> (&done)[kMxDevices])
   return err;
 }
 
-// Token rows of the small kernel's m-tiles and its ring slots for this K: 16 rows, or 8 or 4 where 16 (or
-// 8) rows of K elements would leave fewer than 4 slots.  0 slots: K is too long for the small kernel.
+// How the small kernel runs for this K: split or not; token rows of its m-tiles, 16, or 8 or 4 where 16
+// (or 8) rows of K elements would leave fewer than 4 ring slots a wave; slots.  0 slots: K is too long for it.
 struct MxSmallPlan {
+  bool split;
   int mrows, slots;
   size_t lds;
 };
 static MxSmallPlan mx_small_plan(int K) {
   const int64_t nch = (K + kMxChunk - 1) / kMxChunk;
-  for (int mrows = kMxSmallRows; mrows >= 4; mrows /= 2) {
-    const int64_t fixed = nch * mrows * (kMxChunk / 2 + kMxChunk / 32) + kMxRed;
+  const auto plan = [&](bool split, int mrows) -> MxSmallPlan {
+    const int64_t rows = nch * mrows * (kMxChunk / 2 + kMxChunk / 32);
+    const int64_t fixed = split ? rows + kMxRed : kMxSplit * rows;
     int64_t slots = (kMxLds - fixed) / (kMxSplit * kMxSlot);
     if (slots > kMxMaxSlots) slots = kMxMaxSlots;
-    if (fixed < kMxLds && slots >= 4) return {mrows, (int)slots, (size_t)(fixed + kMxSplit * slots * kMxSlot)};
-  }
-  return {0, 0, 0};
+    if (fixed >= kMxLds || slots < 4) return {split, 0, 0, 0};
+    return {split, mrows, (int)slots, (size_t)(fixed + kMxSplit * slots * kMxSlot)};
+  };
+  MxSmallPlan p = plan(false, kMxSmallRows);
+  for (int mrows = kMxSmallRows; p.slots == 0 && mrows >= 4; mrows /= 2) p = plan(true, mrows);
+  return p;
 }
 
 template <bool kL1>
 static hipError_t launch_mx(const MxGemmArgs& a, const MxSmallPlan& plan, bool small, bool large, hipStream_t stream) {
-  static std::atomic<bool> small_done[kMxDevices], tile_done[kMxDevices];
+  static std::atomic<bool> whole_done[kMxDevices], split_done[kMxDevices], tile_done[kMxDevices];
   hipError_t err = hipSuccess;
   if (small) {
-    err = mx_allow_lds(mx_small_kernel<kL1>, small_done);
+    const auto kernel = plan.split ? mx_small_kernel<kL1, true> : mx_small_kernel<kL1, false>;
+    err = mx_allow_lds(kernel, plan.split ? split_done : whole_done);
     if (err != hipSuccess) return err;
-    hipLaunchKernelGGL(mx_small_kernel<kL1>, dim3(kMxGrid), dim3(kMxSplit * kWave), plan.lds, stream, a, plan.slots,
-                       plan.mrows);
+    hipLaunchKernelGGL(kernel, dim3(kMxGrid), dim3(kMxSplit * kWave), plan.lds, stream, a, plan.slots, plan.mrows);
     err = hipGetLastError();
     if (err != hipSuccess) return err;
   }
