@@ -160,6 +160,7 @@ struct MxGemmArgs {
   void* out;                // bf16 [*, N]
   bool cover_large = false;  // the tile kernel is not launched: the small kernel takes every expert
   bool cover_small = false;  // the small kernel is not launched: the tile kernel takes every expert
+  int32_t mrows = 0;         // token rows of the small kernel's m-tiles
 };
 // max_rows: the caller's bound on an expert's rows, 0 = none.
 hipError_t launch_mx_gemm(const MxGemmArgs& a, bool l1, int64_t max_rows, hipStream_t stream);

@@ -66,6 +66,7 @@ __device__ __forceinline__ int mx_count(const MxGemmArgs& p, int e) { return p.c
 // K = 7168 the split spreads 16 rows' 61 KB over the four waves, which LDS would not hold four times.
 // ============================================================================================
 constexpr int kMxSmallRows = 16;
+constexpr int kMxBn = 256, kMxBm = 256, kMxStageK = 256;  // the tile kernel's weight rows, token rows and stage
 constexpr int kMxSplit = 4;                        // waves, K split
 constexpr int kMxChunk = 512;                      // K elements of a slot
 constexpr int kMxSlotCodes = 16 * kMxChunk / 2;
@@ -94,12 +95,52 @@ __device__ __forceinline__ f32x4 mx_mfma16(u32x4 a, u32x4 b, f32x4 c, uint32_t s
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(av, bv, c, 4, 4, S, (int)sa, S, (int)sb);
 }
 
+// Which kernel takes the experts of more than kMxSmallRows rows.  A tile costs the tile kernel the same time
+// whether the chip is full of tiles or not; the small kernel reads the weights once for every 16 rows, but
+// spreads any work over all CUs.  Measured, dense (us, tile kernel / small kernel): 64 rows x 4096 x 7168
+// 42.7 / 15.0, 256 x 4096 x 7168 61.2 / 44.5, 400 x 4096 x 7168 67.0 / 69.5, 400 x 7168 x 2048 24.9 / 32.6.
+// slots: what the small kernel would stream for them, 0.74 ns each; tiles: of the tile kernel, 256 at a
+// time, 1.45, 1.6 or 2.1 us a stage (64, 128 or 256 token rows).
+struct MxLoad {
+  int64_t slots, tiles;
+  int rows;  // the largest expert's
+};
+__host__ __device__ inline MxLoad mx_load_of(const MxGemmArgs& p, bool l1, int cnt) {
+  if (cnt <= kMxSmallRows || p.mrows == 0) return {0, 0, 0};
+  const int64_t groups = l1 ? p.N / 8 : p.N / 16, nch = (p.K + kMxChunk - 1) / kMxChunk;
+  const int64_t cols = l1 ? kMxBn / 2 : kMxBn;
+  return {(cnt + p.mrows - 1) / p.mrows * groups * nch, (cnt + kMxBm - 1) / kMxBm * ((p.N + cols - 1) / cols), cnt};
+}
+__host__ __device__ inline bool mx_small_takes_all(const MxGemmArgs& p, const MxLoad& l) {
+  const int64_t stages = (p.K + kMxStageK - 1) / kMxStageK * ((l.tiles + kMxGrid - 1) / kMxGrid);
+  return l.slots * 74 < stages * (l.rows <= 64 ? 145000 : l.rows <= 128 ? 160000 : 210000);
+}
+// The same for a grouped call, by one wave, from the counts.
+__device__ __forceinline__ bool mx_small_takes_all(const MxGemmArgs& p, bool l1) {
+  if (p.cover_large || p.cover_small) return p.cover_large;
+  MxLoad sum{0, 0, 0};
+  for (int e = lane_id(); e < p.E; e += kWave) {
+    const MxLoad l = mx_load_of(p, l1, p.counts[e]);
+    sum.slots += l.slots;
+    sum.tiles += l.tiles;
+    sum.rows = sum.rows > l.rows ? sum.rows : l.rows;
+  }
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) {
+    sum.slots += __shfl_xor(sum.slots, o, kWave);
+    sum.tiles += __shfl_xor(sum.tiles, o, kWave);
+    const int r = __shfl_xor(sum.rows, o, kWave);
+    sum.rows = sum.rows > r ? sum.rows : r;
+  }
+  return mx_small_takes_all(p, sum);
+}
+
 // A place in the list of groups: expert e of cnt rows, m-tile mt of it, 16-row weight block j.
 struct MxPlace {
   int e, cnt, mt, j;
 };
 
-__device__ __forceinline__ int mx_small_tiles(const MxGemmArgs& p, int cnt, int mrows) {
+__device__ __forceinline__ int mx_small_tiles(const MxGemmArgs& p, int cnt, int mrows) {  // p.cover_large: as decided
   return cnt <= kMxSmallRows || p.cover_large ? (cnt + mrows - 1) / mrows : 0;
 }
 
@@ -119,9 +160,10 @@ __device__ __forceinline__ void mx_seek(const MxGemmArgs& p, int e0, int mrows, 
 }
 
 template <bool kL1, bool kSplit>
-__global__ __launch_bounds__(kMxSplit* kWave, 1) void mx_small_kernel(MxGemmArgs p, int slots, int mrows) {
+__global__ __launch_bounds__(kMxSplit* kWave, 1) void mx_small_kernel(MxGemmArgs p, int slots) {
   extern __shared__ __attribute__((aligned(16))) uint8_t s_mx[];
-  const int lane = lane_id(), r = lane & 15, g = lane >> 4;
+  const int lane = lane_id(), r = lane & 15, g = lane >> 4, mrows = p.mrows;
+  if (p.counts != nullptr) p.cover_large = mx_small_takes_all(p, kL1);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int nch = (p.K + kMxChunk - 1) / kMxChunk, nblk = p.K / 32;
   const int64_t Kh = p.K / 2, Ks = p.K / 32;
@@ -342,10 +384,8 @@ __global__ __launch_bounds__(kMxSplit* kWave, 1) void mx_small_kernel(MxGemmArgs
 // columns, so both meet in one lane.
 // ============================================================================================
 constexpr int kMxWaves = 8, kMxThreads = kMxWaves * kWave;
-constexpr int kMxBn = 256;                       // weight rows of a tile
-constexpr int kMxBm = 256;                       // token rows of a full tile
 constexpr int kMxBand = 8;                       // m-tiles walked together, for L2 reuse of the weights
-constexpr int kMxStageK = 256, kMxRowBytes = kMxStageK / 2;
+constexpr int kMxRowBytes = kMxStageK / 2;
 constexpr int kMxACodes = kMxBn * kMxRowBytes;   // within a slot: the weights' codes, then the tokens'
 constexpr int kMxStage = kMxACodes + kMxBm * kMxRowBytes;
 constexpr int kMxAScales = kMxBn * 16;           // within a scale buffer
@@ -383,10 +423,11 @@ __global__ __launch_bounds__(kMxThreads, 1) void mx_tile_kernel(MxGemmArgs p) {
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), lane = lane_id();
   const bool wide_scales = K % 512 == 0;  // whole 16-byte scale pieces
   if (wave == 0) {  // exclusive prefix of the experts' m-tiles
+    const bool none = p.counts != nullptr && mx_small_takes_all(p, kL1);
     int carry = 0;
     for (int c = 0; c < E; c += kWave) {
       const int cnt = c + lane < E ? mx_count(p, c + lane) : 0;
-      int incl = cnt > kMxSmallRows || p.cover_small ? (cnt + kMxBm - 1) / kMxBm : 0;
+      int incl = !none && (cnt > kMxSmallRows || p.cover_small) ? (cnt + kMxBm - 1) / kMxBm : 0;
       const int own = incl;
 #pragma unroll
       for (int o = 1; o < kWave; o <<= 1) {
@@ -709,7 +750,7 @@ static hipError_t launch_mx(const MxGemmArgs& a, const MxSmallPlan& plan, bool s
     const auto kernel = plan.split ? mx_small_kernel<kL1, true> : mx_small_kernel<kL1, false>;
     err = mx_allow_lds(kernel, plan.split ? split_done : whole_done);
     if (err != hipSuccess) return err;
-    hipLaunchKernelGGL(kernel, dim3(kMxGrid), dim3(kMxSplit * kWave), plan.lds, stream, a, plan.slots, plan.mrows);
+    hipLaunchKernelGGL(kernel, dim3(kMxGrid), dim3(kMxSplit * kWave), plan.lds, stream, a, plan.slots);
     err = hipGetLastError();
     if (err != hipSuccess) return err;
   }
@@ -726,11 +767,15 @@ static hipError_t launch_mx(const MxGemmArgs& a, const MxSmallPlan& plan, bool s
 hipError_t launch_mx_gemm(const MxGemmArgs& a0, bool l1, int64_t max_rows, hipStream_t stream) {
   MxGemmArgs a = a0;
   const MxSmallPlan plan = mx_small_plan(a.K);
-  // A dense call knows its rows.  A grouped one launches both kernels unless the caller's bound says
-  // that no expert has more than the small kernel's rows; it then covers every expert, should the
-  // bound be wrong.  With a K beyond the small kernel's the tile kernel takes everything.
-  bool small = a.counts != nullptr || a.M <= kMxSmallRows;
-  bool large = a.counts != nullptr ? !(max_rows > 0 && max_rows <= kMxSmallRows) : a.M > kMxSmallRows;
+  a.mrows = plan.mrows;
+  // A dense call knows its rows.  A grouped one launches both kernels, which decide from the counts, unless
+  // the caller's bound says that no expert has more than the small kernel's rows; it then covers every
+  // expert, should the bound be wrong.  With a K beyond the small kernel's the tile kernel takes everything.
+  bool small = true, large = !(max_rows > 0 && max_rows <= kMxSmallRows);
+  if (a.counts == nullptr) {
+    small = a.M <= kMxSmallRows || mx_small_takes_all(a, mx_load_of(a, l1, (int)a.M));
+    large = !small;
+  }
   if (plan.slots == 0) {
     small = false;
     large = true;

@@ -144,6 +144,10 @@ SHAPES = [  # M, N, K
     (33, 128, 128), (64, 80, 2176), (100, 4096, 512), (129, 528, 1152), (255, 256, 256), (256, 256, 512),
     (257, 1040, 896), (513, 2048, 1024), (1000, 304, 2048), (8, 4096, 16384),
     (13, 48, 9088), (9, 32, 20480), (3, 16, 40448), (5, 32, 40576),  # long reductions, few rows
+    # enough tiles for the tile kernel: last rows of each tile height, column edges, K of whole and half
+    # stages, with and without 16-byte scale pieces, of one stage and of two (with tiles beyond one a CU)
+    (1500, 1040, 896), (1400, 1072, 1152), (2060, 784, 640), (1537, 1040, 1024), (1500, 1040, 256),
+    (4200, 4112, 128), (4161, 4112, 384), (4353, 4112, 512),
 ]
 
 
@@ -161,7 +165,8 @@ def test_linear(M, N, K):
 
 @pytest.mark.parametrize("M,N,K", [(0, 32, 128), (1, 16, 128), (1, 2048, 7168), (7, 48, 384), (16, 128, 1024),
                                    (31, 144, 640), (64, 2048, 256), (130, 272, 1152), (257, 512, 2048),
-                                   (520, 1040, 256)])
+                                   (520, 1040, 256), (1500, 528, 896), (1400, 560, 1152), (2060, 400, 512),
+                                   (4200, 2064, 128), (4161, 2064, 384)])
 def test_gate_up_silu(M, N, K):
     rng = np.random.default_rng(M + N + K + 1)
     (ac, as_), (wc, ws) = quantized(rng, M, K, 0.5), quantized(rng, 2 * N, K, 0.1)
@@ -172,11 +177,11 @@ def test_gate_up_silu(M, N, K):
     accept_silu(bf16_np(out[:M]), *X.gate_up(X.decode(ac, as_), X.decode(wc, ws)), K)
 
 
-@pytest.mark.parametrize("M", [3, 40, 200, 300])
-def test_linear_random_codes_and_scales(M):
+@pytest.mark.parametrize("M,N", [(3, 64), (40, 64), (300, 64), (1500, 1040)])
+def test_linear_random_codes_and_scales(M, N):
     """Every code, scales over sixty binades, zero blocks and zero rows."""
     rng = np.random.default_rng(M)
-    N, K = 64, 768
+    K = 768
     ac, wc = (rng.integers(0, 256, (n, K // 2)).astype(np.uint8) for n in (M, N))
     as_, ws = (rng.integers(97, 157, (n, K // 32)).astype(np.uint8) for n in (M, N))
     ac[1] = 0
@@ -188,10 +193,10 @@ def test_linear_random_codes_and_scales(M):
     accept(bf16_np(out), ref, zabs, K)
 
 
-@pytest.mark.parametrize("M", [2, 20, 300])
-def test_linear_nan_scales_reach_their_outputs_only(M):
+@pytest.mark.parametrize("M,N", [(2, 48), (20, 48), (300, 48), (1500, 1040)])
+def test_linear_nan_scales_reach_their_outputs_only(M, N):
     rng = np.random.default_rng(M + 9)
-    N, K = 48, 640
+    K = 640
     (ac, as_), (wc, ws) = quantized(rng, M, K, 1.0), quantized(rng, N, K, 1.0)
     as_[1, K // 32 - 1] = 255
     ws[17, 0] = 255
@@ -246,6 +251,13 @@ EXPERTS = [  # rows by expert, P, H, I
     ([2] * 48, 1, 1024, 256),
     ([0] * 500 + [7, 600, 0, 20], 1, 256, 256),
     ([16] * 3 + [15] * 3 + [31, 32], 1, 640, 512),
+    # enough tiles for the tile kernel beside small experts: every tile height, half stages, several
+    # tiles a workgroup with one and two stages
+    ([300, 0, 70, 20, 500, 129, 17, 260, 16, 190, 3], 8, 1152, 640),
+    ([1100, 33, 0, 450], 1, 1408, 896),
+    ([1100, 33, 0, 450], 16, 512, 720),
+    ([2100, 0, 40, 2060], 1, 256, 2064),
+    ([2100, 0, 40, 2060], 1, 384, 2064),
 ]
 
 
