@@ -77,29 +77,44 @@ __device__ __forceinline__ Mx8 mx_quant8(u32x4 a, u32x4 b) {  // float32
   return {w, sc};
 }
 
-// n8 = elements / 8; rows with row_valid[r] < 0 get zero codes and scales and are not read.
-template <bool kF32>
+// n8 = elements / 8; rows with row_valid[r] < 0 get zero codes and scales and are not read.  kItems strided
+// items a thread, all loaded before the first is used.
+template <bool kF32, int kItems>
 __global__ __launch_bounds__(kMxThreads) void mx_quant_kernel(const void* __restrict__ x, int64_t n8, int64_t cols8,
                                                               const int32_t* __restrict__ row_valid,
                                                               uint32_t* __restrict__ codes,
                                                               uint8_t* __restrict__ scales) {
-  const int64_t step = (int64_t)gridDim.x * kMxThreads;
-  // the four lanes of a block hold the same block in every iteration (n8 and step are multiples of 4)
-  for (int64_t i = (int64_t)blockIdx.x * kMxThreads + threadIdx.x; i < n8; i += step) {
-    Mx8 q{0u, 0u};
-    if (row_valid == nullptr || row_valid[i / cols8] >= 0) {
-      const u32x4* src = static_cast<const u32x4*>(x) + (kF32 ? 2 * i : i);
-      if constexpr (kF32) q = mx_quant8(src[0], src[1]);
-      else q = mx_quant8(src[0]);
+  constexpr int kV = kF32 ? 2 : 1;
+  const int64_t step = (int64_t)gridDim.x * kMxThreads, i0 = (int64_t)blockIdx.x * kMxThreads + threadIdx.x;
+  u32x4 v[kItems][kV];
+  bool ok[kItems];
+  // the four lanes of a block hold the same block (n8 and step are multiples of 4)
+#pragma unroll
+  for (int k = 0; k < kItems; ++k) {
+    const int64_t i = i0 + k * step;
+    ok[k] = i < n8 && (row_valid == nullptr || row_valid[i / cols8] >= 0);
+    const u32x4* src = static_cast<const u32x4*>(x) + kV * i;
+#pragma unroll
+    for (int j = 0; j < kV; ++j) v[k][j] = ok[k] ? __builtin_nontemporal_load(src + j) : u32x4{0u, 0u, 0u, 0u};
+  }
+#pragma unroll
+  for (int k = 0; k < kItems; ++k) {
+    const int64_t i = i0 + k * step;
+    Mx8 q;
+    if constexpr (kF32) q = mx_quant8(v[k][0], v[k][1]);
+    else q = mx_quant8(v[k][0]);
+    if (i < n8) {
+      codes[i] = q.codes;
+      if ((i & 3) == 0) scales[i >> 2] = (uint8_t)q.scale;
     }
-    codes[i] = q.codes;
-    if ((i & 3) == 0) scales[i >> 2] = (uint8_t)q.scale;
   }
 }
 
-static unsigned mx_grid(int64_t n8) {
-  const int64_t g = (n8 + kMxThreads - 1) / kMxThreads;
-  return (unsigned)(g > 8192 ? 8192 : g);
+// Items a thread: 4 once that still fills the chip with threads, else 1.  (49152 x 2048 bf16: 51 us with
+// one and a loop, @Q with four; 8 x 7168: 2.2 us with one.)
+constexpr int64_t kMxManyItems = (int64_t)4 * kMxThreads * 2048;
+static unsigned mx_grid(int64_t n8, int items) {
+  return (unsigned)((n8 + (int64_t)kMxThreads * items - 1) / ((int64_t)kMxThreads * items));
 }
 
 hipError_t launch_mx_quant(const void* x, int dtype, int64_t rows, int64_t cols, const int32_t* row_valid,
@@ -107,12 +122,11 @@ hipError_t launch_mx_quant(const void* x, int dtype, int64_t rows, int64_t cols,
   const int64_t n8 = rows * (cols / 8);
   if (n8 == 0) return hipSuccess;
   uint32_t* c = reinterpret_cast<uint32_t*>(codes);
-  if (dtype == MEGAMOE_DTYPE_F32)
-    hipLaunchKernelGGL(mx_quant_kernel<true>, dim3(mx_grid(n8)), dim3(kMxThreads), 0, stream, x, n8, cols / 8,
-                       row_valid, c, scales);
-  else
-    hipLaunchKernelGGL(mx_quant_kernel<false>, dim3(mx_grid(n8)), dim3(kMxThreads), 0, stream, x, n8, cols / 8,
-                       row_valid, c, scales);
+  const bool f32 = dtype == MEGAMOE_DTYPE_F32, many = n8 >= kMxManyItems;
+  const auto kernel = f32 ? (many ? mx_quant_kernel<true, 4> : mx_quant_kernel<true, 1>)
+                          : (many ? mx_quant_kernel<false, 4> : mx_quant_kernel<false, 1>);
+  hipLaunchKernelGGL(kernel, dim3(mx_grid(n8, many ? 4 : 1)), dim3(kMxThreads), 0, stream, x, n8, cols / 8, row_valid,
+                     c, scales);
   return hipGetLastError();
 }
 
@@ -132,17 +146,45 @@ __device__ __forceinline__ uint32_t mx_value_bits(uint32_t code, uint32_t scale)
   return sign | ((0x80u | man << 6) >> (1 - ex));  // subnormal: ex = 0 or -1, the shifted-out bits are zero
 }
 
-__global__ __launch_bounds__(kMxThreads) void mx_dequant_kernel(const uint32_t* __restrict__ codes,
-                                                                const uint8_t* __restrict__ scales, int64_t n8,
-                                                                u32x4* __restrict__ out) {
-  const int64_t step = (int64_t)gridDim.x * kMxThreads;
-  for (int64_t i = (int64_t)blockIdx.x * kMxThreads + threadIdx.x; i < n8; i += step) {
-    const uint32_t w = codes[i], sc = scales[i >> 2];
-    u32x4 o;
+// Inside the normal range the conversion instruction gives the same values four times as fast.
+__device__ __forceinline__ u32x4 mx_values8(uint32_t w, uint32_t sc) {
+  u32x4 o;
+  if (sc >= 2u && sc <= 251u) {
+    const float s = __uint_as_float(sc << 23);
+    const auto bits = [](bf16x2v v) {
+      uint32_t u;
+      __builtin_memcpy(&u, &v, 4);
+      return u;
+    };
+    o[0] = bits(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 0));
+    o[1] = bits(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 1));
+    o[2] = bits(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 2));
+    o[3] = bits(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 3));
+  } else {
 #pragma unroll
     for (int j = 0; j < 4; ++j)
       o[j] = mx_value_bits((w >> (8 * j)) & 15u, sc) | (mx_value_bits((w >> (8 * j + 4)) & 15u, sc) << 16);
-    out[i] = o;
+  }
+  return o;
+}
+
+template <int kItems>
+__global__ __launch_bounds__(kMxThreads) void mx_dequant_kernel(const uint32_t* __restrict__ codes,
+                                                                const uint8_t* __restrict__ scales, int64_t n8,
+                                                                u32x4* __restrict__ out) {
+  const int64_t step = (int64_t)gridDim.x * kMxThreads, i0 = (int64_t)blockIdx.x * kMxThreads + threadIdx.x;
+  uint32_t w[kItems], sc[kItems];
+#pragma unroll
+  for (int k = 0; k < kItems; ++k) {
+    const int64_t i = i0 + k * step;
+    w[k] = i < n8 ? codes[i] : 0u;
+    sc[k] = i < n8 ? scales[i >> 2] : 127u;
+  }
+#pragma unroll
+  for (int k = 0; k < kItems; ++k) {
+    const int64_t i = i0 + k * step;
+    const u32x4 o = mx_values8(w[k], sc[k]);
+    if (i < n8) __builtin_nontemporal_store(o, out + i);
   }
 }
 
@@ -150,8 +192,10 @@ hipError_t launch_mx_dequant(const uint8_t* codes, const uint8_t* scales, int64_
                              hipStream_t stream) {
   const int64_t n8 = rows * (cols / 8);
   if (n8 == 0) return hipSuccess;
-  hipLaunchKernelGGL(mx_dequant_kernel, dim3(mx_grid(n8)), dim3(kMxThreads), 0, stream,
-                     reinterpret_cast<const uint32_t*>(codes), scales, n8, static_cast<u32x4*>(out));
+  const bool many = n8 >= kMxManyItems;
+  hipLaunchKernelGGL(many ? mx_dequant_kernel<4> : mx_dequant_kernel<1>, dim3(mx_grid(n8, many ? 4 : 1)),
+                     dim3(kMxThreads), 0, stream, reinterpret_cast<const uint32_t*>(codes), scales, n8,
+                     static_cast<u32x4*>(out));
   return hipGetLastError();
 }
 

@@ -32,16 +32,76 @@ __device__ __forceinline__ float load_logit<uint16_t>(const uint16_t* p) {
   return v != v ? -__builtin_huge_valf() : fminf(v, 3.402823466e38f);
 }
 
-__device__ __forceinline__ float score_wave_max(float v) {
-#pragma unroll
-  for (int o = 32; o >= 1; o >>= 1) v = fmaxf(v, __shfl_xor(v, o, kWave));
-  return v;
+// Reductions over a wave with data-parallel-primitive moves (a few cycles a step; a shuffle through LDS
+// takes some 100): rows of 16 lanes by shifts, then lane 15 of a row to the next one and lane 31 to the upper
+// half.  Lane 63 holds the result; a lane that receives nothing receives 0, so 0 must not change it.
+template <int kCtrl>
+__device__ __forceinline__ uint32_t dpp_move(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, kCtrl, 0xF, 0xF, true);
+}
+template <typename F>
+__device__ __forceinline__ uint32_t dpp_reduce(uint32_t v, F f) {
+  v = f(v, dpp_move<0x111>(v));
+  v = f(v, dpp_move<0x112>(v));
+  v = f(v, dpp_move<0x114>(v));
+  v = f(v, dpp_move<0x118>(v));
+  v = f(v, dpp_move<0x142>(v));
+  v = f(v, dpp_move<0x143>(v));
+  return (uint32_t)__builtin_amdgcn_readlane((int)v, kWave - 1);
+}
+__device__ __forceinline__ uint32_t umax(uint32_t a, uint32_t b) { return a > b ? a : b; }
+
+template <int kCtrl>
+__device__ __forceinline__ double dpp_move(double v) {
+  const uint64_t b = __double_as_longlong(v);
+  return __longlong_as_double((long long)((uint64_t)dpp_move<kCtrl>((uint32_t)(b >> 32)) << 32 |
+                                          dpp_move<kCtrl>((uint32_t)b)));
+}
+__device__ __forceinline__ double read_lane(double v, int lane) {
+  const uint64_t b = __double_as_longlong(v);
+  return __longlong_as_double((long long)((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(b >> 32), lane) << 32 |
+                                          (uint32_t)__builtin_amdgcn_readlane((int)b, lane)));
+}
+__device__ __forceinline__ double score_wave_sum(double v) {
+  v += dpp_move<0x111>(v);
+  v += dpp_move<0x112>(v);
+  v += dpp_move<0x114>(v);
+  v += dpp_move<0x118>(v);
+  v += dpp_move<0x142>(v);
+  v += dpp_move<0x143>(v);
+  return read_lane(v, kWave - 1);
 }
 
-__device__ __forceinline__ double score_wave_sum(double v) {
-#pragma unroll
-  for (int o = 32; o >= 1; o >>= 1) v += __shfl_xor(v, o, kWave);
-  return v;
+// e^t: t = n ln 2 + r with |r| <= ln 2 / 2, the Taylor polynomial of e^r up to r^12 / 12! (its
+// remainder is below 2^-52 of e^r) and a scaling by 2^n: 18 instructions, where exp() takes some 40.
+__device__ __forceinline__ double exp_f64(double t) {
+  t = fmin(fmax(t, -800.0), 800.0);  // beyond: 0 and infinity by the scaling
+  const double n = rint(t * 1.4426950408889634);
+  double r = fma(-n, 0x1.62e42fefa39efp-1, t);  // ln 2 to 53 bits, and what is left of it
+  r = fma(-n, 0x1.abc9e3b39803fp-56, r);
+  double p = 1.0 / 479001600;
+  p = fma(p, r, 1.0 / 39916800);
+  p = fma(p, r, 1.0 / 3628800);
+  p = fma(p, r, 1.0 / 362880);
+  p = fma(p, r, 1.0 / 40320);
+  p = fma(p, r, 1.0 / 5040);
+  p = fma(p, r, 1.0 / 720);
+  p = fma(p, r, 1.0 / 120);
+  p = fma(p, r, 1.0 / 24);
+  p = fma(p, r, 1.0 / 6);
+  p = fma(p, r, 0.5);
+  p = fma(p, r, 1.0);
+  p = fma(p, r, 1.0);
+  return ldexp(p, (int)n);
+}
+
+// 1 / (1 + e^-z), the reciprocal by Newton's steps from the hardware's estimate.
+__device__ __forceinline__ double sigmoid_f64(float z) {
+  const double d = 1.0 + exp_f64(-(double)z);
+  double y = __builtin_amdgcn_rcp(d);
+  y = fma(y, fma(-d, y, 1.0), y);
+  y = fma(y, fma(-d, y, 1.0), y);
+  return z < -709.0f ? 0.0 : y;  // there d is infinite, or 1 / d below every float
 }
 
 // Unsigned key whose order is the order of the floats (-0 below +0 is not wanted: both map to +0).
@@ -65,63 +125,61 @@ __global__ __launch_bounds__(kScoreWaves* kWave) void router_scores_kernel(Route
   const T* __restrict__ row = static_cast<const T*>(p.logits) + (int64_t)t * p.E;
   const bool sigmoid = p.score == MEGAMOE_SCORE_SIGMOID;
 
+  const float kNone = -__builtin_huge_valf();
   float z[PL];
-  float m = -__builtin_huge_valf();
 #pragma unroll
   for (int i = 0; i < PL; ++i) {
     const int x = u + p.span * i;
-    const bool in = q < p.n_group && x < size;
-    z[i] = in ? load_logit<T>(row + q * size + x) : -__builtin_huge_valf();
-    m = fmaxf(m, z[i]);
+    z[i] = q < p.n_group && x < size ? load_logit<T>(row + q * size + x) : kNone;
   }
-  double s[PL];
-  double sum = 1.0;
-  if (sigmoid) {
-#pragma unroll
-    for (int i = 0; i < PL; ++i) s[i] = 1.0 / (1.0 + exp(-(double)z[i]));
-  } else {
-    m = score_wave_max(m);
-    sum = 0.0;
-#pragma unroll
-    for (int i = 0; i < PL; ++i) {
-      s[i] = z[i] > -__builtin_huge_valf() ? exp((double)z[i] - (double)m) : 0.0;
-      sum += s[i];
-    }
-    sum = score_wave_sum(sum);
-#pragma unroll
-    for (int i = 0; i < PL; ++i) s[i] = sum > 0.0 ? s[i] / sum : 0.0;
-  }
+  double m = 0.0, inv = 1.0;  // softmax: largest logit, one over the sum
   // Keys of the choices: 0 for an expert that is not available.
   uint32_t key[PL];
-#pragma unroll
-  for (int i = 0; i < PL; ++i) {
+  const auto set_key = [&](int i, float s) {
     const int x = u + p.span * i;
-    float c = (float)s[i];
+    float c = s;
     if (p.bias != nullptr && q < p.n_group && x < size) c += p.bias[q * size + x];
-    const bool ok = z[i] > -__builtin_huge_valf() && c > -__builtin_huge_valf();
-    key[i] = ok ? sort_key(c) : 0u;
+    key[i] = z[i] > kNone && c > kNone ? sort_key(c) : 0u;
+  };
+  if (sigmoid) {
+#pragma unroll
+    for (int i = 0; i < PL; ++i) set_key(i, (float)sigmoid_f64(z[i]));
+  } else {
+    uint32_t mk = 0;
+#pragma unroll
+    for (int i = 0; i < PL; ++i) mk = umax(mk, sort_key(z[i]));
+    m = (double)unsort_key(dpp_reduce(mk, umax));
+    double e[PL], sum = 0.0;
+#pragma unroll
+    for (int i = 0; i < PL; ++i) {
+      e[i] = z[i] > kNone ? exp_f64((double)z[i] - m) : 0.0;
+      sum += e[i];
+    }
+    sum = score_wave_sum(sum);
+    inv = sum > 0.0 ? 1.0 / sum : 0.0;
+#pragma unroll
+    for (int i = 0; i < PL; ++i) set_key(i, (float)(e[i] * inv));
   }
   if (p.topk_group < p.n_group) {
     uint32_t k1 = 0, k2 = 0;  // the two largest keys of the group
 #pragma unroll
     for (int i = 0; i < PL; ++i) {
       const uint32_t lo = key[i] < k1 ? key[i] : k1;
-      k1 = key[i] > k1 ? key[i] : k1;
-      k2 = lo > k2 ? lo : k2;
+      k1 = umax(key[i], k1);
+      k2 = umax(lo, k2);
     }
     for (int o = 1; o < p.span; o <<= 1) {
       const uint32_t o1 = __shfl_xor(k1, o, kWave), o2 = __shfl_xor(k2, o, kWave);
       const uint32_t lo = o1 < k1 ? o1 : k1;
-      const uint32_t hi2 = o2 > k2 ? o2 : k2;
-      k1 = o1 > k1 ? o1 : k1;
-      k2 = lo > hi2 ? lo : hi2;
+      k1 = umax(o1, k1);
+      k2 = umax(lo, umax(o2, k2));
     }
     // A group without an available expert comes after every other one.
-    float gs = k1 ? unsort_key(k1) : -__builtin_huge_valf();
+    float gs = k1 ? unsort_key(k1) : kNone;
     if (p.group_top > 1 && k2) gs += unsort_key(k2);
     int rank = 0;
     for (int g = 0; g < p.n_group; ++g) {
-      const float og = __shfl(gs, g * p.span, kWave);
+      const float og = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(gs), g * p.span));
       rank += (og > gs || (og == gs && g < q)) ? 1 : 0;
     }
     if (rank >= p.topk_group) {
@@ -129,48 +187,43 @@ __global__ __launch_bounds__(kScoreWaves* kWave) void router_scores_kernel(Route
       for (int i = 0; i < PL; ++i) key[i] = 0u;
     }
   }
-  // k rounds: the largest key, the lowest expert among equal ones; the winner's key is then cleared.
+  // k rounds: the largest key of the wave, the lowest expert that has it; its key is then cleared.  Which
+  // lanes hold the key is a lane mask for each i, so the search for the expert is scalar work.
   int my_id = -1;
-  double my_s = 0.0, total = 0.0;
   for (int r = 0; r < p.k; ++r) {
-    uint32_t bk = 0;
-    int bi = 0x7FFFFFFF;
-    double bs = 0.0;
+    uint32_t wk = key[0];
 #pragma unroll
-    for (int i = 0; i < PL; ++i) {  // ascending expert ids within the lane
-      if (key[i] > bk) {
-        bk = key[i];
-        bi = q * size + u + p.span * i;
-        bs = s[i];
-      }
-    }
-    uint32_t wk = bk;
-    int wi = bi;
-#pragma unroll
-    for (int o = 32; o >= 1; o >>= 1) {
-      const uint32_t ok = __shfl_xor(wk, o, kWave);
-      const int oi = __shfl_xor(wi, o, kWave);
-      if (ok > wk || (ok == wk && oi < wi)) {
-        wk = ok;
-        wi = oi;
-      }
-    }
+    for (int i = 1; i < PL; ++i) wk = umax(wk, key[i]);
+    wk = dpp_reduce(wk, umax);
     if (wk == 0) break;  // nothing available is left: the remaining slots stay empty
-    const uint64_t owner = __ballot(bk == wk && bi == wi);
-    const double ws = __shfl(bs, __ffsll((unsigned long long)owner) - 1, kWave);
-    total += ws;
-    if (lane == r) {
-      my_id = wi;
-      my_s = ws;
+    int win = 0x7FFFFFFF, wi = 0, wl = 0;
+#pragma unroll
+    for (int i = 0; i < PL; ++i) {
+      const uint64_t mask = __ballot(key[i] == wk);
+      if (mask) {  // expert ids ascend with the lane
+        const int l = __builtin_ctzll(mask), e = (l / p.span) * size + (l & (p.span - 1)) + p.span * i;
+        if (e < win) {
+          win = e;
+          wi = i;
+          wl = l;
+        }
+      }
     }
 #pragma unroll
     for (int i = 0; i < PL; ++i)
-      if (q * size + u + p.span * i == wi) key[i] = 0u;
+      if (i == wi && lane == wl) key[i] = 0u;
+    if (lane == r) my_id = win;
   }
+  // The winners' weights, one lane each.
+  double ws = 0.0;
+  if (my_id >= 0) {
+    const float wz = load_logit<T>(row + my_id);
+    ws = sigmoid ? sigmoid_f64(wz) : exp_f64((double)wz - m) * inv;
+  }
+  const double d = p.renormalize ? score_wave_sum(ws) : 1.0;
   if (lane < p.k) {
-    const double d = p.renormalize ? total : 1.0;
     p.ids[(int64_t)t * p.k + lane] = my_id;
-    p.weights[(int64_t)t * p.k + lane] = my_id >= 0 && d > 0.0 ? (float)(my_s * (double)p.scale / d) : 0.0f;
+    p.weights[(int64_t)t * p.k + lane] = d > 0.0 ? (float)(ws * (double)p.scale / d) : 0.0f;
   }
 }
 
@@ -209,12 +262,17 @@ hipError_t launch_router_scores(const RouterScoreArgs& a0, int dtype, hipStream_
 // float64 up to the one rounding of dz.  One wave per token, lane l holding experts l + 64 i; the
 // chosen experts' scores are computed one per lane.
 template <typename T>
-__device__ __forceinline__ void store_logit(T* p, double v);
+__device__ __forceinline__ T round_logit(double v);
 template <>
-__device__ __forceinline__ void store_logit<float>(float* p, double v) { *p = (float)v; }
+__device__ __forceinline__ float round_logit<float>(double v) { return (float)v; }
 template <>
-__device__ __forceinline__ void store_logit<uint16_t>(uint16_t* p, double v) {
-  *p = (uint16_t)f64_to_bf16_bits(v);
+__device__ __forceinline__ uint16_t round_logit<uint16_t>(double v) { return (uint16_t)f64_to_bf16_bits(v); }
+
+__device__ __forceinline__ float read_lane(float v, int lane) {
+  return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(v), lane));
+}
+__device__ __forceinline__ uint16_t read_lane(uint16_t v, int lane) {
+  return (uint16_t)__builtin_amdgcn_readlane((int)v, lane);
 }
 
 template <typename T, int PL>
@@ -235,52 +293,59 @@ __global__ __launch_bounds__(kScoreWaves* kWave) void router_scores_bwd_kernel(R
     g = id >= 0 ? (double)p.grad_weights[(int64_t)t * p.k + lane] * (double)p.scale : 0.0;
   }
   double s[PL];
-  double m = 0.0, sum = 1.0;
+  double m = 0.0, inv = 1.0;
   if (!sigmoid) {
-    float z[PL], mf = -__builtin_huge_valf();
+    const float kNone = -__builtin_huge_valf();
+    float z[PL];
+    uint32_t mk = 0;
 #pragma unroll
     for (int i = 0; i < PL; ++i) {
       const int e = lane + kWave * i;
-      z[i] = e < p.E ? load_logit<T>(row + e) : -__builtin_huge_valf();
-      mf = fmaxf(mf, z[i]);
+      z[i] = e < p.E ? load_logit<T>(row + e) : kNone;
+      mk = umax(mk, sort_key(z[i]));
     }
-    m = (double)score_wave_max(mf);
-    sum = 0.0;
+    m = (double)unsort_key(dpp_reduce(mk, umax));
+    double sum = 0.0;
 #pragma unroll
     for (int i = 0; i < PL; ++i) {
-      s[i] = z[i] > -__builtin_huge_valf() ? exp((double)z[i] - m) : 0.0;
+      s[i] = z[i] > kNone ? exp_f64((double)z[i] - m) : 0.0;
       sum += s[i];
     }
     sum = score_wave_sum(sum);
-#pragma unroll
-    for (int i = 0; i < PL; ++i) s[i] = sum > 0.0 ? s[i] / sum : 0.0;
+    inv = sum > 0.0 ? 1.0 / sum : 0.0;
   }
   double sj = 0.0;  // score of this lane's chosen expert
   if (id >= 0) {
     const float zj = load_logit<T>(row + id);
-    if (sigmoid) sj = 1.0 / (1.0 + exp(-(double)zj));
-    else sj = zj > -__builtin_huge_valf() && sum > 0.0 ? exp((double)zj - m) / sum : 0.0;
+    if (sigmoid) sj = sigmoid_f64(zj);
+    else sj = zj > -__builtin_huge_valf() ? exp_f64((double)zj - m) * inv : 0.0;
   }
   if (p.renormalize) {
     const double S = score_wave_sum(sj), gs = score_wave_sum(g * sj);
     g = S > 0.0 && id >= 0 ? (g - gs / S) / S : 0.0;
   }
   const double dot = sigmoid ? 0.0 : score_wave_sum(g * sj);
-  const double d1 = sigmoid ? g * sj * (1.0 - sj) : g;  // what slot `lane` adds to its expert
-  double acc[PL];
-#pragma unroll
-  for (int i = 0; i < PL; ++i) acc[i] = 0.0;
+  // g'_e of this lane's expert: the slots that name it, in slot order; then its gradient.
+  double ge = 0.0;
   for (int j = 0; j < p.k; ++j) {
-    const int ej = __shfl(id, j, kWave);
-    const double dj = __shfl(d1, j, kWave);
+    const double gj = read_lane(g, j);
+    ge += __builtin_amdgcn_readlane(id, j) == id ? gj : 0.0;
+  }
+  const T mine = round_logit<T>(sigmoid ? ge * sj * (1.0 - sj) : sj * (ge - dot));
+  T v[PL];
+#pragma unroll
+  for (int i = 0; i < PL; ++i) v[i] = round_logit<T>(sigmoid ? 0.0 : -(s[i] * inv * dot));
+  for (int j = 0; j < p.k; ++j) {
+    const int ej = __builtin_amdgcn_readlane(id, j);
+    const T vj = read_lane(mine, j);
 #pragma unroll
     for (int i = 0; i < PL; ++i)
-      if (lane + kWave * i == ej) acc[i] += dj;
+      if (lane + kWave * i == ej) v[i] = vj;
   }
 #pragma unroll
   for (int i = 0; i < PL; ++i) {
     const int e = lane + kWave * i;
-    if (e < p.E) store_logit<T>(out + e, sigmoid ? acc[i] : s[i] * (acc[i] - dot));
+    if (e < p.E) out[e] = v[i];
   }
 }
 
