@@ -53,7 +53,7 @@ struct RouterScoreArgs {
   float scale;
   int32_t* ids;
   float* weights;
-  int32_t span = 0;  // lanes of a wave that hold one group (set by the launcher)
+  int32_t span_log2 = 0;  // 2^span_log2 lanes of a wave hold one group (set by the launcher)
 };
 hipError_t launch_router_scores(const RouterScoreArgs& a, int dtype, hipStream_t stream);
 struct RouterScoreBwdArgs {

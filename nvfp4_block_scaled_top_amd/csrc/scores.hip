@@ -18,19 +18,9 @@ namespace megamoe {
 
 constexpr int kScoreWaves = 4;  // tokens per workgroup, one wave each
 
-// A logit as float64; NaN is taken as -inf (not available), +inf as the largest float.
-template <typename T>
-__device__ __forceinline__ float load_logit(const T* p);
-template <>
-__device__ __forceinline__ float load_logit<float>(const float* p) {
-  const float v = *p;
-  return v != v ? -__builtin_huge_valf() : fminf(v, 3.402823466e38f);
-}
-template <>
-__device__ __forceinline__ float load_logit<uint16_t>(const uint16_t* p) {
-  const float v = bf16_bits_to_f32(*p);
-  return v != v ? -__builtin_huge_valf() : fminf(v, 3.402823466e38f);
-}
+// A logit as float32; NaN is taken as -inf (not available), +inf as the largest float.
+__device__ __forceinline__ float logit_of(float v) { return v != v ? -__builtin_huge_valf() : fminf(v, 3.402823466e38f); }
+__device__ __forceinline__ float logit_of(uint16_t v) { return logit_of(bf16_bits_to_f32(v)); }
 
 // Reductions over a wave with data-parallel-primitive moves (a few cycles a step; a shuffle through LDS
 // takes some 100): rows of 16 lanes by shifts, then lane 15 of a row to the next one and lane 31 to the upper
@@ -73,34 +63,45 @@ __device__ __forceinline__ double score_wave_sum(double v) {
 }
 
 // e^t: t = n ln 2 + r with |r| <= ln 2 / 2, the Taylor polynomial of e^r up to r^12 / 12! (its
-// remainder is below 2^-52 of e^r) and a scaling by 2^n: 18 instructions, where exp() takes some 40.
-__device__ __forceinline__ double exp_f64(double t) {
+// remainder is below 2^-52 of e^r) and a scaling by 2^n: 18 instructions, where exp() takes some 40.  The
+// constants are held in scalar registers: left to itself the compiler moves each into vector registers before
+// every use, two moves a multiplication.
+struct ExpConstants {
+  double c[13], log2e, ln2_hi, ln2_lo;
+};
+__device__ __forceinline__ ExpConstants exp_constants() {
+  ExpConstants k{{1.0, 1.0, 0.5, 1.0 / 6, 1.0 / 24, 1.0 / 120, 1.0 / 720, 1.0 / 5040, 1.0 / 40320, 1.0 / 362880,
+                  1.0 / 3628800, 1.0 / 39916800, 1.0 / 479001600},
+                 1.4426950408889634,
+                 0x1.62e42fefa39efp-1,  // ln 2 to 53 bits, and what is left of it
+                 0x1.abc9e3b39803fp-56};
+#pragma unroll
+  for (int i = 3; i < 12; ++i) asm volatile("" : "+s"(k.c[i]));  // 0.5 and 1 are operands of an instruction
+  asm volatile("" : "+s"(k.log2e));
+  asm volatile("" : "+s"(k.ln2_hi));
+  asm volatile("" : "+s"(k.ln2_lo));
+  return k;
+}
+__device__ __forceinline__ double exp_f64(const ExpConstants& k, double t) {
   t = fmin(fmax(t, -800.0), 800.0);  // beyond: 0 and infinity by the scaling
-  const double n = rint(t * 1.4426950408889634);
-  double r = fma(-n, 0x1.62e42fefa39efp-1, t);  // ln 2 to 53 bits, and what is left of it
-  r = fma(-n, 0x1.abc9e3b39803fp-56, r);
-  double p = 1.0 / 479001600;
-  p = fma(p, r, 1.0 / 39916800);
-  p = fma(p, r, 1.0 / 3628800);
-  p = fma(p, r, 1.0 / 362880);
-  p = fma(p, r, 1.0 / 40320);
-  p = fma(p, r, 1.0 / 5040);
-  p = fma(p, r, 1.0 / 720);
-  p = fma(p, r, 1.0 / 120);
-  p = fma(p, r, 1.0 / 24);
-  p = fma(p, r, 1.0 / 6);
-  p = fma(p, r, 0.5);
-  p = fma(p, r, 1.0);
-  p = fma(p, r, 1.0);
+  const double n = rint(t * k.log2e);
+  double r = fma(-n, k.ln2_hi, t);
+  r = fma(-n, k.ln2_lo, r);
+  double p = k.c[12];
+#pragma unroll
+  for (int i = 11; i >= 0; --i) p = fma(p, r, k.c[i]);
   return ldexp(p, (int)n);
 }
 
-// 1 / (1 + e^-z), the reciprocal by Newton's steps from the hardware's estimate.
-__device__ __forceinline__ double sigmoid_f64(float z) {
-  const double d = 1.0 + exp_f64(-(double)z);
+// 1 / d by Newton's steps from the hardware's estimate (d normal).
+__device__ __forceinline__ double reciprocal_f64(double d) {
   double y = __builtin_amdgcn_rcp(d);
   y = fma(y, fma(-d, y, 1.0), y);
-  y = fma(y, fma(-d, y, 1.0), y);
+  return fma(y, fma(-d, y, 1.0), y);
+}
+// 1 / (1 + e^-z)
+__device__ __forceinline__ double sigmoid_f64(const ExpConstants& k, float z) {
+  const double y = reciprocal_f64(1.0 + exp_f64(k, -(double)z));
   return z < -709.0f ? 0.0 : y;  // there d is infinite, or 1 / d below every float
 }
 
@@ -121,29 +122,36 @@ __global__ __launch_bounds__(kScoreWaves* kWave) void router_scores_kernel(Route
   const int lane = lane_id();
   const int t = blockIdx.x * kScoreWaves + threadIdx.x / kWave;
   if (t >= p.T) return;  // whole waves only
-  const int size = p.E / p.n_group, q = lane / p.span, u = lane & (p.span - 1);
+  const int span = 1 << p.span_log2, size = p.E / p.n_group, q = lane >> p.span_log2, u = lane & (span - 1);
   const T* __restrict__ row = static_cast<const T*>(p.logits) + (int64_t)t * p.E;
   const bool sigmoid = p.score == MEGAMOE_SCORE_SIGMOID;
 
+  const ExpConstants ec = exp_constants();
   const float kNone = -__builtin_huge_valf();
-  float z[PL];
+  // All loads before their first use, at valid addresses also where a lane has no expert: a guarded load each
+  // would wait for the one before.
+  float z[PL], bias[PL];
+  {
+    T raw[PL];
 #pragma unroll
-  for (int i = 0; i < PL; ++i) {
-    const int x = u + p.span * i;
-    z[i] = q < p.n_group && x < size ? load_logit<T>(row + q * size + x) : kNone;
+    for (int i = 0; i < PL; ++i) {
+      const int x = u + span * i, e = q < p.n_group && x < size ? q * size + x : 0;
+      raw[i] = row[e];
+      bias[i] = p.bias != nullptr ? p.bias[e] : 0.0f;
+    }
+#pragma unroll
+    for (int i = 0; i < PL; ++i) z[i] = q < p.n_group && u + span * i < size ? logit_of(raw[i]) : kNone;
   }
   double m = 0.0, inv = 1.0;  // softmax: largest logit, one over the sum
   // Keys of the choices: 0 for an expert that is not available.
   uint32_t key[PL];
   const auto set_key = [&](int i, float s) {
-    const int x = u + p.span * i;
-    float c = s;
-    if (p.bias != nullptr && q < p.n_group && x < size) c += p.bias[q * size + x];
+    const float c = s + bias[i];  // (s is not -0)
     key[i] = z[i] > kNone && c > kNone ? sort_key(c) : 0u;
   };
   if (sigmoid) {
 #pragma unroll
-    for (int i = 0; i < PL; ++i) set_key(i, (float)sigmoid_f64(z[i]));
+    for (int i = 0; i < PL; ++i) set_key(i, (float)sigmoid_f64(ec, z[i]));
   } else {
     uint32_t mk = 0;
 #pragma unroll
@@ -152,7 +160,7 @@ __global__ __launch_bounds__(kScoreWaves* kWave) void router_scores_kernel(Route
     double e[PL], sum = 0.0;
 #pragma unroll
     for (int i = 0; i < PL; ++i) {
-      e[i] = z[i] > kNone ? exp_f64((double)z[i] - m) : 0.0;
+      e[i] = z[i] > kNone ? exp_f64(ec, (double)z[i] - m) : 0.0;
       sum += e[i];
     }
     sum = score_wave_sum(sum);
@@ -168,7 +176,7 @@ __global__ __launch_bounds__(kScoreWaves* kWave) void router_scores_kernel(Route
       k1 = umax(key[i], k1);
       k2 = umax(lo, k2);
     }
-    for (int o = 1; o < p.span; o <<= 1) {
+    for (int o = 1; o < span; o <<= 1) {
       const uint32_t o1 = __shfl_xor(k1, o, kWave), o2 = __shfl_xor(k2, o, kWave);
       const uint32_t lo = o1 < k1 ? o1 : k1;
       k1 = umax(o1, k1);
@@ -179,7 +187,7 @@ __global__ __launch_bounds__(kScoreWaves* kWave) void router_scores_kernel(Route
     if (p.group_top > 1 && k2) gs += unsort_key(k2);
     int rank = 0;
     for (int g = 0; g < p.n_group; ++g) {
-      const float og = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(gs), g * p.span));
+      const float og = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(gs), g << p.span_log2));
       rank += (og > gs || (og == gs && g < q)) ? 1 : 0;
     }
     if (rank >= p.topk_group) {
@@ -201,7 +209,7 @@ __global__ __launch_bounds__(kScoreWaves* kWave) void router_scores_kernel(Route
     for (int i = 0; i < PL; ++i) {
       const uint64_t mask = __ballot(key[i] == wk);
       if (mask) {  // expert ids ascend with the lane
-        const int l = __builtin_ctzll(mask), e = (l / p.span) * size + (l & (p.span - 1)) + p.span * i;
+        const int l = __builtin_ctzll(mask), e = (l >> p.span_log2) * size + (l & (span - 1)) + span * i;
         if (e < win) {
           win = e;
           wi = i;
@@ -217,8 +225,8 @@ __global__ __launch_bounds__(kScoreWaves* kWave) void router_scores_kernel(Route
   // The winners' weights, one lane each.
   double ws = 0.0;
   if (my_id >= 0) {
-    const float wz = load_logit<T>(row + my_id);
-    ws = sigmoid ? sigmoid_f64(wz) : exp_f64((double)wz - m) * inv;
+    const float wz = logit_of(row[my_id]);
+    ws = sigmoid ? sigmoid_f64(ec, wz) : exp_f64(ec, (double)wz - m) * inv;
   }
   const double d = p.renormalize ? score_wave_sum(ws) : 1.0;
   if (lane < p.k) {
@@ -229,7 +237,7 @@ __global__ __launch_bounds__(kScoreWaves* kWave) void router_scores_kernel(Route
 
 template <typename T>
 static hipError_t launch_scores_t(const RouterScoreArgs& a, hipStream_t stream) {
-  const int per = (a.E / a.n_group + a.span - 1) / a.span;
+  const int span = 1 << a.span_log2, per = (a.E / a.n_group + span - 1) / span;
   const dim3 grid((a.T + kScoreWaves - 1) / kScoreWaves), block(kScoreWaves * kWave);
 #define MEGAMOE_SCORES(PL)                                                                  \
   if (per <= PL) {                                                                          \
@@ -249,8 +257,8 @@ static hipError_t launch_scores_t(const RouterScoreArgs& a, hipStream_t stream) 
 hipError_t launch_router_scores(const RouterScoreArgs& a0, int dtype, hipStream_t stream) {
   if (a0.T == 0) return hipSuccess;
   RouterScoreArgs a = a0;
-  a.span = kWave;
-  while (a.span * a.n_group > kWave) a.span >>= 1;
+  a.span_log2 = 6;
+  while ((a.n_group << a.span_log2) > kWave) --a.span_log2;
   return dtype == MEGAMOE_DTYPE_F32 ? launch_scores_t<float>(a, stream) : launch_scores_t<uint16_t>(a, stream);
 }
 
@@ -292,23 +300,26 @@ __global__ __launch_bounds__(kScoreWaves* kWave) void router_scores_bwd_kernel(R
     if (id < 0 || id >= p.E) id = -1;
     g = id >= 0 ? (double)p.grad_weights[(int64_t)t * p.k + lane] * (double)p.scale : 0.0;
   }
+  const ExpConstants ec = exp_constants();
   double s[PL];
   double m = 0.0, inv = 1.0;
   if (!sigmoid) {
     const float kNone = -__builtin_huge_valf();
     float z[PL];
+    T raw[PL];
     uint32_t mk = 0;
 #pragma unroll
+    for (int i = 0; i < PL; ++i) raw[i] = row[lane + kWave * i < p.E ? lane + kWave * i : 0];  // all in flight
+#pragma unroll
     for (int i = 0; i < PL; ++i) {
-      const int e = lane + kWave * i;
-      z[i] = e < p.E ? load_logit<T>(row + e) : kNone;
+      z[i] = lane + kWave * i < p.E ? logit_of(raw[i]) : kNone;
       mk = umax(mk, sort_key(z[i]));
     }
     m = (double)unsort_key(dpp_reduce(mk, umax));
     double sum = 0.0;
 #pragma unroll
     for (int i = 0; i < PL; ++i) {
-      s[i] = z[i] > kNone ? exp_f64((double)z[i] - m) : 0.0;
+      s[i] = z[i] > kNone ? exp_f64(ec, (double)z[i] - m) : 0.0;
       sum += s[i];
     }
     sum = score_wave_sum(sum);
@@ -316,13 +327,14 @@ __global__ __launch_bounds__(kScoreWaves* kWave) void router_scores_bwd_kernel(R
   }
   double sj = 0.0;  // score of this lane's chosen expert
   if (id >= 0) {
-    const float zj = load_logit<T>(row + id);
-    if (sigmoid) sj = sigmoid_f64(zj);
-    else sj = zj > -__builtin_huge_valf() ? exp_f64((double)zj - m) * inv : 0.0;
+    const float zj = logit_of(row[id]);
+    if (sigmoid) sj = sigmoid_f64(ec, zj);
+    else sj = zj > -__builtin_huge_valf() ? exp_f64(ec, (double)zj - m) * inv : 0.0;
   }
   if (p.renormalize) {
     const double S = score_wave_sum(sj), gs = score_wave_sum(g * sj);
-    g = S > 0.0 && id >= 0 ? (g - gs / S) / S : 0.0;
+    const double rS = S > 0.0 ? 1.0 / S : 0.0;
+    g = id >= 0 ? (g - gs * rS) * rS : 0.0;
   }
   const double dot = sigmoid ? 0.0 : score_wave_sum(g * sj);
   // g'_e of this lane's expert: the slots that name it, in slot order; then its gradient.
@@ -336,11 +348,11 @@ __global__ __launch_bounds__(kScoreWaves* kWave) void router_scores_bwd_kernel(R
 #pragma unroll
   for (int i = 0; i < PL; ++i) v[i] = round_logit<T>(sigmoid ? 0.0 : -(s[i] * inv * dot));
   for (int j = 0; j < p.k; ++j) {
-    const int ej = __builtin_amdgcn_readlane(id, j);
+    const int ej = __builtin_amdgcn_readlane(id, j);  // -1 is no expert: -1 / 64 is no i
     const T vj = read_lane(mine, j);
+    const bool here = lane == (ej & (kWave - 1));
 #pragma unroll
-    for (int i = 0; i < PL; ++i)
-      if (lane + kWave * i == ej) v[i] = vj;
+    for (int i = 0; i < PL; ++i) v[i] = here && (ej >> 6) == i ? vj : v[i];
   }
 #pragma unroll
   for (int i = 0; i < PL; ++i) {

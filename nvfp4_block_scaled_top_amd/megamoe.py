@@ -387,7 +387,7 @@ def _on(t: torch.Tensor, stream):
     _arg then refuses it)."""
     if not t.is_cuda:
         return -1, None
-    dev = torch.cuda.current_device()
+    dev = torch._C._cuda_getDevice()  # torch.cuda.current_device() of an initialized runtime
     return dev, torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
