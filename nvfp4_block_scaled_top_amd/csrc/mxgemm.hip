@@ -477,14 +477,15 @@ __global__ __launch_bounds__(kMxThreads, 1) void mx_tile_kernel(MxGemmArgs p) {
            lds_addr(reinterpret_cast<uint8_t*>(s_row + 64 * wave)));
     }
   };
-  // Waves 0-3 bring the stages: wave w weight rows 64 w .. 64 w + 63 and the w-th quarter of the token
-  // rows.  (They share the SIMDs with waves 4-7, which multiply meanwhile.)  What a load adds to its
-  // tensor's address is kept in units of 16 bytes for the codes and of 4 for the scales (operands of an
-  // expert are below 64 GB), the eight weight loads' in the lanes of one register: with all of it
-  // computed anew, 40 instructions a load, a stage's loads took 3800 cycles to issue.
-  uint32_t w_off = 0, a_off[8] = {0, 0, 0, 0, 0, 0, 0, 0}, ws_off = 0, as_off = 0;
+  // Every wave brings an eighth of a stage's weight and token rows, waves 0-3 ahead of their products and
+  // waves 4-7, which share the SIMDs with them, after the first quarter of theirs: 306 us for
+  // 16381 x 4096 x 7168 on random codes, 317 with all of them ahead, 316 with waves 0-3 bringing all, 314
+  // to 316 with waves 4-7 later.  What a load adds to its tensor's address is kept in units of 16 bytes for
+  // the codes and of 4 for the scales (operands of an expert are below 64 GB), the four weight loads' in
+  // the lanes of one register: with all of it computed anew, 40 instructions a load, a stage's loads took
+  // 3800 cycles to issue.
+  uint32_t w_off = 0, a_off[4] = {0, 0, 0, 0}, s_off = 0;
   const auto set_loads = [&](const MxTile& x) __attribute__((always_inline)) {
-    if (wave >= 4) return;
     int ln = lane;
     asm volatile("" : "+v"(ln));  // nothing of this is kept in registers across the tile
     const auto a_row = [&](int R) -> uint32_t {
@@ -501,67 +502,69 @@ __global__ __launch_bounds__(kMxThreads, 1) void mx_tile_kernel(MxGemmArgs p) {
         return (uint32_t)(c < p.N ? c : p.N - 8 + (c & 7));
       }
     };
-    w_off = w_row(64 * wave + 8 * (ln & 7)) * (uint32_t)(Kh / 16);
-    ws_off = w_row(64 * wave + ln) * (uint32_t)(Ks / 4);
-    as_off = a_row(64 * wave + ln) * (uint32_t)(Ks / 4);
+    w_off = w_row(32 * wave + 8 * (ln & 3)) * (uint32_t)(Kh / 16);
+    s_off = (wave < 4 ? w_row(64 * wave + ln) : a_row(64 * (wave - 4) + ln)) * (uint32_t)(Ks / 4);
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      a_off[j] = a_row((8 * (2 * x.wb * wave + j) + ln / 8) & (kMxBm - 1)) * (uint32_t)(Kh / 16);
+    for (int j = 0; j < 4; ++j)
+      a_off[j] = a_row((8 * (x.wb * wave + j) + ln / 8) & (kMxBm - 1)) * (uint32_t)(Kh / 16);
   };
-  int issued = 0, scale_issued = 0;  // parities of the slots
-  const auto issue = [&](const MxTile& x, int ks) __attribute__((always_inline)) {
-    const int slot = issued & 1, sslot = scale_issued & 1;
-    ++issued;
-    if (!(ks & 1)) ++scale_issued;
-    if (wave >= 4) return;
+  // Stage ks of tile x into slot `slot`, its scales (even ks) into buffer `buf`.
+  const auto issue = [&](const MxTile& x, int ks, int slot, int buf) __attribute__((always_inline)) {
     int ln = lane;
     asm volatile("" : "+v"(ln));  // what follows from the lane is computed here, not held through the tile
-    const uint32_t base = lds_addr(s_mx + slot * kMxStage);
+    const uint32_t base = lds_addr(s_mx + (slot & 1) * kMxStage);
     const int64_t wn0 = (int64_t)x.e * (kL1 ? 2 : 1) * p.N;
     const uint8_t* const wb = p.w_codes + wn0 * Kh + kMxRowBytes * ks;
     const uint8_t* const pad = reinterpret_cast<const uint8_t*>(g_mx_pad);
     // Lane l of a load brings a block of row l / 8 to place l % 8.
     const int blk0 = (ln & 7) ^ mx_swz(ln / 8);  // of an even 8-row piece (^ 4: odd)
     const uint32_t w_lane = (uint32_t)(ln / 8) * (uint32_t)Kh;
-    const bool whole = (ks + 1) * 8 <= nblk;  // else the last stage, of four blocks
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int blk = j & 1 ? blk0 ^ 4 : blk0;
-      const uint8_t* src = wb + ((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)w_off, j) << 4);
-      const uint32_t to = base + (64 * wave + 8 * j) * kMxRowBytes;
+    const uint32_t wl0 = w_lane + 16 * blk0, wl1 = w_lane + 16 * (blk0 ^ 4);
+    const uint8_t* const ab = p.a_codes + kMxRowBytes * ks;
+    const uint32_t to_w = base + 32 * wave * kMxRowBytes, to_a = base + kMxACodes + 8 * x.wb * wave * kMxRowBytes;
+    if ((ks + 1) * 8 <= nblk) {
       // Weights read once bypass the caches: 96 experts of 100 rows (2048 -> 7168) take 202 us instead of
       // 217; weights that the m-tiles of an expert share do not (16381 x 4096 x 7168: 321 us instead of 308).
-      if (whole && x.once) dma16snt(src, w_lane + 16 * blk, to);
-      else if (whole) dma16s(src, w_lane + 16 * blk, to);
-      else dma16(blk < 4 ? src + w_lane + 16 * blk : pad, to);
-    }
-    const uint8_t* const ab = p.a_codes + kMxRowBytes * ks;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      if (j < 2 * x.wb) {
+      for (int j = 0; j < 4; ++j) {
+        const uint8_t* src = wb + ((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)w_off, j) << 4);
+        if (x.once) dma16snt(src, j & 1 ? wl1 : wl0, to_w + 8 * j * kMxRowBytes);
+        else dma16s(src, j & 1 ? wl1 : wl0, to_w + 8 * j * kMxRowBytes);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (j >= x.wb) break;
+        const int blk = (x.wb * wave + j) & 1 ? blk0 ^ 4 : blk0;
+        dma16(ab + 16 * blk + (uint64_t)a_off[j] * 16, to_a + 8 * j * kMxRowBytes);
+      }
+    } else {  // the last stage, of four blocks
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
         const int blk = j & 1 ? blk0 ^ 4 : blk0;
-        const uint8_t* src = ab + 16 * blk + (uint64_t)a_off[j] * 16;
-        dma16(whole || blk < 4 ? src : pad, base + kMxACodes + 8 * (2 * x.wb * wave + j) * kMxRowBytes);
+        const uint8_t* src = wb + ((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)w_off, j) << 4);
+        dma16(blk < 4 ? src + (j & 1 ? wl1 : wl0) : pad, to_w + 8 * j * kMxRowBytes);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (j >= x.wb) break;
+        const int blk = (x.wb * wave + j) & 1 ? blk0 ^ 4 : blk0;
+        dma16(blk < 4 ? ab + 16 * blk + (uint64_t)a_off[j] * 16 : pad, to_a + 8 * j * kMxRowBytes);
       }
     }
-    if (ks & 1) return;
-    // the scales of 64 weight rows, and of 64 token rows
-    const uint32_t to = lds_addr(s_mx + kMxScales + sslot * kMxScaleBuf) + 16 * 64 * wave;
-    const uint8_t* const ws = p.w_scales + wn0 * Ks + 8 * ks;
-    const uint8_t* const as = p.a_scales + 8 * ks;
+    if ((ks & 1) || wave >= 4 + x.wb) return;
+    // the scales of 64 weight rows (waves 0-3) or token rows (waves 4-7)
+    const uint32_t to = lds_addr(s_mx + kMxScales + (buf & 1) * kMxScaleBuf) + 16 * 64 * wave;
+    const uint8_t* const sc = (wave < 4 ? p.w_scales + wn0 * Ks : p.a_scales) + 8 * ks;
     if (wide_scales) {
-      dma16(ws + (uint64_t)ws_off * 4, to);
-      if (wave < x.wb) dma16(as + (uint64_t)as_off * 4, to + kMxAScales);
+      dma16(sc + (uint64_t)s_off * 4, to);
     } else {
       // K not a multiple of 512: words, 16 rows a load
       const int word = ln & 3;
       const bool in = 4 * (ks * 2 + word) < nblk;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const uint64_t wo = (uint64_t)(uint32_t)__shfl((int)ws_off, 16 * j + ln / 4, kWave) * 4 + 4 * word;
-        const uint64_t ao = (uint64_t)(uint32_t)__shfl((int)as_off, 16 * j + ln / 4, kWave) * 4 + 4 * word;
-        dma4(in ? ws + wo : pad + 16, to + 256 * j);
-        if (wave < x.wb) dma4(in ? as + ao : pad + 16, to + kMxAScales + 256 * j);
+        const uint64_t o = (uint64_t)(uint32_t)__shfl((int)s_off, 16 * j + ln / 4, kWave) * 4 + 4 * word;
+        dma4(in ? sc + o : pad + 16, to + 256 * j);
       }
     }
   };
@@ -574,8 +577,8 @@ __global__ __launch_bounds__(kMxThreads, 1) void mx_tile_kernel(MxGemmArgs p) {
   wait_vmcnt<0>();
   mx_barrier();
   set_loads(cur);
-  issue(cur, 0);
-  int stage = 0, sstage = 0;
+  issue(cur, 0, 0, 0);
+  int stage = 0, sstage = 0;  // parities: of the slot and of the scale buffer in use
   bool first = true;
 
   const auto run_tile = [&](auto wb_tag) __attribute__((always_inline)) {
@@ -605,7 +608,9 @@ __global__ __launch_bounds__(kMxThreads, 1) void mx_tile_kernel(MxGemmArgs p) {
       }
       const bool last = ks + 1 == nks;
       if (last && more) set_loads(nxt);
-      if (!last || more) issue(last ? nxt : cur, last ? 0 : ks + 1);
+      const bool any = !last || more;
+      const int to_ks = last ? 0 : ks + 1, buf = sstage + ((ks & 1) || last ? 1 : 0);
+      if (any && wave < 4) issue(last ? nxt : cur, to_ks, stage + 1, buf);
       int ln = lane;
       asm volatile("" : "+v"(ln));  // a few instructions a stage instead of registers
       const int r = ln & 31, h = ln >> 5, swz = mx_swz(r);  // (of rows 32 i + r too)
@@ -644,8 +649,13 @@ __global__ __launch_bounds__(kMxThreads, 1) void mx_tile_kernel(MxGemmArgs p) {
 #pragma unroll
           for (int f = 0; f < WB; ++f) acc[i][f] = mx_mfma32<S>(w[S & 1][f], a[S & 1][i], acc[i][f], wsc[f], asc[i]);
         __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int f = 0; f < WB; ++f) asm volatile("" : "+v"(acc[i][f]));  // (products do not move past loads)
       };
       step(IntTag<0>{});
+      if (any && wave >= 4) issue(last ? nxt : cur, to_ks, stage + 1, buf);
       step(IntTag<1>{});
       step(IntTag<2>{});
       step(IntTag<3>{});
