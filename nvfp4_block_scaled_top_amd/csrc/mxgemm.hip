@@ -477,13 +477,14 @@ __global__ __launch_bounds__(kMxThreads, 1) void mx_tile_kernel(MxGemmArgs p) {
            lds_addr(reinterpret_cast<uint8_t*>(s_row + 64 * wave)));
     }
   };
-  // Every wave brings an eighth of a stage's weight and token rows, waves 0-3 ahead of their products and
-  // waves 4-7, which share the SIMDs with them, after the first quarter of theirs: 306 us for
-  // 16381 x 4096 x 7168 on random codes, 317 with all of them ahead, 316 with waves 0-3 bringing all, 314
-  // to 316 with waves 4-7 later.  What a load adds to its tensor's address is kept in units of 16 bytes for
-  // the codes and of 4 for the scales (operands of an expert are below 64 GB), the four weight loads' in
-  // the lanes of one register: with all of it computed anew, 40 instructions a load, a stage's loads took
-  // 3800 cycles to issue.
+  // Every wave brings an eighth of a stage's weight and token rows.  Under a 256-row tile waves 4-7, which
+  // share the SIMDs with waves 0-3, do so after the first quarter of their products, waves 0-3 before
+  // theirs: 306 us for 16381 x 4096 x 7168 on random codes, 317 with all of them before, 314 to 316 with
+  // waves 4-7 later.  Under lower tiles, which wait for memory, all bring theirs first: 96 experts of 48
+  // rows (2048 -> 7168) 183 us, 195 the other way.  What a load adds to its tensor's address is kept in
+  // units of 16 bytes for the codes and of 4 for the scales (operands of an expert are below 64 GB), the
+  // four weight loads' in the lanes of one register: with all of it computed anew, 40 instructions a load,
+  // a stage's loads took 3800 cycles to issue.
   uint32_t w_off = 0, a_off[4] = {0, 0, 0, 0}, s_off = 0;
   const auto set_loads = [&](const MxTile& x) __attribute__((always_inline)) {
     int ln = lane;
@@ -610,7 +611,7 @@ __global__ __launch_bounds__(kMxThreads, 1) void mx_tile_kernel(MxGemmArgs p) {
       if (last && more) set_loads(nxt);
       const bool any = !last || more;
       const int to_ks = last ? 0 : ks + 1, buf = sstage + ((ks & 1) || last ? 1 : 0);
-      if (any && wave < 4) issue(last ? nxt : cur, to_ks, stage + 1, buf);
+      if (any && (WB < 4 || wave < 4)) issue(last ? nxt : cur, to_ks, stage + 1, buf);
       int ln = lane;
       asm volatile("" : "+v"(ln));  // a few instructions a stage instead of registers
       const int r = ln & 31, h = ln >> 5, swz = mx_swz(r);  // (of rows 32 i + r too)
@@ -655,7 +656,7 @@ __global__ __launch_bounds__(kMxThreads, 1) void mx_tile_kernel(MxGemmArgs p) {
           for (int f = 0; f < WB; ++f) asm volatile("" : "+v"(acc[i][f]));  // (products do not move past loads)
       };
       step(IntTag<0>{});
-      if (any && wave >= 4) issue(last ? nxt : cur, to_ks, stage + 1, buf);
+      if (WB == 4 && any && wave >= 4) issue(last ? nxt : cur, to_ks, stage + 1, buf);
       step(IntTag<1>{});
       step(IntTag<2>{});
       step(IntTag<3>{});
