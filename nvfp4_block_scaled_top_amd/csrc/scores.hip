@@ -235,6 +235,10 @@ __global__ __launch_bounds__(kScoreWaves* kWave) void router_scores_kernel(Route
   }
 }
 
+// Tokens of a launch: a grid holds fewer than 2^32 threads, 2^26 tokens.
+constexpr int64_t kScoreTokens = (int64_t)1 << 24;
+static int64_t logit_bytes(int dtype) { return dtype == MEGAMOE_DTYPE_F32 ? 4 : 2; }
+
 template <typename T>
 static hipError_t launch_scores_t(const RouterScoreArgs& a, hipStream_t stream) {
   const int span = 1 << a.span_log2, per = (a.E / a.n_group + span - 1) / span;
@@ -255,11 +259,18 @@ static hipError_t launch_scores_t(const RouterScoreArgs& a, hipStream_t stream) 
 }
 
 hipError_t launch_router_scores(const RouterScoreArgs& a0, int dtype, hipStream_t stream) {
-  if (a0.T == 0) return hipSuccess;
   RouterScoreArgs a = a0;
   a.span_log2 = 6;
   while ((a.n_group << a.span_log2) > kWave) --a.span_log2;
-  return dtype == MEGAMOE_DTYPE_F32 ? launch_scores_t<float>(a, stream) : launch_scores_t<uint16_t>(a, stream);
+  hipError_t err = hipSuccess;
+  for (int64_t t = 0; t < a0.T && err == hipSuccess; t += kScoreTokens) {
+    a.T = (int32_t)(a0.T - t < kScoreTokens ? a0.T - t : kScoreTokens);
+    a.logits = static_cast<const char*>(a0.logits) + t * a.E * logit_bytes(dtype);
+    a.ids = a0.ids + t * a.k;
+    a.weights = a0.weights + t * a.k;
+    err = dtype == MEGAMOE_DTYPE_F32 ? launch_scores_t<float>(a, stream) : launch_scores_t<uint16_t>(a, stream);
+  }
+  return err;
 }
 
 // ---- gradient ------------------------------------------------------------------------------------
@@ -377,9 +388,18 @@ static hipError_t launch_scores_bwd_t(const RouterScoreBwdArgs& a, hipStream_t s
   return hipErrorInvalidValue;  // not reached: at most 1024 experts
 }
 
-hipError_t launch_router_scores_bwd(const RouterScoreBwdArgs& a, int dtype, hipStream_t stream) {
-  if (a.T == 0) return hipSuccess;
-  return dtype == MEGAMOE_DTYPE_F32 ? launch_scores_bwd_t<float>(a, stream) : launch_scores_bwd_t<uint16_t>(a, stream);
+hipError_t launch_router_scores_bwd(const RouterScoreBwdArgs& a0, int dtype, hipStream_t stream) {
+  RouterScoreBwdArgs a = a0;
+  hipError_t err = hipSuccess;
+  for (int64_t t = 0; t < a0.T && err == hipSuccess; t += kScoreTokens) {
+    a.T = (int32_t)(a0.T - t < kScoreTokens ? a0.T - t : kScoreTokens);
+    a.logits = static_cast<const char*>(a0.logits) + t * a.E * logit_bytes(dtype);
+    a.grad_logits = static_cast<char*>(a0.grad_logits) + t * a.E * logit_bytes(dtype);
+    a.ids = a0.ids + t * a.k;
+    a.grad_weights = a0.grad_weights + t * a.k;
+    err = dtype == MEGAMOE_DTYPE_F32 ? launch_scores_bwd_t<float>(a, stream) : launch_scores_bwd_t<uint16_t>(a, stream);
+  }
+  return err;
 }
 
 }  // namespace megamoe

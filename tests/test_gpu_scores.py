@@ -227,6 +227,31 @@ def test_gradient_in_place():
         assert torch.equal(zt, want)
 
 
+@pytest.mark.parametrize("T,E,k,dtype", [(2 ** 26 + 3, 2, 1, torch.bfloat16), (2 ** 22 + 3, 1024, 8, torch.float32)])
+def test_more_tokens_than_a_grid_and_logits_past_32_bits(T, E, k, dtype):
+    """Every row is one of 1009 rows, so the expected output is a table's."""
+    gen = torch.Generator(device=DEV).manual_seed(3)
+    few = torch.randn(1009, E, generator=gen, device=DEV).to(dtype)
+    which = torch.arange(T, device=DEV) % 1009
+    kw = dict(score="softmax", renormalize=False, scale=1.5)
+    z = few[which]
+    g = torch.ones(1, k, device=DEV).expand(T, k).contiguous()
+    out = []
+    for rows in (few, z):
+        ids = torch.full((len(rows), k), -7, dtype=torch.int32, device=DEV)
+        w = torch.full((len(rows), k), 9.0, device=DEV)
+        mm.moe_router_scores(rows, k, ids, w, **kw)
+        out.append((ids, w))
+    grad = torch.empty_like(few)
+    mm.moe_router_scores_bwd(few, out[0][0], g[:1009], grad, **kw)
+    mm.moe_router_scores_bwd(z, out[1][0], g, z, **kw)  # in place
+    step = 2 ** 21
+    for a in range(0, T, step):
+        i = which[a:a + step]
+        assert torch.equal(out[1][0][a:a + step], out[0][0][i]) and torch.equal(out[1][1][a:a + step], out[0][1][i])
+        assert torch.equal(z[a:a + step], grad[i])
+
+
 # ---- with the routing step -----------------------------------------------------------------------
 
 @pytest.mark.parametrize("T,P", [(0, 1), (1, 1), (8, 128), (700, 8)])
