@@ -421,7 +421,9 @@ __global__ __launch_bounds__(kMxThreads, 1) void mx_tile_kernel(MxGemmArgs p) {
   const int E = p.E, K = p.K, nks = (K + kMxStageK - 1) / kMxStageK, nblk = K / 32;
   const int64_t Kh = K / 2, Ks = K / 32;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), lane = lane_id();
-  const bool wide_scales = K % 512 == 0;  // whole 16-byte scale pieces
+  // whole scale pieces of 16 bytes, aligned
+  const bool wide_scales =
+      K % 512 == 0 && ((reinterpret_cast<uintptr_t>(p.w_scales) | reinterpret_cast<uintptr_t>(p.a_scales)) & 15) == 0;
   if (wave == 0) {  // exclusive prefix of the experts' m-tiles
     const bool none = p.counts != nullptr && mx_small_takes_all(p, kL1);
     int carry = 0;
@@ -559,7 +561,7 @@ __global__ __launch_bounds__(kMxThreads, 1) void mx_tile_kernel(MxGemmArgs p) {
     if (wide_scales) {
       dma16(sc + (uint64_t)s_off * 4, to);
     } else {
-      // K not a multiple of 512: words, 16 rows a load
+      // else words, 16 rows a load
       const int word = ln & 3;
       const bool in = 4 * (ks * 2 + word) < nblk;
 #pragma unroll

@@ -24,7 +24,8 @@ def dev(a):
 
 
 def bf16_np(t):
-    return t.detach().float().cpu().numpy().astype(np.float64)
+    with np.errstate(invalid="ignore"):  # signalling NaN
+        return t.detach().float().cpu().numpy().astype(np.float64)
 
 
 def bf16_round(a):
@@ -230,6 +231,69 @@ def test_linear_large_is_repeatable_and_matches_samples():
     accept(bf16_np(out)[rows], ref, zabs, K)
 
 
+@pytest.mark.parametrize("off", [4, 8, 12])
+@pytest.mark.parametrize("M", [5, 700])
+def test_linear_scales_aligned_to_words(M, off):
+    """Scales at any multiple of 4, codes and outputs at an odd multiple of 16: the same bits."""
+    rng = np.random.default_rng(M + off)
+    N, K = 2064, 1024
+    (ac, as_), (wc, ws) = quantized(rng, M, K, 0.5), quantized(rng, N, K, 0.1)
+
+    def at(a, o):
+        buf = torch.empty(a.size + 64, dtype=torch.uint8, device=DEV)
+        v = buf[o:o + a.size].view(a.shape)
+        v.copy_(torch.from_numpy(a))
+        return v
+    want = torch.empty(M, N, dtype=torch.bfloat16, device=DEV)
+    mm.mxfp4_linear(dev(ac), dev(as_), dev(wc), dev(ws), want)
+    out = torch.empty(M * N + 8, dtype=torch.bfloat16, device=DEV)[8:].view(M, N)
+    mm.mxfp4_linear(at(ac, 16), at(as_, off), at(wc, 48), at(ws, 16 - off), out)
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("M,N,K", [(300000, 16, 32768), (300000, 256, 32768), (4, 300000, 32768), (600, 300000, 32768),
+                                   (131077, 32784, 128)])
+def test_linear_offsets_past_32_bits(M, N, K):
+    """Codes beyond 4 GB and more than 2^32 outputs: samples against the oracle, ends included."""
+    gen = torch.Generator(device=DEV).manual_seed(N)
+
+    def operand(rows):
+        c = torch.randint(0, 256, (rows, K // 2), dtype=torch.uint8, device=DEV, generator=gen)
+        return c, torch.randint(118, 124, (rows, K // 32), dtype=torch.uint8, device=DEV, generator=gen)
+    (ac, as_), (wc, ws) = operand(M), operand(N)
+    out = torch.full((M, N), float("nan"), dtype=torch.bfloat16, device=DEV)
+    mm.mxfp4_linear(ac, as_, wc, ws, out)
+    torch.cuda.synchronize()
+    rng = np.random.default_rng(1)
+    pick = [torch.from_numpy(np.unique(np.concatenate([rng.choice(n, min(n, 20), replace=False), [0, n // 2, n - 1]])))
+            for n in (M, N)]
+    part = lambda t, i: t[i.to(DEV)].cpu().numpy()  # noqa: E731
+    ref, zabs = X.product(X.decode(part(ac, pick[0]), part(as_, pick[0])), X.decode(part(wc, pick[1]), part(ws, pick[1])))
+    got = out[pick[0].to(DEV)][:, pick[1].to(DEV)]
+    accept(bf16_np(got), ref, zabs, K)
+    assert not torch.isnan(out.view(-1)[:: 4099]).any() and not torch.isnan(out[:, -1]).any()
+
+
+def test_quantize_and_decode_past_32_bits():
+    """2^32 elements and some: each row as the same row of a small tensor."""
+    rows, cols = 2 ** 21 + 5, 2048
+    gen = torch.Generator(device=DEV).manual_seed(8)
+    few = (torch.randn(64, cols, generator=gen, device=DEV) * 0.3).to(torch.bfloat16)
+    x = few.repeat(rows // 64 + 1, 1)[:rows]
+    out = []
+    for t in (few, x):
+        c, s = (torch.empty(len(t), cols // n, dtype=torch.uint8, device=DEV) for n in (2, 32))
+        mm.mxfp4_quantize_act(t, c, s)
+        y = torch.empty_like(t)
+        mm.mxfp4_dequantize(c, s, y)
+        out.append((c, s, y))
+    for a in range(0, rows, 2 ** 17):
+        n = min(2 ** 17, rows - a)
+        for small, large in zip(*out):
+            assert torch.equal(large[a:a + n], small.repeat(2 ** 11, 1)[:n])
+
+
 # ---- experts -------------------------------------------------------------------------------------
 
 def tables(counts, P, T, rng):
@@ -364,6 +428,22 @@ def test_layer_from_ids_equals_layer_from_logits():
     ids, w = L.topk_ids.clone(), L.topk_weights.clone()
     L.out.fill_(float("nan"))
     assert torch.equal(L.forward(x, ids, w, W), a)
+
+
+@pytest.mark.parametrize("T", [12, 200])
+def test_layer_same_expert_twice(T):
+    """A token that names an expert twice has two equal rows there; an expert then has more rows than T."""
+    W, x, _, L = make_layer(T, 2, 8, 0, 8, 256, 128, 1, T)
+    ids = torch.full((T, 2), 3, dtype=torch.int32, device=DEV)
+    w = torch.tensor([[0.75, -0.25]], device=DEV).expand(T, 2).contiguous()
+    out = L.forward(x, ids, w, W).clone()
+    assert int(L.counts[3]) == 2 * T and int(L.counts.sum()) == 2 * T
+    y = L.y[L.token_rows.view(T, 2).long()]
+    assert torch.equal(y[:, 0], y[:, 1])
+    hv, rows = X.decode(np_i32(L.h_codes).astype(np.uint8), np_i32(L.h_scales).astype(np.uint8)), np_i32(L.token_rows)[::2]
+    ref, zabs = X.product(hv[rows], X.decode(np_i32(W.w2_codes[3]).astype(np.uint8), np_i32(W.w2_scales[3]).astype(np.uint8)))
+    accept(bf16_np(y[:, 0]), ref, zabs, 128)
+    assert torch.equal(out, (y[:, 0].float() * 0.5).to(torch.bfloat16))  # 0.75 y - 0.25 y, exact
 
 
 @pytest.mark.parametrize("T", [0, 2, 100])
