@@ -612,7 +612,8 @@ int32_t nvfp4_linear_gate_up_silu_nvfp4(const uint8_t* a_codes, const uint8_t* a
  *              scales (pass row_token to quantize permuted rows).
  * codes        uint8 [rows, cols/2];  scales uint8 [rows, cols/32].
  * out_bf16     bf16 [rows, cols]: the values, exact; beyond bf16's range (6 * 2^126 and up) infinite.
- * Limits: rows >= 0, cols > 0 and a multiple of 32; x, codes and out_bf16 aligned to 16 bytes.
+ * Limits: rows >= 0, cols > 0 and a multiple of 32, fewer than 2^37 elements; x, codes and out_bf16
+ * aligned to 16 bytes, no output overlapping an input.
  * ---------------------------------------------------------------------------------------- */
 int32_t mxfp4_quantize_act(const void* x, int32_t dtype, int64_t rows, int64_t cols,
                            const int32_t* row_valid, uint8_t* codes, uint8_t* scales, void* stream);
@@ -630,7 +631,8 @@ int32_t mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t ro
  * w_codes/w_scales   [N, K/2], [N, K/32];  w13 [2I, K/2], [2I, K/32], rows 0..I-1 gate, I..2I-1 up.
  * out_bf16 bf16 [M, N];  h_bf16 bf16 [M, I].
  * Limits: 0 <= M < 2^31, K >= 128 and a multiple of 128, N and I >= 16 and multiples of 16, below
- * 2^30; codes and outputs aligned to 16 bytes, scales to 4.  With M == 0 the call enqueues nothing.
+ * 2^30; A's codes and W's below 2^36 bytes each; codes and outputs aligned to 16 bytes, scales to 4.
+ * With M == 0 the call enqueues nothing.
  * ---------------------------------------------------------------------------------------- */
 int32_t mxfp4_linear(const uint8_t* a_codes, const uint8_t* a_scales, int64_t M, int32_t K,
                      const uint8_t* w_codes, const uint8_t* w_scales, int32_t N, void* out_bf16, void* stream);
@@ -654,11 +656,12 @@ int32_t mxfp4_linear_gate_up_silu(const uint8_t* a_codes, const uint8_t* a_scale
  * w13 [E, 2I, H/2], [E, 2I, H/32];  w2 [E, H, I/2], [E, H, I/32].
  * M_cap        rows of h and y: megamoe_row_capacity(T, k, E, P).
  * max_rows_per_expert  a bound on counts[e] the caller expects, or 0 if none: it may change which
- *              kernels launch, never the results; a bound that is too low costs time only.
+ *              kernels launch and with them the order of the FP32 sums, nothing else; a bound that is too
+ *              low costs time only.
  * h_bf16 bf16 [M_cap, I];  y_bf16 bf16 [M_cap, H].
  * Limits: E as for moe_route_permute; the reduced dimension (H for L1, I for L2) a multiple of 128,
- * the output dimension a multiple of 16; alignment as for mxfp4_linear.  With M_cap == 0 the row
- * arrays may be NULL and the call enqueues nothing.
+ * the output dimension a multiple of 16; M_cap rows of codes, and one expert's codes, below 2^36 bytes;
+ * alignment as for mxfp4_linear.  With M_cap == 0 the row arrays may be NULL and the call enqueues nothing.
  * ---------------------------------------------------------------------------------------- */
 int32_t moe_grouped_gemm_l1_silu_mxfp4(const uint8_t* x_codes, const uint8_t* x_scales,
                                        const int32_t* row_token, const int32_t* padded_offsets,

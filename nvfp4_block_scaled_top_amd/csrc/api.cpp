@@ -636,8 +636,9 @@ int32_t moe_router_scores_bwd(const void* logits, int32_t dtype, int32_t T, int3
 
 // ---- MXFP4 ---------------------------------------------------------------------------------------
 
+// (2^37 elements: as many as a launch has threads for; their bf16 and codes would not fit the GPU)
 static bool mx_matrix_ok(int64_t rows, int64_t cols) {
-  return rows >= 0 && cols > 0 && cols % 32 == 0 && rows <= ((int64_t)1 << 40) / cols;
+  return rows >= 0 && cols > 0 && cols % 32 == 0 && rows < ((int64_t)1 << 37) / cols;
 }
 
 int32_t mxfp4_quantize_act(const void* x, int32_t dtype, int64_t rows, int64_t cols, const int32_t* row_valid,

@@ -142,12 +142,18 @@ def test_mxfp4_reject_bad_args(lib):
         assert lin(FAKE, FAKE, 4, 256, FAKE, FAKE, n, None, None) == -1
         assert lin(FAKE, ODD, 4, 256, FAKE, FAKE, n, FAKE, None) == -6
         assert lin(FAKE, FAKE, 4, 256, FAKE, FAKE, n, ODD, None) == -6
+        assert lin(FAKE, FAKE, 1 << 30, 256, FAKE, FAKE, n, FAKE, None) == -2     # 2^37 bytes of A
+        assert lin(FAKE, FAKE, 4, 1 << 17, FAKE, FAKE, 1 << 20, FAKE, None) == -2  # 2^36 of W
+    assert q(FAKE, 0, 1 << 31, 64, None, FAKE, FAKE, None) == -2 and d(FAKE, FAKE, 1 << 31, 64, FAKE, None) == -2
     l1, l2 = lib.moe_grouped_gemm_l1_silu_mxfp4, lib.moe_grouped_gemm_l2_mxfp4
     a7, a6 = [FAKE] * 7, [FAKE] * 6
     assert l1(*a7, 8, 192, 128, 64, 0, FAKE, None) == -2       # H % 128
     assert l1(*a7, 8, 256, 120, 64, 0, FAKE, None) == -2       # I % 16
     assert l1(*a7, 0, 256, 128, 64, 0, FAKE, None) == -2 and l1(*a7, 1025, 256, 128, 64, 0, FAKE, None) == -2
     assert l1(*a7, 8, 256, 128, -1, 0, FAKE, None) == -2 and l1(*a7, 8, 256, 128, 64, -1, FAKE, None) == -2
+    assert l1(*a7, 8, 1 << 17, 1 << 19, 64, 0, FAKE, None) == -2  # 2^36 bytes an expert
+    assert l2(*a6, 8, 1 << 20, 1 << 17, 64, 0, FAKE, None) == -2
+    assert l1(*a7, 8, 256, 128, 1 << 30, 0, FAKE, None) == -2
     assert l1(*a7, 8, 256, 128, 64, 0, None, None) == -1
     assert l1(FAKE, FAKE, None, *[FAKE] * 4, 8, 256, 128, 64, 0, FAKE, None) == -1
     assert l1(*a7, 8, 256, 128, 64, 0, ODD, None) == -6
