@@ -62,7 +62,8 @@ __device__ __forceinline__ int mx_count(const MxGemmArgs& p, int e) { return p.c
 // Where the token rows of the whole K fit LDS four times beside the rings (K up to 2048), K is not split:
 // every wave takes groups of its own and keeps its own copy of the token rows, and nothing is shared
 // or waited for.  With K = 2048 split in four a wave has one slot between two barriers: the down projection
-// of a 512-token prompt (384 experts, 7168 x 2048) took 814 us, and takes 632 (4.8 TB/s) without the split; with
+// of a 512-token prompt (384 experts, 7168 x 2048) took 814 us, and 632 without the split (528, 5.8 TB/s, with
+// the places found as below; these loads alone stream 7.2 TB/s); with
 // K = 7168 the split spreads 16 rows' 61 KB over the four waves, which LDS would not hold four times.
 // ============================================================================================
 constexpr int kMxSmallRows = 16;
@@ -159,6 +160,39 @@ __device__ __forceinline__ void mx_seek(const MxGemmArgs& p, int e0, int mrows, 
   }
 }
 
+// The place of group g of the list, nt groups an m-tile: the experts' m-tiles are summed 64 at a time.
+// (Walking the experts one by one, a load each, the last wave of 384 experts began 150 us late.)
+__device__ __forceinline__ MxPlace mx_place(const MxGemmArgs& p, int64_t g, int nt, int mrows) {
+  MxPlace at;
+  int64_t m = g / nt;
+  at.j = (int)(g % nt);
+  at.e = 0;
+  at.cnt = (int)p.M;
+  if (p.counts != nullptr) {
+    for (int c = 0; c < p.E; c += kWave) {
+      const int cnt = c + lane_id() < p.E ? mx_count(p, c + lane_id()) : 0;
+      const int own = mx_small_tiles(p, cnt, mrows);
+      int incl = own;
+#pragma unroll
+      for (int o = 1; o < kWave; o <<= 1) {
+        const int t = __shfl_up(incl, o, kWave);
+        if (lane_id() >= o) incl += t;
+      }
+      const uint64_t past = __ballot((int64_t)incl > m);
+      if (past) {
+        const int l = __builtin_amdgcn_readfirstlane(__ffsll((unsigned long long)past) - 1);
+        at.e = c + l;
+        at.cnt = __builtin_amdgcn_readlane(cnt, l);
+        m -= __builtin_amdgcn_readlane(incl - own, l);
+        break;
+      }
+      m -= __builtin_amdgcn_readlane(incl, kWave - 1);
+    }
+  }
+  at.mt = (int)m;
+  return at;
+}
+
 template <bool kL1, bool kSplit>
 __global__ __launch_bounds__(kMxSplit* kWave, 1) void mx_small_kernel(MxGemmArgs p, int slots) {
   extern __shared__ __attribute__((aligned(16))) uint8_t s_mx[];
@@ -190,23 +224,7 @@ __global__ __launch_bounds__(kMxSplit* kWave, 1) void mx_small_kernel(MxGemmArgs
   const int64_t gb = part * groups / parts, ge = (part + 1) * groups / parts;
   if (gb >= ge) return;  // with the split, the whole workgroup
 
-  MxPlace cur;  // of the group that is computed
-  {
-    int64_t m = gb / nt;
-    cur.j = (int)(gb % nt);
-    if (p.counts == nullptr) {
-      cur.e = 0;
-      cur.cnt = (int)p.M;
-      cur.mt = (int)m;
-    } else {
-      for (mx_seek(p, 0, mrows, cur);; mx_seek(p, cur.e + 1, mrows, cur)) {
-        const int n = mx_small_tiles(p, cur.cnt, mrows);
-        if (m < n || cur.e >= p.E) break;
-        m -= n;
-      }
-      cur.mt = (int)m;
-    }
-  }
+  MxPlace cur = mx_place(p, gb, nt, mrows);  // of the group that is computed
   const auto next = [&](MxPlace& at) {
     if (++at.j < nt) return;
     at.j = 0;
