@@ -198,6 +198,8 @@ int32_t moe_route_scores(const void* logits, int32_t dtype, int32_t T, int32_t n
  * with renormalize scale / S * (g_j - sum_i g_i n_i);
  *   sigmoid: grad_e = g'_e s_e (1 - s_e);   softmax: grad_e = s_e (g'_e - sum_j g'_j s_j)
  * with g'_e the sum over the slots that name e (0 for the others), in float64 with one rounding.
+ * Renormalised gradients are finite at any distance of the chosen logits from the row's largest or from 0,
+ * and exactly 0 for experts that no slot names.
  * Ids outside [0, num_experts_global) (the empty slots) take no part.
  *
  * logits, dtype, score, renormalize, scale   as given to moe_router_scores.

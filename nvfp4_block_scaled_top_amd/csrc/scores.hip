@@ -278,6 +278,9 @@ hipError_t launch_router_scores(const RouterScoreArgs& a0, int dtype, hipStream_
 // g'_j = scale * g_j (weights kept) or scale / S * (g_j - sum_i g_i n_i) (renormalised), and
 //   sigmoid: dz_e = g'_e s_e (1 - s_e);    softmax: dz_e = s_e (g'_e - sum_j g'_j s_j),
 // with g'_e = 0 for experts that were not chosen (an expert listed twice takes both slots' share).
+// Renormalised, sum_j g'_j s_j = 0: a softmax's gradient is then that of a softmax over the chosen experts
+// alone and 0 elsewhere, the other logits are not read, and only ratios of chosen scores remain, which
+// relative_score gives at any distance from the row's largest logit.
 // float64 up to the one rounding of dz.  One wave per token, lane l holding experts l + 64 i; the
 // chosen experts' scores are computed one per lane.
 template <typename T>
@@ -294,6 +297,12 @@ __device__ __forceinline__ uint16_t read_lane(uint16_t v, int lane) {
   return (uint16_t)__builtin_amdgcn_readlane((int)v, lane);
 }
 
+// e^(z - the largest z of the wave's chosen lanes), 0 for the others.
+__device__ __forceinline__ double relative_score(const ExpConstants& ec, float z, bool chosen) {
+  const uint32_t mk = dpp_reduce(chosen ? sort_key(z) : 0u, umax);
+  return chosen && z > -__builtin_huge_valf() ? exp_f64(ec, (double)z - (double)unsort_key(mk)) : 0.0;
+}
+
 template <typename T, int PL>
 __global__ __launch_bounds__(kScoreWaves* kWave) void router_scores_bwd_kernel(RouterScoreBwdArgs p) {
   const int lane = lane_id();
@@ -303,6 +312,7 @@ __global__ __launch_bounds__(kScoreWaves* kWave) void router_scores_bwd_kernel(R
   const T* row = static_cast<const T*>(p.logits) + (int64_t)t * p.E;
   T* out = static_cast<T*>(p.grad_logits) + (int64_t)t * p.E;
   const bool sigmoid = p.score == MEGAMOE_SCORE_SIGMOID;
+  const bool every = !sigmoid && !p.renormalize;  // every logit has a gradient
 
   int id = -1;
   double g = 0.0;
@@ -314,7 +324,7 @@ __global__ __launch_bounds__(kScoreWaves* kWave) void router_scores_bwd_kernel(R
   const ExpConstants ec = exp_constants();
   double s[PL];
   double m = 0.0, inv = 1.0;
-  if (!sigmoid) {
+  if (every) {
     const float kNone = -__builtin_huge_valf();
     float z[PL];
     T raw[PL];
@@ -336,28 +346,36 @@ __global__ __launch_bounds__(kScoreWaves* kWave) void router_scores_bwd_kernel(R
     sum = score_wave_sum(sum);
     inv = sum > 0.0 ? 1.0 / sum : 0.0;
   }
-  double sj = 0.0;  // score of this lane's chosen expert
-  if (id >= 0) {
-    const float zj = logit_of(row[id]);
-    if (sigmoid) sj = sigmoid_f64(ec, zj);
-    else sj = zj > -__builtin_huge_valf() ? exp_f64(ec, (double)zj - m) * inv : 0.0;
+  double sj = 0.0, cj = 1.0;  // score of this lane's chosen expert; sigmoid: 1 minus it
+  const float zj = id >= 0 ? logit_of(row[id]) : -__builtin_huge_valf();
+  if (sigmoid) {
+    sj = sigmoid_f64(ec, zj);
+    cj = 1.0 - sj;
+  } else if (every) {
+    sj = zj > -__builtin_huge_valf() ? exp_f64(ec, (double)zj - m) * inv : 0.0;
   }
   if (p.renormalize) {
-    const double S = score_wave_sum(sj), gs = score_wave_sum(g * sj);
+    double S = sigmoid ? score_wave_sum(sj) : 0.0;
+    // Sigmoids below 2^-60 are e^z to float64's last bit.
+    if (S < 0x1p-60) {
+      sj = relative_score(ec, zj, id >= 0);
+      S = score_wave_sum(sj);
+    }
+    const double gs = score_wave_sum(g * sj);
     const double rS = S > 0.0 ? 1.0 / S : 0.0;
     g = id >= 0 ? (g - gs * rS) * rS : 0.0;
   }
-  const double dot = sigmoid ? 0.0 : score_wave_sum(g * sj);
+  const double dot = every ? score_wave_sum(g * sj) : 0.0;
   // g'_e of this lane's expert: the slots that name it, in slot order; then its gradient.
   double ge = 0.0;
   for (int j = 0; j < p.k; ++j) {
     const double gj = read_lane(g, j);
     ge += __builtin_amdgcn_readlane(id, j) == id ? gj : 0.0;
   }
-  const T mine = round_logit<T>(sigmoid ? ge * sj * (1.0 - sj) : sj * (ge - dot));
+  const T mine = round_logit<T>(sigmoid ? ge * sj * cj : sj * (ge - dot));
   T v[PL];
 #pragma unroll
-  for (int i = 0; i < PL; ++i) v[i] = round_logit<T>(sigmoid ? 0.0 : -(s[i] * inv * dot));
+  for (int i = 0; i < PL; ++i) v[i] = round_logit<T>(every ? -(s[i] * inv * dot) : 0.0);
   for (int j = 0; j < p.k; ++j) {
     const int ej = __builtin_amdgcn_readlane(id, j);  // -1 is no expert: -1 / 64 is no i
     const T vj = read_lane(mine, j);

@@ -57,9 +57,25 @@ def gate_up(a: np.ndarray, w13: np.ndarray):
 
 # ---- scored router -------------------------------------------------------------------------------
 
-def scores(logits: np.ndarray, kind: str) -> np.ndarray:
+def finite_logits(logits: np.ndarray) -> np.ndarray:
+    """float64 logits with NaN taken as -inf and +inf as the largest float32."""
     z = np.asarray(logits, np.float64)
-    z = np.where(np.isnan(z), -np.inf, np.minimum(z, float(np.finfo(np.float32).max)))
+    return np.where(np.isnan(z), -np.inf, np.minimum(z, float(np.finfo(np.float32).max)))
+
+
+def shares(z: np.ndarray, kind: str) -> np.ndarray:
+    """s_j / sum_i s_i of the scores of logits z [n], from their logarithms, which do not underflow
+    (a softmax's common factor cancels); zeros where no logit is above -inf."""
+    z = np.asarray(z, np.float64)
+    if not np.any(z > -np.inf):
+        return np.zeros(z.shape)
+    log_s = -np.logaddexp(0.0, -z) if kind == "sigmoid" else z
+    e = np.exp(log_s - log_s.max())
+    return e / e.sum()
+
+
+def scores(logits: np.ndarray, kind: str) -> np.ndarray:
+    z = finite_logits(logits)
     with np.errstate(over="ignore", invalid="ignore"):
         if kind == "sigmoid":
             return 1.0 / (1.0 + np.exp(-z))
@@ -99,17 +115,25 @@ def router(logits, k, bias=None, score="sigmoid", n_group=1, topk_group=1, group
 
 
 def router_bwd(logits, ids, grad, score="sigmoid", renormalize=True, scale=1.0):
-    """Gradient of the weights with respect to the logits, float64 [T, E]."""
-    s = scores(logits, score)
+    """Gradient of the weights with respect to the logits, float64 [T, E].  Renormalised, with
+    n_j = s_j / S: dw_j / dz_e = scale n_j ([e = e_j] - n_e) f_e, f = 1 - s for sigmoid scores and 1 for
+    softmax, whose sum over all experts cancels in n."""
+    z, s = finite_logits(logits), scores(logits, score)
     out = np.zeros_like(s)
     for t in range(s.shape[0]):
         at = [(j, e) for j, e in enumerate(ids[t]) if 0 <= e < s.shape[1]]
-        total = sum(s[t, e] for _, e in at) if renormalize else 1.0
-        if total <= 0:
+        if not at:
             continue
-        mean = sum(float(grad[t, j]) * s[t, e] for j, e in at) / total if renormalize else 0.0
-        d = np.zeros(s.shape[1])
-        for j, e in at:
-            d[e] += scale / total * (float(grad[t, j]) - mean)
-        out[t] = d * s[t] * (1 - s[t]) if score == "sigmoid" else s[t] * (d - (d * s[t]).sum())
+        g = np.array([float(grad[t, j]) for j, _ in at])
+        if renormalize:
+            n = shares(z[t, [e for _, e in at]], score)
+            part = scale * n * (g - (g * n).sum())
+        else:
+            part = scale * g * s[t, [e for _, e in at]]
+        if score == "sigmoid":
+            part = part * (1 - s[t, [e for _, e in at]])
+        elif not renormalize:
+            out[t] = -s[t] * part.sum()
+        for (_, e), d in zip(at, part):
+            out[t, e] += d
     return out

@@ -252,6 +252,53 @@ def test_more_tokens_than_a_grid_and_logits_past_32_bits(T, E, k, dtype):
         assert torch.equal(z[a:a + step], grad[i])
 
 
+# Chosen logits far below the row's largest (softmax) or 0 (sigmoid): their scores are float64 subnormals from 709
+# on and 0 from 745 on.  One row each.
+FAR = [0.0, 30.0, 41.0, 42.0, 100.0, 700.0, 706.0, 709.0, 712.0, 720.0, 736.0, 744.0, 745.5, 750.0, 800.0, 1e4, 1e30]
+
+
+def far_rows(seed, dtype):
+    """float32 logits [len(FAR), 40], representable in dtype, and the ids of 5 of them: 0 the largest logit,
+    the chosen ones FAR below it, within 3 of each other."""
+    rng = np.random.default_rng(seed)
+    z = -rng.uniform(0.5, 4, (len(FAR), 40))
+    z[:, 0] = 0.0
+    ids = np.stack([1 + rng.permutation(39)[:5] for _ in FAR]).astype(np.int32)
+    for t, far in enumerate(FAR):
+        z[t, ids[t]] -= far
+    return torch.from_numpy(z.astype(np.float32)).to(dtype).float().numpy(), ids
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+def test_renormalized_gradient_far_from_the_largest_logit(score, dtype):
+    """Within one rounding of scale * n_j (g_j - sum g n) f_j, f_j <= 1, whose shares n_j of either side are off by
+    less than 2^-42 of themselves (an exponent of at most 800 in float64, and sums of 5)."""
+    z, ids = far_rows(21, dtype)
+    if score == "sigmoid":
+        z[:, 0] = -1.0
+    rng = np.random.default_rng(22)
+    grad = rng.standard_normal(ids.shape).astype(np.float32)
+    ids[3, 2] = ids[3, 0]     # an expert named twice
+    ids[9, 1] = -1
+    z[10, ids[10, 4]] = -np.inf
+    kw = dict(score=score, renormalize=True, scale=2.5)
+    out, zh, _ = run_bwd(z, ids, grad, dtype, **kw)
+    got, ref = out.float().cpu().numpy().astype(np.float64), X.router_bwd(zh, ids, grad, **kw)
+    half, tiny = (2.0 ** -24, F32_TINY) if dtype == torch.float32 else (2.0 ** -8, 2.0 ** -134)
+    n = np.zeros_like(ref)
+    for t in range(len(ids)):
+        at = [e for e in ids[t] if e >= 0]
+        np.add.at(n[t], at, X.shares(zh[t, at], score))
+    size = 2 * 2.5 * np.abs(grad).max(1, keepdims=True) * n
+    assert np.isfinite(got).all()
+    assert np.all(np.abs(got - ref) <= np.abs(ref) * half + size * 2.0 ** -40 + tiny)
+    named = np.zeros_like(n, bool)
+    for t in range(len(ids)):
+        named[t, ids[t][ids[t] >= 0]] = True
+    assert np.all(got[~named] == 0)
+
+
 # ---- with the routing step -----------------------------------------------------------------------
 
 @pytest.mark.parametrize("T,P", [(0, 1), (1, 1), (8, 128), (700, 8)])

@@ -85,6 +85,26 @@ def test_oracle_router_masks():
     assert w[0].tolist() == [0, 0, 0] and w[1].tolist() == [0.5, 0.5, 0]
 
 
+FAR = [0.0, -40.0, -700.0, -709.0, -720.0, -744.0, -746.0, -1e4, -1e30]
+
+
+@pytest.mark.parametrize("far", FAR)
+def test_oracle_gradient_far_from_the_largest_logit(far):
+    """Two chosen logits, `far` below the row's largest (softmax) or 0 (sigmoid): n_1 = 1 / (1 + e^(z_2 - z_1))
+    of scores that are e^z up to a common factor; dw_1 = -dw_2 = scale * n_1 n_2 (g_1 - g_2)."""
+    z = np.array([[0.0, far - 1.0, far - 1.75, -3.0]])
+    ids, grad = np.array([[1, 2]]), np.array([[1.0, -0.5]])
+    d = z[0, 2] - z[0, 1]  # as rounded
+    n = 1 / (1 + np.exp(d))
+    want = 2.5 * n * (1 - n) * 1.5
+    got = X.router_bwd(z, ids, grad, "softmax", True, 2.5)[0]
+    assert np.all(np.abs(got - [0, want, -want, 0]) <= want * 2.0 ** -40)
+    if far <= -40.0:
+        z[0, 0] = -3.0
+        got = X.router_bwd(z, ids, grad, "sigmoid", True, 2.5)[0]
+        assert np.all(np.abs(got - [0, want, -want, 0]) <= want * 2.0 ** -40)
+
+
 def test_scores_reject_bad_args(lib):
     f = lib.moe_router_scores
 
