@@ -158,8 +158,9 @@ int32_t moe_route_logits(const float* logits, int32_t T, int32_t num_experts_glo
  *     the topk_group best groups stay;
  *   ids: the k largest choices of the groups that stay, in descending order; ties, of groups and of
  *     experts, go to the lower index;
- *   weights: fl32(scale * s / S), S = the sum of the k chosen scores with renormalize, else 1
- *     (0 where S is 0).
+ *   weights: fl32(scale * s / S), S = the sum of the k chosen scores with renormalize, else 1.  s / S is
+ *     the ratio of the scores' exact values, also where they underflow float64 (chosen experts far
+ *     below the largest logit, through the bias or the groups, or sigmoids of logits below -709).
  * A logit of -inf or NaN, and a choice of -inf or NaN, make an expert unavailable: it is never
  * chosen.  With fewer than k available, the remaining slots get id -1 and weight 0 (which
  * moe_route_permute drops).  +inf counts as the largest float.

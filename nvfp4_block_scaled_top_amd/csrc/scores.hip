@@ -7,7 +7,7 @@
 // group_top largest choices, the topk_group best groups stay, and the k largest choices among
 // their experts win (ties, of groups and of experts, go to the lower index).  The weights come
 // from the scores, without the bias: w_j = scale * s_j / S, S the sum over the winners
-// (renormalised) or 1.
+// (renormalised) or 1; s_j / S keeps its value where the scores underflow.
 //
 // The choice is float32 so that it is the same number in any implementation: float64 scores that
 // differ in their last bits round to the same float32 but for one pair in 2^29.
@@ -112,6 +112,17 @@ __device__ __forceinline__ uint32_t sort_key(float c) {
 }
 __device__ __forceinline__ float unsort_key(uint32_t u) {
   return __uint_as_float(u & 0x80000000u ? u & 0x7FFFFFFFu : ~u);
+}
+
+// A sum of chosen scores below this is taken of relative_score instead.
+constexpr double kFarScores = 0x1p-60;
+
+// e^(z - the largest z of the wave's chosen lanes), 0 for the others: chosen scores up to a common factor, where
+// the scores themselves lose bits or underflow.  Softmax scores are that, and so are sigmoids below 2^-60, which
+// are e^z to float64's last bit.
+__device__ __forceinline__ double relative_score(const ExpConstants& ec, float z, bool chosen) {
+  const uint32_t mk = dpp_reduce(chosen ? sort_key(z) : 0u, umax);
+  return chosen && z > -__builtin_huge_valf() ? exp_f64(ec, (double)z - (double)unsort_key(mk)) : 0.0;
 }
 
 // One wave per token.  The wave's lanes are split into equal power-of-two runs of `span` lanes, one
@@ -224,11 +235,19 @@ __global__ __launch_bounds__(kScoreWaves* kWave) void router_scores_kernel(Route
   }
   // The winners' weights, one lane each.
   double ws = 0.0;
+  float wz = kNone;
   if (my_id >= 0) {
-    const float wz = logit_of(row[my_id]);
+    wz = logit_of(row[my_id]);
     ws = sigmoid ? sigmoid_f64(ec, wz) : exp_f64(ec, (double)wz - m) * inv;
   }
-  const double d = p.renormalize ? score_wave_sum(ws) : 1.0;
+  double d = 1.0;
+  if (p.renormalize) {
+    d = score_wave_sum(ws);
+    if (d < kFarScores) {  // the bias or the groups left only experts far below the others
+      ws = relative_score(ec, wz, my_id >= 0);
+      d = score_wave_sum(ws);
+    }
+  }
   if (lane < p.k) {
     p.ids[(int64_t)t * p.k + lane] = my_id;
     p.weights[(int64_t)t * p.k + lane] = d > 0.0 ? (float)(ws * (double)p.scale / d) : 0.0f;
@@ -297,12 +316,6 @@ __device__ __forceinline__ uint16_t read_lane(uint16_t v, int lane) {
   return (uint16_t)__builtin_amdgcn_readlane((int)v, lane);
 }
 
-// e^(z - the largest z of the wave's chosen lanes), 0 for the others.
-__device__ __forceinline__ double relative_score(const ExpConstants& ec, float z, bool chosen) {
-  const uint32_t mk = dpp_reduce(chosen ? sort_key(z) : 0u, umax);
-  return chosen && z > -__builtin_huge_valf() ? exp_f64(ec, (double)z - (double)unsort_key(mk)) : 0.0;
-}
-
 template <typename T, int PL>
 __global__ __launch_bounds__(kScoreWaves* kWave) void router_scores_bwd_kernel(RouterScoreBwdArgs p) {
   const int lane = lane_id();
@@ -356,8 +369,7 @@ __global__ __launch_bounds__(kScoreWaves* kWave) void router_scores_bwd_kernel(R
   }
   if (p.renormalize) {
     double S = sigmoid ? score_wave_sum(sj) : 0.0;
-    // Sigmoids below 2^-60 are e^z to float64's last bit.
-    if (S < 0x1p-60) {
+    if (S < kFarScores) {
       sj = relative_score(ec, zj, id >= 0);
       S = score_wave_sum(sj);
     }

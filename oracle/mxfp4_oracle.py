@@ -87,7 +87,7 @@ def scores(logits: np.ndarray, kind: str) -> np.ndarray:
 
 def router(logits, k, bias=None, score="sigmoid", n_group=1, topk_group=1, group_top=2, renormalize=True, scale=1.0):
     """ids int32 [T, k] (-1: none available) and weights float64 [T, k], one token at a time."""
-    s = scores(logits, score)
+    z, s = finite_logits(logits), scores(logits, score)
     T, E = s.shape
     c = s.astype(np.float32)
     if bias is not None:
@@ -107,10 +107,8 @@ def router(logits, k, bias=None, score="sigmoid", n_group=1, topk_group=1, group
             kept = {g for _, g in sorted(by_group)[:topk_group]}
             live = [e for e in live if e // size in kept]
         win = sorted(live, key=lambda e: (-c[t, e], e))[:k]
-        total = sum(s[t, e] for e in win) if renormalize else 1.0
-        for j, e in enumerate(win):
-            ids[t, j] = e
-            w[t, j] = scale * s[t, e] / total if total > 0 else 0.0
+        ids[t, :len(win)] = win
+        w[t, :len(win)] = scale * (shares(z[t, win], score) if renormalize else s[t, win])
     return ids, w
 
 

@@ -271,6 +271,21 @@ def far_rows(seed, dtype):
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+def test_renormalized_weights_far_from_the_largest_logit(score, dtype):
+    """A bias of a row's own forces its experts, so a token a call."""
+    z, ids = far_rows(20, dtype)
+    if score == "sigmoid":
+        z[:, 0] = -1.0
+    for t in range(len(z)):
+        bias = np.zeros(40, np.float32)
+        bias[ids[t]] = 100.0 - np.arange(5)
+        got, w = check(z[t:t + 1], 5, bias, dtype, score=score, renormalize=True, scale=2.5)
+        assert np.array_equal(got[0], ids[t]) and abs(w.sum() - 2.5) <= 5 * 2.5 * 2.0 ** -24
+        check(z[t:t + 1], 5, bias, dtype, score=score, renormalize=False, scale=2.5)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
 def test_renormalized_gradient_far_from_the_largest_logit(score, dtype):
     """Within one rounding of scale * n_j (g_j - sum g n) f_j, f_j <= 1, whose shares n_j of either side are off by
     less than 2^-42 of themselves (an exponent of at most 800 in float64, and sums of 5)."""

@@ -105,6 +105,18 @@ def test_oracle_gradient_far_from_the_largest_logit(far):
         assert np.all(np.abs(got - [0, want, -want, 0]) <= want * 2.0 ** -40)
 
 
+@pytest.mark.parametrize("far", FAR)
+def test_oracle_weights_far_from_the_largest_logit(far):
+    """A bias that forces two experts, `far` below the row's largest logit (softmax) or 0 (sigmoid)."""
+    z = np.array([[0.0, far - 1.0, far - 1.75, -3.0]], np.float32)
+    bias = np.array([0, 5, 4, 0], np.float32)
+    n = 1 / (1 + np.exp(float(z[0, 2]) - float(z[0, 1])))
+    for score in ("softmax", "sigmoid") if far <= -40.0 else ("softmax",):
+        ids, w = X.router(z, 2, bias, score, scale=2.5)
+        assert ids.tolist() == [[1, 2]]
+        assert np.all(np.abs(w[0] - [2.5 * n, 2.5 * (1 - n)]) <= 2.5 * 2.0 ** -40)
+
+
 def test_scores_reject_bad_args(lib):
     f = lib.moe_router_scores
 
