@@ -300,7 +300,8 @@ hipError_t launch_router_scores(const RouterScoreArgs& a0, int dtype, hipStream_
 // Renormalised, sum_j g'_j s_j = 0: a softmax's gradient is then that of a softmax over the chosen experts
 // alone and 0 elsewhere, the other logits are not read, and only ratios of chosen scores remain, which
 // relative_score gives at any distance from the row's largest logit.
-// float64 up to the one rounding of dz.  One wave per token, lane l holding experts l + 64 i; the
+// float64 up to the one rounding of dz; 1 - s_e = sigmoid(-z_e) is not subtracted, which would leave no correct bit
+// from z = 37 on.  One wave per token, lane l holding experts l + 64 i; the
 // chosen experts' scores are computed one per lane.
 template <typename T>
 __device__ __forceinline__ T round_logit(double v);
@@ -359,11 +360,12 @@ __global__ __launch_bounds__(kScoreWaves* kWave) void router_scores_bwd_kernel(R
     sum = score_wave_sum(sum);
     inv = sum > 0.0 ? 1.0 / sum : 0.0;
   }
-  double sj = 0.0, cj = 1.0;  // score of this lane's chosen expert; sigmoid: 1 minus it
+  double sj = 0.0, cj = 1.0;  // score of this lane's chosen expert; sigmoid: 1 minus it (of bits of its own)
   const float zj = id >= 0 ? logit_of(row[id]) : -__builtin_huge_valf();
   if (sigmoid) {
-    sj = sigmoid_f64(ec, zj);
-    cj = 1.0 - sj;
+    const double e = exp_f64(ec, -fabs((double)zj)), y = reciprocal_f64(1.0 + e);
+    sj = zj < 0.0f ? e * y : y;
+    cj = zj < 0.0f ? y : e * y;
   } else if (every) {
     sj = zj > -__builtin_huge_valf() ? exp_f64(ec, (double)zj - m) * inv : 0.0;
   }

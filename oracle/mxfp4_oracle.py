@@ -129,7 +129,8 @@ def router_bwd(logits, ids, grad, score="sigmoid", renormalize=True, scale=1.0):
         else:
             part = scale * g * s[t, [e for _, e in at]]
         if score == "sigmoid":
-            part = part * (1 - s[t, [e for _, e in at]])
+            with np.errstate(over="ignore"):
+                part = part / (1 + np.exp(z[t, [e for _, e in at]]))  # 1 - s, without the loss of a subtraction
         elif not renormalize:
             out[t] = -s[t] * part.sum()
         for (_, e), d in zip(at, part):

@@ -314,6 +314,31 @@ def test_renormalized_gradient_far_from_the_largest_logit(score, dtype):
     assert np.all(got[~named] == 0)
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_sigmoid_gradient_of_large_logits(dtype):
+    """grad * s (1 - s) has no cancellation of its own: one rounding, and 2^-40 for the two sides' float64.
+    Renormalised, g_j - sum g n may cancel: 2^-40 of what is subtracted."""
+    z = np.concatenate([np.arange(-64, 65), [-705.0, -100.0, 72.5, 88.0, 100.0, 705.0, 1e30, -1e30]])
+    z = torch.from_numpy(np.tile(z, (3, 1)).astype(np.float32)).to(dtype).float().numpy()
+    rng = np.random.default_rng(14)
+    ids = np.concatenate([rng.permutation(z.shape[1]), [0] * 55])[:192].reshape(3, 64).astype(np.int32)
+    grad = rng.standard_normal(ids.shape).astype(np.float32)
+    half, tiny = (2.0 ** -24, F32_TINY) if dtype == torch.float32 else (2.0 ** -8, 2.0 ** -134)
+    for rows in (slice(0, 2), slice(2, 3)):  # ids named once; one of them named often
+        for renormalize in (False, True):
+            kw = dict(score="sigmoid", renormalize=renormalize, scale=2.5)
+            out, zh, _ = run_bwd(z[rows], ids[rows], grad[rows], dtype, **kw)
+            got, ref = out.float().cpu().numpy().astype(np.float64), X.router_bwd(zh, ids[rows], grad[rows], **kw)
+            size = np.zeros_like(ref)
+            with np.errstate(over="ignore"):
+                slope = X.scores(zh, "sigmoid") / (1 + np.exp(zh.astype(np.float64)))
+            for t, at in enumerate(ids[rows]):
+                s = X.scores(zh[t:t + 1], "sigmoid")[0, at]
+                np.add.at(size[t], at, 2.5 * np.abs(grad[rows][t]) if not renormalize else
+                          2 * 2.5 * np.abs(grad[rows][t]).max() / s.sum())
+            assert np.all(np.abs(got - ref) <= np.abs(ref) * half + size * slope * 2.0 ** -40 + tiny)
+
+
 # ---- with the routing step -----------------------------------------------------------------------
 
 @pytest.mark.parametrize("T,P", [(0, 1), (1, 1), (8, 128), (700, 8)])

@@ -117,6 +117,15 @@ def test_oracle_weights_far_from_the_largest_logit(far):
         assert np.all(np.abs(w[0] - [2.5 * n, 2.5 * (1 - n)]) <= 2.5 * 2.0 ** -40)
 
 
+def test_oracle_sigmoid_gradient_of_large_logits():
+    """s (1 - s) = 1 / (2 cosh(z / 2))^2."""
+    z = np.array([[-60.0, -20, -1, 0, 1, 20, 30, 36, 37, 40, 60, 100, 700]])
+    ids = np.arange(z.shape[1])[None]
+    got = X.router_bwd(z, ids, np.ones(ids.shape), "sigmoid", False, 1.0)
+    want = 1 / (2 * np.cosh(z / 2)) ** 2
+    assert np.all(np.abs(got - want) <= want * 2.0 ** -40)
+
+
 def test_scores_reject_bad_args(lib):
     f = lib.moe_router_scores
 
