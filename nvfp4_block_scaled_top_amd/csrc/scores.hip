@@ -300,8 +300,10 @@ hipError_t launch_router_scores(const RouterScoreArgs& a0, int dtype, hipStream_
 // Renormalised, sum_j g'_j s_j = 0: a softmax's gradient is then that of a softmax over the chosen experts
 // alone and 0 elsewhere, the other logits are not read, and only ratios of chosen scores remain, which
 // relative_score gives at any distance from the row's largest logit.
-// float64 up to the one rounding of dz; 1 - s_e = sigmoid(-z_e) is not subtracted, which would leave no correct bit
-// from z = 37 on.  One wave per token, lane l holding experts l + 64 i; the
+// float64 up to the one rounding of dz, and 1 - s_e never by a subtraction, which would leave no correct bit from
+// z = 37 on (or such a distance to a softmax's other logits): for a sigmoid it is sigmoid(-z_e), and a
+// softmax's g'_e - sum_j g'_j s_j is taken relative to the expert x of the largest logit, the only one whose score
+// may be near 1, as (g'_e - g'_x) - sum_{i != x} (g'_i - g'_x) s_i.  One wave per token, lane l holding experts l + 64 i; the
 // chosen experts' scores are computed one per lane.
 template <typename T>
 __device__ __forceinline__ T round_logit(double v);
@@ -337,7 +339,8 @@ __global__ __launch_bounds__(kScoreWaves* kWave) void router_scores_bwd_kernel(R
   }
   const ExpConstants ec = exp_constants();
   double s[PL];
-  double m = 0.0, inv = 1.0;
+  double m = 0.0, inv = 1.0, rest = 0.0;  // softmax: largest logit, one over the sum, the sum but for the largest
+  int x = 0;                              // the expert of the largest logit
   if (every) {
     const float kNone = -__builtin_huge_valf();
     float z[PL];
@@ -350,15 +353,19 @@ __global__ __launch_bounds__(kScoreWaves* kWave) void router_scores_bwd_kernel(R
       z[i] = lane + kWave * i < p.E ? logit_of(raw[i]) : kNone;
       mk = umax(mk, sort_key(z[i]));
     }
-    m = (double)unsort_key(dpp_reduce(mk, umax));
-    double sum = 0.0;
+    const uint32_t top = dpp_reduce(mk, umax);
+    const float mz = unsort_key(top);
+    m = (double)mz;
+#pragma unroll
+    for (int i = PL - 1; i >= 0; --i) x = z[i] == mz ? lane + kWave * i : x;
+    x = __builtin_amdgcn_readlane(x, __builtin_ctzll(__ballot(mk == top)));
 #pragma unroll
     for (int i = 0; i < PL; ++i) {
       s[i] = z[i] > kNone ? exp_f64(ec, (double)z[i] - m) : 0.0;
-      sum += s[i];
+      rest += lane + kWave * i == x ? 0.0 : s[i];
     }
-    sum = score_wave_sum(sum);
-    inv = sum > 0.0 ? 1.0 / sum : 0.0;
+    rest = score_wave_sum(rest);
+    inv = mz > kNone ? 1.0 / (1.0 + rest) : 0.0;
   }
   double sj = 0.0, cj = 1.0;  // score of this lane's chosen expert; sigmoid: 1 minus it (of bits of its own)
   const float zj = id >= 0 ? logit_of(row[id]) : -__builtin_huge_valf();
@@ -379,17 +386,22 @@ __global__ __launch_bounds__(kScoreWaves* kWave) void router_scores_bwd_kernel(R
     const double rS = S > 0.0 ? 1.0 / S : 0.0;
     g = id >= 0 ? (g - gs * rS) * rS : 0.0;
   }
-  const double dot = every ? score_wave_sum(g * sj) : 0.0;
   // g'_e of this lane's expert: the slots that name it, in slot order; then its gradient.
   double ge = 0.0;
   for (int j = 0; j < p.k; ++j) {
     const double gj = read_lane(g, j);
     ge += __builtin_amdgcn_readlane(id, j) == id ? gj : 0.0;
   }
-  const T mine = round_logit<T>(sigmoid ? ge * sj * cj : sj * (ge - dot));
+  double gx = 0.0, dot = 0.0;  // g'_x and sum_{i != x} (g'_i - g'_x) s_i
+  if (every) {
+    const uint64_t named = __ballot(id == x);
+    if (named) gx = read_lane(ge, __builtin_ctzll(named));
+    dot = score_wave_sum(id == x ? 0.0 : g * sj) - gx * (rest * inv);
+  }
+  const T mine = round_logit<T>(sigmoid ? ge * sj * cj : sj * (ge - gx - dot));
   T v[PL];
 #pragma unroll
-  for (int i = 0; i < PL; ++i) v[i] = round_logit<T>(every ? -(s[i] * inv * dot) : 0.0);
+  for (int i = 0; i < PL; ++i) v[i] = round_logit<T>(every ? -(s[i] * inv * (gx + dot)) : 0.0);
   for (int j = 0; j < p.k; ++j) {
     const int ej = __builtin_amdgcn_readlane(id, j);  // -1 is no expert: -1 / 64 is no i
     const T vj = read_lane(mine, j);

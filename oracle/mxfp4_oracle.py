@@ -127,12 +127,15 @@ def router_bwd(logits, ids, grad, score="sigmoid", renormalize=True, scale=1.0):
             n = shares(z[t, [e for _, e in at]], score)
             part = scale * n * (g - (g * n).sum())
         else:
-            part = scale * g * s[t, [e for _, e in at]]
+            part = scale * g
+            if score == "softmax":  # s_e (G_e - sum_i s_i G_i), as a sum of what does not cancel
+                G = np.zeros(s.shape[1])
+                np.add.at(G, [e for _, e in at], part)
+                out[t] = s[t] * (s[t] * (G[:, None] - G)).sum(1)
+                continue
+            part = part * s[t, [e for _, e in at]]
         if score == "sigmoid":
             with np.errstate(over="ignore"):
                 part = part / (1 + np.exp(z[t, [e for _, e in at]]))  # 1 - s, without the loss of a subtraction
-        elif not renormalize:
-            out[t] = -s[t] * part.sum()
-        for (_, e), d in zip(at, part):
-            out[t, e] += d
+        np.add.at(out[t], [e for _, e in at], part)
     return out

@@ -339,6 +339,41 @@ def test_sigmoid_gradient_of_large_logits(dtype):
             assert np.all(np.abs(got - ref) <= np.abs(ref) * half + size * slope * 2.0 ** -40 + tiny)
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("E,k", [(2, 1), (40, 1), (40, 5), (300, 8), (1024, 3)])
+def test_softmax_gradient_of_a_dominant_expert(E, k, dtype):
+    """One logit up to 700 above the others, named by the slots or not, once or twice, or shared by two experts.
+    With x its expert and G the slots' gradients by expert: s_e ((G_e - G_x) - sum_{i != x} (G_i - G_x) s_i), one
+    rounding, and 2^-40 of what is summed."""
+    rng = np.random.default_rng(E + k)
+    gaps = [0.0, 5.0, 20.0, 30.0, 36.0, 37.0, 38.0, 50.0, 80.0, 100.0, 700.0]
+    z = rng.standard_normal((4 * len(gaps), E))
+    x = rng.integers(0, E, len(z))
+    ids = np.stack([rng.permutation(E)[:k] for _ in z]).astype(np.int32)
+    for t in range(len(z)):
+        z[t] -= z[t].max() + gaps[t // 4]
+        z[t, x[t]] = 0.5
+        if t % 4 < 3:
+            ids[t, 0] = x[t]
+        if t % 4 == 1:
+            ids[t, k - 1] = x[t]
+        if t % 4 == 2:
+            z[t, (x[t] + 1) % E] = 0.5
+    grad = rng.standard_normal(ids.shape).astype(np.float32)
+    kw = dict(score="softmax", renormalize=False, scale=2.5)
+    out, zh, _ = run_bwd(z, ids, grad, dtype, **kw)
+    got, ref = out.float().cpu().numpy().astype(np.float64), X.router_bwd(zh, ids, grad, **kw)
+    half, tiny = (2.0 ** -24, F32_TINY) if dtype == torch.float32 else (2.0 ** -8, 2.0 ** -134)
+    s, G = X.scores(zh, "softmax"), np.zeros_like(ref)
+    for t, at in enumerate(ids):
+        np.add.at(G[t], at, 2.5 * grad[t].astype(np.float64))
+    top = zh.argmax(1)[:, None]
+    Gx, sx = np.take_along_axis(G, top, 1), np.copy(s)
+    np.put_along_axis(sx, top, 0.0, 1)
+    size = s * (np.abs(G - Gx) + (sx * (np.abs(G) + np.abs(Gx))).sum(1, keepdims=True))
+    assert np.all(np.abs(got - ref) <= np.abs(ref) * half + size * 2.0 ** -40 + tiny)
+
+
 # ---- with the routing step -----------------------------------------------------------------------
 
 @pytest.mark.parametrize("T,P", [(0, 1), (1, 1), (8, 128), (700, 8)])

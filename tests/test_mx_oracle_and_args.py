@@ -126,6 +126,14 @@ def test_oracle_sigmoid_gradient_of_large_logits():
     assert np.all(np.abs(got - want) <= want * 2.0 ** -40)
 
 
+@pytest.mark.parametrize("gap", [0.0, 20.0, 37.0, 60.0, 700.0])
+def test_oracle_softmax_gradient_of_a_dominant_expert(gap):
+    """Two experts: s_0 (1 - s_0) = 1 / (2 cosh(gap / 2))^2, of either sign."""
+    got = X.router_bwd(np.array([[0.0, -gap]]), np.array([[0]]), np.array([[1.0]]), "softmax", False, 1.0)[0]
+    want = 1 / (2 * np.cosh(gap / 2)) ** 2
+    assert np.all(np.abs(got - [want, -want]) <= want * 2.0 ** -40)
+
+
 def test_scores_reject_bad_args(lib):
     f = lib.moe_router_scores
 
