@@ -633,8 +633,8 @@ int32_t mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t ro
  * a_codes/a_scales   MXFP4 A [M, K/2], [M, K/32] (e.g. from mxfp4_quantize_act).
  * w_codes/w_scales   [N, K/2], [N, K/32];  w13 [2I, K/2], [2I, K/32], rows 0..I-1 gate, I..2I-1 up.
  * out_bf16 bf16 [M, N];  h_bf16 bf16 [M, I].
- * Limits: 0 <= M < 2^31, K >= 128 and a multiple of 128, N and I >= 16 and multiples of 16, below
- * 2^30; A's codes and W's below 2^36 bytes each; codes and outputs aligned to 16 bytes, scales to 4.
+ * Limits: 0 <= M < 2^31, K >= 128 and a multiple of 128, N and I >= 16 and multiples of 16, all three
+ * below 2^30; A's codes and W's below 2^36 bytes each; codes and outputs aligned to 16 bytes, scales to 4.
  * With M == 0 the call enqueues nothing.
  * ---------------------------------------------------------------------------------------- */
 int32_t mxfp4_linear(const uint8_t* a_codes, const uint8_t* a_scales, int64_t M, int32_t K,
@@ -663,7 +663,7 @@ int32_t mxfp4_linear_gate_up_silu(const uint8_t* a_codes, const uint8_t* a_scale
  *              low costs time only.
  * h_bf16 bf16 [M_cap, I];  y_bf16 bf16 [M_cap, H].
  * Limits: E as for moe_route_permute; the reduced dimension (H for L1, I for L2) a multiple of 128,
- * the output dimension a multiple of 16; M_cap rows of codes, and one expert's codes, below 2^36 bytes;
+ * the output dimension a multiple of 16, both below 2^30; M_cap rows of codes, and one expert's codes, below 2^36 bytes;
  * alignment as for mxfp4_linear.  With M_cap == 0 the row arrays may be NULL and the call enqueues nothing.
  * ---------------------------------------------------------------------------------------- */
 int32_t moe_grouped_gemm_l1_silu_mxfp4(const uint8_t* x_codes, const uint8_t* x_scales,

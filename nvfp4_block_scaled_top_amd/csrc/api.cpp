@@ -664,8 +664,9 @@ int32_t mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t ro
 
 // Checks and launch shared by the four MXFP4 products.  rows: rows of the output buffer.
 static int32_t mx_gemm(const MxGemmArgs& a, bool l1, int64_t rows, int32_t max_rows_per_expert, void* stream) {
-  if (a.E < 1 || a.E > MEGAMOE_MAX_EXPERTS || a.K < 128 || a.K % 128 != 0 || a.N < 16 || a.N % 16 != 0 ||
-      a.N >= (1 << 30) || rows < 0 || rows >= (int64_t)1 << 31 || max_rows_per_expert < 0)
+  // K < 2^30: the kernels round K up to their stages in 32 bits and add 7 rows of K / 2 bytes to an address in as many
+  if (a.E < 1 || a.E > MEGAMOE_MAX_EXPERTS || a.K < 128 || a.K % 128 != 0 || a.K >= (1 << 30) || a.N < 16 ||
+      a.N % 16 != 0 || a.N >= (1 << 30) || rows < 0 || rows >= (int64_t)1 << 31 || max_rows_per_expert < 0)
     return MEGAMOE_ERR_SHAPE;
   // row offsets are 32-bit counts of 16 bytes (a token tensor has no more rows than the output)
   if (rows * (a.K / 2) >= (int64_t)1 << 36 || (l1 ? 2 : 1) * (int64_t)a.N * (a.K / 2) >= (int64_t)1 << 36)

@@ -212,6 +212,19 @@ def test_mxfp4_reject_bad_args(lib):
     assert l2(*a6, 8, 256, 128, 64, 0, None, None) == -1
 
 
+def test_mxfp4_products_refuse_reductions_of_2_30(lib):
+    """A lane's 32-bit offset of 7 weight rows of K / 2 bytes, and K rounded up to a stage, hold K below 2^30.
+    (Every operand here is below 2^36 bytes: K alone refuses the call.)"""
+    for K in (1 << 30, 1227133568, 2 ** 31 - 512, 2 ** 31 - 384, 2 ** 31 - 256, 2 ** 31 - 128):
+        assert lib.mxfp4_linear(FAKE, FAKE, 1, K, FAKE, FAKE, 16, FAKE, None) == -2
+        assert lib.mxfp4_linear_gate_up_silu(FAKE, FAKE, 1, K, FAKE, FAKE, 16, FAKE, None) == -2
+        assert lib.moe_grouped_gemm_l1_silu_mxfp4(*[FAKE] * 7, 8, K, 16, 1, 0, FAKE, None) == -2
+        assert lib.moe_grouped_gemm_l2_mxfp4(*[FAKE] * 6, 8, 16, K, 1, 0, FAKE, None) == -2
+    K = (1 << 30) - 128  # accepted: the next check is the first to refuse
+    assert 7 * (K // 2) + 16 * 8 < 2 ** 32 and K + 511 < 2 ** 31
+    assert lib.mxfp4_linear(FAKE, FAKE, 1, K, FAKE, None, 16, FAKE, None) == -1
+
+
 def test_binding_refuses_wrong_tensors():
     """The binding's own checks come before the library: type, shape, device."""
     z = torch.zeros(4, 8)
