@@ -663,8 +663,9 @@ int32_t mxfp4_linear_gate_up_silu(const uint8_t* a_codes, const uint8_t* a_scale
  *              low costs time only.
  * h_bf16 bf16 [M_cap, I];  y_bf16 bf16 [M_cap, H].
  * Limits: E as for moe_route_permute; the reduced dimension (H for L1, I for L2) a multiple of 128,
- * the output dimension a multiple of 16, both below 2^30; M_cap rows of codes, and one expert's codes, below 2^36 bytes;
- * alignment as for mxfp4_linear.  With M_cap == 0 the row arrays may be NULL and the call enqueues nothing.
+ * the output dimension a multiple of 16, both below 2^30; M_cap rows of codes, x_codes (T is not an
+ * argument: T <= M_cap with M_cap as above) and one expert's codes below 2^36 bytes each; alignment as for
+ * mxfp4_linear.  With M_cap == 0 the row arrays may be NULL and the call enqueues nothing.
  * ---------------------------------------------------------------------------------------- */
 int32_t moe_grouped_gemm_l1_silu_mxfp4(const uint8_t* x_codes, const uint8_t* x_scales,
                                        const int32_t* row_token, const int32_t* padded_offsets,

@@ -668,7 +668,7 @@ static int32_t mx_gemm(const MxGemmArgs& a, bool l1, int64_t rows, int32_t max_r
   if (a.E < 1 || a.E > MEGAMOE_MAX_EXPERTS || a.K < 128 || a.K % 128 != 0 || a.K >= (1 << 30) || a.N < 16 ||
       a.N % 16 != 0 || a.N >= (1 << 30) || rows < 0 || rows >= (int64_t)1 << 31 || max_rows_per_expert < 0)
     return MEGAMOE_ERR_SHAPE;
-  // row offsets are 32-bit counts of 16 bytes (a token tensor has no more rows than the output)
+  // row offsets are 32-bit counts of 16 bytes (a gathered token tensor's rows are at most M_cap)
   if (rows * (a.K / 2) >= (int64_t)1 << 36 || (l1 ? 2 : 1) * (int64_t)a.N * (a.K / 2) >= (int64_t)1 << 36)
     return MEGAMOE_ERR_SHAPE;
   if (!a.w_codes || !a.w_scales) return MEGAMOE_ERR_NULL;

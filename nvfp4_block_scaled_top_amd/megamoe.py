@@ -494,6 +494,8 @@ def moe_grouped_gemm_l1_silu_mxfp4(x_codes, x_scales, row_token, padded_offsets,
     T, Hh = x_codes.shape
     E, I2, _ = w13_codes.shape
     M_cap, I = h_bf16.shape
+    if T * Hh >= 1 << 36:  # row offsets are 32-bit counts of 16 bytes; the library is not told T
+        raise MegaMoEError(f"x_codes has {T * Hh} bytes, expected less than 2^36")
     dev, st = _on(x_codes, stream)
     _check("moe_grouped_gemm_l1_silu_mxfp4", lib().moe_grouped_gemm_l1_silu_mxfp4(
         _arg("x_codes", x_codes, _U8, (T, Hh), dev), _arg("x_scales", x_scales, _U8, (T, Hh // 16), dev),

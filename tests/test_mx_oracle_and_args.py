@@ -242,6 +242,21 @@ def test_binding_refuses_wrong_tensors():
         mm.mxfp4_quantize_act(z.half(), u8(4, 4), u8(4, 1))
 
 
+def test_binding_refuses_more_token_codes_than_offsets_reach():
+    """x of 2^36 bytes of codes beside an output of a few rows (meta tensors: nothing is allocated)."""
+    def meta(*s, d=torch.uint8):
+        return torch.empty(*s, dtype=d, device="meta")
+
+    def call(T, H=256):
+        mm.moe_grouped_gemm_l1_silu_mxfp4(meta(T, H // 2), meta(T, H // 32), meta(64, d=torch.int32), meta(5, d=torch.int32),
+                                          meta(4, d=torch.int32), meta(4, 256, H // 2), meta(4, 256, H // 32),
+                                          meta(64, 128, d=torch.bfloat16))
+    with pytest.raises(mm.MegaMoEError, match="2\\^36"):
+        call(1 << 29)
+    with pytest.raises(mm.MegaMoEError, match="GPU"):
+        call((1 << 29) - 1)
+
+
 def test_mx_layer_weight_shapes():
     w = layer.MXMoEWeights.empty(4, 256, 128, device="cpu")
     assert (w.num_experts, w.hidden, w.intermediate) == (4, 256, 128)
