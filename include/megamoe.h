@@ -172,7 +172,8 @@ int32_t moe_route_logits(const float* logits, int32_t T, int32_t num_experts_glo
  * topk_ids int32 [T, k];  topk_weights float32 [T, k].
  * Limits: 0 <= T, 1 <= num_experts_global <= MEGAMOE_ROUTER_MAX_EXPERTS, T*k < 2^31,
  * n_group <= MEGAMOE_ROUTER_MAX_GROUPS and a divisor of num_experts_global, topk_group <= n_group,
- * 1 <= k <= min(64, topk_group * num_experts_global / n_group), scale finite.
+ * 1 <= k <= min(64, topk_group * num_experts_global / n_group), scale finite; pointers aligned to their
+ * elements (logits 4 or 2 bytes, the others 4).
  * ---------------------------------------------------------------------------------------- */
 int32_t moe_router_scores(const void* logits, int32_t dtype, int32_t T, int32_t num_experts_global, int32_t k,
                           const float* bias, int32_t score, int32_t n_group, int32_t topk_group,

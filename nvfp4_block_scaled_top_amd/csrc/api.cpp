@@ -568,11 +568,11 @@ int32_t nvfp4_linear_gate_up_silu_nvfp4(const uint8_t* a_codes, const uint8_t* a
 
 static bool dtype_ok(int32_t d) { return d == MEGAMOE_DTYPE_BF16 || d == MEGAMOE_DTYPE_F32; }
 static bool score_ok(int32_t s) { return s == MEGAMOE_SCORE_SOFTMAX || s == MEGAMOE_SCORE_SIGMOID; }
-// The caller's pointers that kernels read or write in words wider than their elements.
 static bool aligned(const void* p, size_t to) { return reinterpret_cast<uintptr_t>(p) % to == 0; }
+static size_t dtype_bytes(int32_t d) { return d == MEGAMOE_DTYPE_F32 ? 4 : 2; }
 
-static int32_t scores_args_ok(const void* logits, int32_t dtype, int32_t T, int32_t Eg, int32_t k, int32_t score,
-                              int32_t n_group, int32_t topk_group, int32_t group_top, float scale,
+static int32_t scores_args_ok(const void* logits, int32_t dtype, int32_t T, int32_t Eg, int32_t k, const float* bias,
+                              int32_t score, int32_t n_group, int32_t topk_group, int32_t group_top, float scale,
                               const int32_t* topk_ids, const float* topk_weights) {
   if (!router_shape_ok(T, Eg, k) || !dtype_ok(dtype) || !score_ok(score)) return MEGAMOE_ERR_SHAPE;
   if (n_group < 1 || n_group > MEGAMOE_ROUTER_MAX_GROUPS || Eg % n_group != 0 || topk_group < 1 ||
@@ -580,14 +580,16 @@ static int32_t scores_args_ok(const void* logits, int32_t dtype, int32_t T, int3
       !std::isfinite(scale))
     return MEGAMOE_ERR_SHAPE;
   if (T > 0 && (!logits || !topk_ids || !topk_weights)) return MEGAMOE_ERR_NULL;
+  if (!aligned(logits, dtype_bytes(dtype)) || !aligned(bias, 4) || !aligned(topk_ids, 4) || !aligned(topk_weights, 4))
+    return MEGAMOE_ERR_ALIGN;
   return MEGAMOE_OK;
 }
 
 int32_t moe_router_scores(const void* logits, int32_t dtype, int32_t T, int32_t num_experts_global, int32_t k,
                           const float* bias, int32_t score, int32_t n_group, int32_t topk_group, int32_t group_top,
                           int32_t renormalize, float scale, int32_t* topk_ids, float* topk_weights, void* stream) {
-  const int32_t rc = scores_args_ok(logits, dtype, T, num_experts_global, k, score, n_group, topk_group, group_top,
-                                    scale, topk_ids, topk_weights);
+  const int32_t rc = scores_args_ok(logits, dtype, T, num_experts_global, k, bias, score, n_group, topk_group,
+                                    group_top, scale, topk_ids, topk_weights);
   if (rc != MEGAMOE_OK) return rc;
   const int32_t dev = check_device();
   if (dev != MEGAMOE_OK) return dev;
@@ -602,8 +604,8 @@ int32_t moe_route_scores(const void* logits, int32_t dtype, int32_t T, int32_t n
                          int32_t pad_multiple, int32_t block_m_override, int32_t* topk_ids, float* topk_weights,
                          int32_t* counts, int32_t* expert_offsets, int32_t* padded_offsets, int32_t* row_token,
                          int32_t* token_rows, int32_t* sched, void* workspace, size_t workspace_bytes, void* stream) {
-  int32_t rc = scores_args_ok(logits, dtype, T, num_experts_global, k, score, n_group, topk_group, group_top, scale,
-                              topk_ids, topk_weights);
+  int32_t rc = scores_args_ok(logits, dtype, T, num_experts_global, k, bias, score, n_group, topk_group, group_top,
+                              scale, topk_ids, topk_weights);
   if (rc != MEGAMOE_OK) return rc;
   rc = route_args_ok(T, k, expert_begin, num_experts, pad_multiple, block_m_override, topk_ids, counts,
                      expert_offsets, padded_offsets, row_token, token_rows, sched, workspace, workspace_bytes);
@@ -627,6 +629,9 @@ int32_t moe_router_scores_bwd(const void* logits, int32_t dtype, int32_t T, int3
   if (!router_shape_ok(T, num_experts_global, k) || !dtype_ok(dtype) || !score_ok(score) || !std::isfinite(scale))
     return MEGAMOE_ERR_SHAPE;
   if (T > 0 && (!logits || !topk_ids || !grad_weights || !grad_logits)) return MEGAMOE_ERR_NULL;
+  if (!aligned(logits, dtype_bytes(dtype)) || !aligned(topk_ids, 4) || !aligned(grad_weights, 4) ||
+      !aligned(grad_logits, dtype_bytes(dtype)))
+    return MEGAMOE_ERR_ALIGN;
   const int32_t dev = check_device();
   if (dev != MEGAMOE_OK) return dev;
   const RouterScoreBwdArgs a{logits, T, num_experts_global, k, score, renormalize != 0, scale, topk_ids, grad_weights,

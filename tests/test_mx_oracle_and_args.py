@@ -167,6 +167,29 @@ def test_scores_reject_bad_args(lib):
     assert r(None, 1, 4, 384, 6, None, 1, 8, 4, 2, 1, 1.0, 0, 48, 1, 0, FAKE, FAKE, *ok, FAKE, 4096, None) == -1
 
 
+def test_scores_reject_misaligned_pointers(lib):
+    """Every array at its elements' alignment: 4 bytes, 2 for bf16 logits."""
+    def fwd(logits=FAKE, dtype=1, bias=FAKE, ids=FAKE, w=FAKE):
+        return lib.moe_router_scores(logits, dtype, 4, 384, 6, bias, 1, 8, 4, 2, 1, 1.0, ids, w, None)
+
+    def route(logits=FAKE, dtype=1, bias=FAKE, ids=FAKE, w=FAKE):
+        return lib.moe_route_scores(logits, dtype, 4, 384, 6, bias, 1, 8, 4, 2, 1, 1.0, 0, 48, 1, 0, ids, w, *[FAKE] * 6,
+                                    FAKE, 4096, None)
+
+    def bwd(logits=FAKE, dtype=1, ids=FAKE, grad=FAKE, out=FAKE):
+        return lib.moe_router_scores_bwd(logits, dtype, 4, 384, 6, 1, 1, 1.0, ids, grad, out, None)
+
+    for f in (fwd, route):
+        for name in ("logits", "bias", "ids", "w"):
+            assert f(**{name: ODD}) == -6 and f(dtype=0, **{name: FAKE + 1}) == -6
+    for name in ("logits", "ids", "grad", "out"):
+        assert bwd(**{name: ODD}) == -6 and bwd(dtype=0, **{name: FAKE + 1}) == -6
+    # bf16 logits at 2 bytes: the next check is the first to refuse
+    assert lib.moe_router_scores(ODD, 0, 4, 384, 6, None, 1, 8, 4, 2, 1, 1.0, FAKE, ODD, None) == -6
+    assert lib.moe_route_scores(ODD, 0, 4, 384, 6, None, 1, 8, 4, 2, 1, 1.0, 0, 0, 1, 0, FAKE, FAKE, *[FAKE] * 6, FAKE,
+                                4096, None) == -2
+
+
 def test_mxfp4_reject_bad_args(lib):
     q, d = lib.mxfp4_quantize_act, lib.mxfp4_dequantize
     assert q(FAKE, 0, 4, 48, None, FAKE, FAKE, None) == -2     # cols % 32
