@@ -154,8 +154,8 @@ int32_t moe_route_logits(const float* logits, int32_t T, int32_t num_experts_glo
  *   s_e = sigmoid(z_e), or softmax over all num_experts_global experts, in float64;
  *   c_e = fl32(s_e) + bias_e in float32 (the choice; the bias steers the choice alone);
  *   groups: the experts lie in n_group groups of num_experts_global / n_group consecutive ids; a
- *     group's score is the float32 sum of its group_top largest choices (of those there are);
- *     the topk_group best groups stay;
+ *     group's score is the float32 sum of its group_top largest choices (of those there are); the
+ *     topk_group best groups stay, those without an available expert after all others;
  *   ids: the k largest choices of the groups that stay, in descending order; ties, of groups and of
  *     experts, go to the lower index;
  *   weights: fl32(scale * s / S), S = the sum of the k chosen scores with renormalize, else 1.  s / S is

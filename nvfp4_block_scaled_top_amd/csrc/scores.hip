@@ -193,13 +193,13 @@ __global__ __launch_bounds__(kScoreWaves* kWave) void router_scores_kernel(Route
       k1 = umax(o1, k1);
       k2 = umax(lo, umax(o2, k2));
     }
-    // A group without an available expert comes after every other one.
-    float gs = k1 ? unsort_key(k1) : kNone;
-    if (p.group_top > 1 && k2) gs += unsort_key(k2);
+    // A group without an available expert has key 0 and comes after every other one, also after a sum that
+    // overflows to -inf.
+    const uint32_t gk = p.group_top > 1 && k2 ? sort_key(unsort_key(k1) + unsort_key(k2)) : k1;
     int rank = 0;
     for (int g = 0; g < p.n_group; ++g) {
-      const float og = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(gs), g << p.span_log2));
-      rank += (og > gs || (og == gs && g < q)) ? 1 : 0;
+      const uint32_t og = (uint32_t)__builtin_amdgcn_readlane((int)gk, g << p.span_log2);
+      rank += (og > gk || (og == gk && g < q)) ? 1 : 0;
     }
     if (rank >= p.topk_group) {
 #pragma unroll

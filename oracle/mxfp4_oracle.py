@@ -102,9 +102,10 @@ def router(logits, k, bias=None, score="sigmoid", n_group=1, topk_group=1, group
             by_group = []
             for g in range(n_group):
                 best = sorted((c[t, e] for e in live if e // size == g), reverse=True)[:group_top]
-                total = np.float32(-np.inf) if not best else best[0] if len(best) == 1 else np.float32(best[0] + best[1])
-                by_group.append((-total, g))
-            kept = {g for _, g in sorted(by_group)[:topk_group]}
+                with np.errstate(over="ignore"):
+                    total = np.float32(0) if not best else best[0] if len(best) == 1 else np.float32(best[0] + best[1])
+                by_group.append((not best, -total, g))  # groups without an available expert come last
+            kept = {g for *_, g in sorted(by_group)[:topk_group]}
             live = [e for e in live if e // size in kept]
         win = sorted(live, key=lambda e: (-c[t, e], e))[:k]
         ids[t, :len(win)] = win

@@ -96,6 +96,23 @@ def test_masks_and_extremes(score):
                 check(z, k, b, score=score, renormalize=renorm, **groups)
 
 
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("group_top", [1, 2])
+def test_groups_of_choices_at_the_ends_of_float32(score, group_top):
+    """Sums of a group's choices that overflow to either infinity, beside groups with no available expert
+    (before them, after them and between them) and groups with a single one."""
+    rng = np.random.default_rng(17)
+    E, low = 48, np.float32(-3e38)
+    z = rng.standard_normal((12, E)).astype(np.float32)
+    for t in range(12):
+        z[t, 8 * (t % 6):8 * (t % 6) + 8] = -np.inf
+        z[t, 8 * (t // 3):8 * (t // 3) + (8 if t % 2 else 7)] = -np.inf
+    for bias in (np.full(E, low), np.full(E, -low), np.where(np.arange(E) % 16 < 8, low, np.float32(-1e-3)),
+                 np.where(np.arange(E) % 8 < 7, low, np.float32(0)), np.full(E, np.finfo(np.float32).min)):
+        for topk_group in (1, 2, 4):
+            check(z, 5, bias.astype(np.float32), score=score, n_group=6, topk_group=topk_group, group_top=group_top)
+
+
 def test_large_batch_matches_oracle_on_samples_and_is_repeatable():
     rng = np.random.default_rng(5)
     z = rng.standard_normal((8192, 384)).astype(np.float32)

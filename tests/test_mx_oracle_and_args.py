@@ -85,6 +85,16 @@ def test_oracle_router_masks():
     assert w[0].tolist() == [0, 0, 0] and w[1].tolist() == [0.5, 0.5, 0]
 
 
+def test_oracle_router_group_sums_that_overflow():
+    """A group whose sum of choices is -inf in float32 is still before one without an available expert."""
+    z = np.zeros((1, 12), np.float32)
+    z[0, :4] = -np.inf
+    bias = np.full(12, -3e38, np.float32)
+    for top, want in ((2, [4, 5]), (1, [4, 5])):
+        ids, w = X.router(z, 2, bias, "sigmoid", 3, 1, top)
+        assert ids.tolist() == [want] and w.tolist() == [[0.5, 0.5]]
+
+
 FAR = [0.0, -40.0, -700.0, -709.0, -720.0, -744.0, -746.0, -1e4, -1e30]
 
 
