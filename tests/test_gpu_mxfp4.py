@@ -363,6 +363,71 @@ def test_experts(i, bound):
     assert np.all(hg[free] == 7.0) and np.all(yg[free] == 7.0)  # rows without an assignment: as they were
 
 
+def random_operand(rng, *shape):
+    """Any codes under scales over six binades around 2^-5: sums of a few units at the lengths used here."""
+    *rows, K = shape
+    return rng.integers(0, 256, (*rows, K // 2), dtype=np.uint8), rng.integers(119, 125, (*rows, K // 32), dtype=np.uint8)
+
+
+# Reductions that the small kernel splits over its waves, with m-tiles of 16, 8 and 4 token rows.  With some 20
+# m-tiles of 17 or 18 groups a workgroup has more than one group, and many cross into the next m-tile or expert
+# (empty ones between them).
+LONG = [
+    (2688, [3, 0, 16, 1, 0, 0, 15, 16, 9, 5, 16, 0, 1, 12, 16, 33, 7, 16, 0, 2, 40]),
+    (2816, [16] * 12 + [0] * 70 + [15, 0, 1] * 3 + [17]),
+    (7168, [1, 16, 0, 15, 4, 0, 0, 16, 16, 31, 2, 8, 16, 0, 5, 16, 1, 20, 16]),
+    (12288, [8, 1, 0, 15, 16, 0, 9, 7, 16, 3, 25, 0, 16, 16, 1]),
+    (24576, [4, 0, 1, 15, 16, 3, 0, 5, 16, 18, 2]),
+]
+
+
+@pytest.mark.parametrize("bound", [0, 1])
+@pytest.mark.parametrize("K,counts", LONG, ids=[str(K) for K, _ in LONG])
+def test_experts_long_reductions(K, counts, bound):
+    rng = np.random.default_rng(K)
+    counts = np.array(counts, np.int32)
+    E, T, I, H = len(counts), int(counts.max()) + 3, 144, 272
+    poff, row_token = tables(counts, 1, T, rng)
+    M_cap = len(row_token)
+    (xc, xs), (hc, hs) = random_operand(rng, T, K), random_operand(rng, M_cap, K)
+    (w13c, w13s), (w2c, w2s) = random_operand(rng, E, 2 * I, K), random_operand(rng, E, H, K)
+    used = np.nonzero(counts)[0]
+    w13s[counts == 0] = w2s[counts == 0] = 255  # never read
+    rt, po, ct = dev(row_token), dev(poff), dev(counts)
+    h = torch.full((M_cap, I), 7.0, dtype=torch.bfloat16, device=DEV)
+    y = torch.full((M_cap, H), 7.0, dtype=torch.bfloat16, device=DEV)
+    mm.moe_grouped_gemm_l1_silu_mxfp4(dev(xc), dev(xs), rt, po, ct, dev(w13c), dev(w13s), h, max_rows_per_expert=bound)
+    mm.moe_grouped_gemm_l2_mxfp4(dev(hc), dev(hs), po, ct, dev(w2c), dev(w2s), y, max_rows_per_expert=bound)
+    torch.cuda.synchronize()
+    hg, yg, free = bf16_np(h), bf16_np(y), np.ones(M_cap, bool)
+    xv, hv = X.decode(xc, xs), X.decode(hc, hs)
+    for e in used:
+        r = np.arange(poff[e], poff[e] + counts[e])
+        free[r] = False
+        accept_silu(hg[r], *X.gate_up(xv[row_token[r]], X.decode(w13c[e], w13s[e])), K)
+        ref, zabs = X.product(hv[r], X.decode(w2c[e], w2s[e]))
+        accept(yg[r], ref, zabs, K)
+    assert np.all(hg[free] == 7.0) and np.all(yg[free] == 7.0)
+
+
+@pytest.mark.parametrize("M,K", [(40, 2688), (47, 7168), (21, 12288), (11, 24576)])
+def test_linear_long_reductions_of_several_m_tiles(M, K):
+    """The same kernel on a dense call of three m-tiles and more, 387 groups of weight rows and 390 of gate+up."""
+    rng = np.random.default_rng(M + K)
+    N, I = 2064, 1040
+    (ac, as_), (wc, ws) = random_operand(rng, M, K), random_operand(rng, 2 * I, K)
+    out = torch.full((M + 1, N), 7.0, dtype=torch.bfloat16, device=DEV)
+    h = torch.full((M + 1, I), 7.0, dtype=torch.bfloat16, device=DEV)
+    a, w = (dev(ac), dev(as_)), (dev(wc), dev(ws))
+    mm.mxfp4_linear(*a, w[0][:N], w[1][:N], out[:M])
+    mm.mxfp4_linear_gate_up_silu(*a, *w, h[:M])
+    torch.cuda.synchronize()
+    assert torch.all(out[M:] == 7.0) and torch.all(h[M:] == 7.0)
+    av, wv = X.decode(ac, as_), X.decode(wc, ws)
+    accept(bf16_np(out[:M]), *X.product(av, wv[:N]), K)
+    accept_silu(bf16_np(h[:M]), *X.gate_up(av, wv), K)
+
+
 def test_experts_no_rows():
     """M_cap = 0: nothing is enqueued."""
     u8 = lambda *s: torch.zeros(*s, dtype=torch.uint8, device=DEV)  # noqa: E731
