@@ -367,22 +367,26 @@ __global__ __launch_bounds__(kScoreWaves* kWave) void router_scores_bwd_kernel(R
     rest = score_wave_sum(rest);
     inv = mz > kNone ? 1.0 / (1.0 + rest) : 0.0;
   }
-  double sj = 0.0, cj = 1.0;  // score of this lane's chosen expert; sigmoid: 1 minus it (of bits of its own)
+  // This lane's chosen expert: its score, up to a common factor where it is divided by the sum, and what its g'
+  // is multiplied with, s or for a sigmoid s (1 - s).
+  double sj = 0.0, fj = 0.0;
   const float zj = id >= 0 ? logit_of(row[id]) : -__builtin_huge_valf();
   if (sigmoid) {
     const double e = exp_f64(ec, -fabs((double)zj)), y = reciprocal_f64(1.0 + e);
     sj = zj < 0.0f ? e * y : y;
-    cj = zj < 0.0f ? y : e * y;
-  } else if (every) {
-    sj = zj > -__builtin_huge_valf() ? exp_f64(ec, (double)zj - m) * inv : 0.0;
+    fj = e * y * y;
+  } else {
+    if (p.renormalize) sj = relative_score(ec, zj, id >= 0);
+    else if (zj > -__builtin_huge_valf()) sj = exp_f64(ec, (double)zj - m) * inv;
+    fj = sj;
   }
   if (p.renormalize) {
-    double S = sigmoid ? score_wave_sum(sj) : 0.0;
-    if (S < kFarScores) {
-      sj = relative_score(ec, zj, id >= 0);
+    double S = score_wave_sum(sj), gs = score_wave_sum(g * sj);
+    if (sigmoid && S < kFarScores) {
+      fj = sj = relative_score(ec, zj, id >= 0);
       S = score_wave_sum(sj);
+      gs = score_wave_sum(g * sj);
     }
-    const double gs = score_wave_sum(g * sj);
     const double rS = S > 0.0 ? 1.0 / S : 0.0;
     g = id >= 0 ? (g - gs * rS) * rS : 0.0;
   }
@@ -398,7 +402,7 @@ __global__ __launch_bounds__(kScoreWaves* kWave) void router_scores_bwd_kernel(R
     if (named) gx = read_lane(ge, __builtin_ctzll(named));
     dot = score_wave_sum(id == x ? 0.0 : g * sj) - gx * (rest * inv);
   }
-  const T mine = round_logit<T>(sigmoid ? ge * sj * cj : sj * (ge - gx - dot));
+  const T mine = round_logit<T>(fj * (ge - gx - dot));
   T v[PL];
 #pragma unroll
   for (int i = 0; i < PL; ++i) v[i] = round_logit<T>(every ? -(s[i] * inv * (gx + dot)) : 0.0);
