@@ -117,12 +117,12 @@ __device__ __forceinline__ float unsort_key(uint32_t u) {
 // A sum of chosen scores below this is taken of relative_score instead.
 constexpr double kFarScores = 0x1p-60;
 
-// e^(z - the largest z of the wave's chosen lanes), 0 for the others: chosen scores up to a common factor, where
-// the scores themselves lose bits or underflow.  Softmax scores are that, and so are sigmoids below 2^-60, which
-// are e^z to float64's last bit.
-__device__ __forceinline__ double relative_score(const ExpConstants& ec, float z, bool chosen) {
-  const uint32_t mk = dpp_reduce(chosen ? sort_key(z) : 0u, umax);
-  return chosen && z > -__builtin_huge_valf() ? exp_f64(ec, (double)z - (double)unsort_key(mk)) : 0.0;
+// Key of a chosen lane's logit, 0 for the others; the wave's largest is relative_score's `top`.
+__device__ __forceinline__ uint32_t chosen_key(float z, bool chosen) { return chosen ? sort_key(z) : 0u; }
+// e^(z - the largest chosen logit), 0 for the other lanes: chosen scores up to a common factor, where the scores themselves lose
+// bits or underflow.  Softmax scores are that, and so are sigmoids below 2^-60, which are e^z to float64's last bit.
+__device__ __forceinline__ double relative_score(const ExpConstants& ec, float z, bool chosen, uint32_t top) {
+  return chosen && z > -__builtin_huge_valf() ? exp_f64(ec, (double)z - (double)unsort_key(top)) : 0.0;
 }
 
 // One wave per token.  The wave's lanes are split into equal power-of-two runs of `span` lanes, one
@@ -244,7 +244,7 @@ __global__ __launch_bounds__(kScoreWaves* kWave) void router_scores_kernel(Route
   if (p.renormalize) {
     d = score_wave_sum(ws);
     if (d < kFarScores) {  // the bias or the groups left only experts far below the others
-      ws = relative_score(ec, wz, my_id >= 0);
+      ws = relative_score(ec, wz, my_id >= 0, dpp_reduce(chosen_key(wz, my_id >= 0), umax));
       d = score_wave_sum(ws);
     }
   }
@@ -303,7 +303,8 @@ hipError_t launch_router_scores(const RouterScoreArgs& a0, int dtype, hipStream_
 // float64 up to the one rounding of dz, and 1 - s_e never by a subtraction, which would leave no correct bit from
 // z = 37 on (or such a distance to a softmax's other logits): for a sigmoid it is sigmoid(-z_e), and a
 // softmax's g'_e - sum_j g'_j s_j is taken relative to the expert x of the largest logit, the only one whose score
-// may be near 1, as (g'_e - g'_x) - sum_{i != x} (g'_i - g'_x) s_i.  One wave per token, lane l holding experts l + 64 i; the
+// may be near 1, as (g'_e - g'_x) - sum_{i != x} (g'_i - g'_x) s_i, and g_j - sum_i g_i n_i relative to the slot of
+// the largest chosen logit (one renormalised weight alone: 0 exactly).  One wave per token, lane l holding experts l + 64 i; the
 // chosen experts' scores are computed one per lane.
 template <typename T>
 __device__ __forceinline__ T round_logit(double v);
@@ -365,7 +366,7 @@ __global__ __launch_bounds__(kScoreWaves* kWave) void router_scores_bwd_kernel(R
       rest += lane + kWave * i == x ? 0.0 : s[i];
     }
     rest = score_wave_sum(rest);
-    inv = mz > kNone ? 1.0 / (1.0 + rest) : 0.0;
+    inv = mz > kNone ? reciprocal_f64(1.0 + rest) : 0.0;
   }
   // This lane's chosen expert: its score, up to a common factor where it is divided by the sum, and what its g'
   // is multiplied with, s or for a sigmoid s (1 - s).
@@ -375,19 +376,20 @@ __global__ __launch_bounds__(kScoreWaves* kWave) void router_scores_bwd_kernel(R
     const double e = exp_f64(ec, -fabs((double)zj)), y = reciprocal_f64(1.0 + e);
     sj = zj < 0.0f ? e * y : y;
     fj = e * y * y;
-  } else {
-    if (p.renormalize) sj = relative_score(ec, zj, id >= 0);
-    else if (zj > -__builtin_huge_valf()) sj = exp_f64(ec, (double)zj - m) * inv;
-    fj = sj;
+  } else if (every) {
+    fj = sj = zj > -__builtin_huge_valf() ? exp_f64(ec, (double)zj - m) * inv : 0.0;
   }
   if (p.renormalize) {
+    const uint32_t key = chosen_key(zj, id >= 0), top = dpp_reduce(key, umax);
+    g -= read_lane(g, __builtin_ctzll(__ballot(key == top)));
+    if (!sigmoid) fj = sj = relative_score(ec, zj, id >= 0, top);
     double S = score_wave_sum(sj), gs = score_wave_sum(g * sj);
     if (sigmoid && S < kFarScores) {
-      fj = sj = relative_score(ec, zj, id >= 0);
+      fj = sj = relative_score(ec, zj, id >= 0, top);
       S = score_wave_sum(sj);
       gs = score_wave_sum(g * sj);
     }
-    const double rS = S > 0.0 ? 1.0 / S : 0.0;
+    const double rS = S > 0.0 ? reciprocal_f64(S) : 0.0;
     g = id >= 0 ? (g - gs * rS) * rS : 0.0;
   }
   // g'_e of this lane's expert: the slots that name it, in slot order; then its gradient.
@@ -396,16 +398,18 @@ __global__ __launch_bounds__(kScoreWaves* kWave) void router_scores_bwd_kernel(R
     const double gj = read_lane(g, j);
     ge += __builtin_amdgcn_readlane(id, j) == id ? gj : 0.0;
   }
-  double gx = 0.0, dot = 0.0;  // g'_x and sum_{i != x} (g'_i - g'_x) s_i
-  if (every) {
-    const uint64_t named = __ballot(id == x);
-    if (named) gx = read_lane(ge, __builtin_ctzll(named));
-    dot = score_wave_sum(id == x ? 0.0 : g * sj) - gx * (rest * inv);
-  }
-  const T mine = round_logit<T>(fj * (ge - gx - dot));
   T v[PL];
 #pragma unroll
-  for (int i = 0; i < PL; ++i) v[i] = round_logit<T>(every ? -(s[i] * inv * (gx + dot)) : 0.0);
+  for (int i = 0; i < PL; ++i) v[i] = round_logit<T>(0.0);
+  if (every) {
+    const uint64_t named = __ballot(id == x);
+    const double gx = named ? read_lane(ge, __builtin_ctzll(named)) : 0.0;
+    const double dot = score_wave_sum(id == x ? 0.0 : g * sj) - gx * (rest * inv);  // sum_{i != x} (g'_i - g'_x) s_i
+#pragma unroll
+    for (int i = 0; i < PL; ++i) v[i] = round_logit<T>(-(s[i] * inv * (gx + dot)));
+    ge = ge - gx - dot;
+  }
+  const T mine = round_logit<T>(fj * ge);
   for (int j = 0; j < p.k; ++j) {
     const int ej = __builtin_amdgcn_readlane(id, j);  // -1 is no expert: -1 / 64 is no i
     const T vj = read_lane(mine, j);

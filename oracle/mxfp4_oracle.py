@@ -126,7 +126,7 @@ def router_bwd(logits, ids, grad, score="sigmoid", renormalize=True, scale=1.0):
         g = np.array([float(grad[t, j]) for j, _ in at])
         if renormalize:
             n = shares(z[t, [e for _, e in at]], score)
-            part = scale * n * (g - (g * n).sum())
+            part = scale * n * (n * (g[:, None] - g)).sum(1)  # n_j (g_j - sum_i n_i g_i), as a sum of what does not cancel
         else:
             part = scale * g
             if score == "softmax":  # s_e (G_e - sum_i s_i G_i), as a sum of what does not cancel

@@ -391,6 +391,36 @@ def test_softmax_gradient_of_a_dominant_expert(E, k, dtype):
     assert np.all(np.abs(got - ref) <= np.abs(ref) * half + size * 2.0 ** -40 + tiny)
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("E,k", [(2, 1), (2, 2), (40, 1), (40, 5), (1024, 64)])
+def test_renormalized_gradient_of_a_dominant_expert(E, k, score, dtype):
+    """One chosen logit up to 700 above the other chosen ones, in any slot: with x its slot,
+    scale * n_j f_j ((g_j - g_x) - sum_{i != x} n_i (g_i - g_x)), one rounding, and 2^-40 of what is summed.  One slot
+    alone: exactly 0."""
+    rng = np.random.default_rng(E + k + 1)
+    gaps = np.repeat([0.0, 5.0, 20.0, 30.0, 36.0, 37.0, 38.0, 50.0, 80.0, 100.0, 700.0], 3)
+    z = rng.standard_normal((len(gaps), E)) - 4 - gaps[:, None]
+    ids = np.stack([rng.permutation(E)[:k] for _ in z]).astype(np.int32)
+    x = rng.integers(0, k, (len(z), 1))
+    np.put_along_axis(z, np.take_along_axis(ids, x, 1), 0.5, 1)
+    grad = rng.standard_normal(ids.shape).astype(np.float32)
+    kw = dict(score=score, renormalize=True, scale=2.5)
+    out, zh, _ = run_bwd(z, ids, grad, dtype, **kw)
+    got, ref = out.float().cpu().numpy().astype(np.float64), X.router_bwd(zh, ids, grad, **kw)
+    half, tiny = (2.0 ** -24, F32_TINY) if dtype == torch.float32 else (2.0 ** -8, 2.0 ** -134)
+    n = np.stack([X.shares(zh[t, ids[t]], score) for t in range(len(z))])
+    h = np.abs(grad.astype(np.float64) - np.take_along_axis(grad, x, 1))
+    part = 2.5 * n * (h + (n * h).sum(1, keepdims=True))
+    if score == "sigmoid":
+        part = part / (1 + np.exp(np.take_along_axis(zh, ids, 1).astype(np.float64)))
+    size = np.zeros_like(ref)
+    np.put_along_axis(size, ids, part, 1)
+    assert np.all(np.abs(got - ref) <= np.abs(ref) * half + size * 2.0 ** -40 + tiny)
+    if k == 1:
+        assert not got.any()
+
+
 # ---- with the routing step -----------------------------------------------------------------------
 
 @pytest.mark.parametrize("T,P", [(0, 1), (1, 1), (8, 128), (700, 8)])

@@ -137,6 +137,19 @@ def test_oracle_sigmoid_gradient_of_large_logits():
 
 
 @pytest.mark.parametrize("gap", [0.0, 20.0, 37.0, 60.0, 700.0])
+def test_oracle_renormalized_gradient_of_a_dominant_expert(gap):
+    """Two slots: n_0 n_1 (g_0 - g_1), of either sign."""
+    z, ids, g = np.array([[0.5 - gap, 0.5, -1.0]]), np.array([[0, 1]]), np.array([[1.0, -2.0]])
+    want = 3 / (2 * np.cosh(gap / 2)) ** 2
+    assert np.all(np.abs(X.router_bwd(z, ids, g, "softmax", True, 1.0)[0] - [want, -want, 0]) <= want * 2.0 ** -40)
+    r = np.exp(0.5 - gap) / (1 + np.exp(0.5 - gap)) * (1 + np.exp(-0.5))  # s_0 / s_1
+    want = 3 * r / (1 + r) ** 2 * np.array([1 / (1 + np.exp(0.5 - gap)), -1 / (1 + np.exp(0.5)), 0])
+    assert np.all(np.abs(X.router_bwd(z, ids, g, "sigmoid", True, 1.0)[0] - want) <= np.abs(want) * 2.0 ** -40)
+    for score in ("softmax", "sigmoid"):
+        assert not X.router_bwd(z, ids[:, :1], g[:, :1], score, True, 1.0).any()
+
+
+@pytest.mark.parametrize("gap", [0.0, 20.0, 37.0, 60.0, 700.0])
 def test_oracle_softmax_gradient_of_a_dominant_expert(gap):
     """Two experts: s_0 (1 - s_0) = 1 / (2 cosh(gap / 2))^2, of either sign."""
     got = X.router_bwd(np.array([[0.0, -gap]]), np.array([[0]]), np.array([[1.0]]), "softmax", False, 1.0)[0]
