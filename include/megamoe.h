@@ -615,7 +615,7 @@ int32_t nvfp4_linear_gate_up_silu_nvfp4(const uint8_t* a_codes, const uint8_t* a
  * row_valid    nullable int32 [rows]: rows with row_valid[r] < 0 are not read and get zero codes and
  *              scales (pass row_token to quantize permuted rows).
  * codes        uint8 [rows, cols/2];  scales uint8 [rows, cols/32].
- * out_bf16     bf16 [rows, cols]: the values, exact; beyond bf16's range (6 * 2^126 and up) infinite.
+ * out_bf16     bf16 [rows, cols]: the values, exact; beyond bf16's range (2^128 and up) infinite.
  * Limits: rows >= 0, cols > 0 and a multiple of 32, fewer than 2^37 elements; x, codes and out_bf16
  * aligned to 16 bytes, no output overlapping an input.
  * ---------------------------------------------------------------------------------------- */

@@ -132,7 +132,7 @@ hipError_t launch_mx_quant(const void* x, int dtype, int64_t rows, int64_t cols,
 
 // Decoder: one lane per code word (eight elements, 16 bytes of bf16).  e2m1 * 2^(scale - 127) has two
 // significant bits and is exact in bf16, the subnormal products of scale 0 included; above the range
-// (6 * 2^126 and up) it is the infinity of bf16.
+// (2^128 and up) it is the infinity of bf16.
 __device__ __forceinline__ uint32_t mx_value_bits(uint32_t code, uint32_t scale) {
   if (scale == 0xFFu) return 0x7FC0u;
   const uint32_t mag = code & 7u, sign = (code & 8u) << 12;

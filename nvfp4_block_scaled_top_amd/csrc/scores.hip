@@ -63,7 +63,7 @@ __device__ __forceinline__ double score_wave_sum(double v) {
 }
 
 // e^t: t = n ln 2 + r with |r| <= ln 2 / 2, the Taylor polynomial of e^r up to r^12 / 12! (its
-// remainder is below 2^-52 of e^r) and a scaling by 2^n: 18 instructions, where exp() takes some 40.  The
+// remainder is at most 1.04 * 2^-52 of e^r) and a scaling by 2^n: 18 instructions, where exp() takes some 40.  The
 // constants are held in scalar registers: left to itself the compiler moves each into vector registers before
 // every use, two moves a multiplication.
 struct ExpConstants {
