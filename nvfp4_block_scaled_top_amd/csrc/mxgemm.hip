@@ -52,14 +52,15 @@ __device__ __forceinline__ int mx_count(const MxGemmArgs& p, int e) { return p.c
 // registers.  The ring runs on across groups and m-tiles.
 //
 // The token rows' part of K stays in LDS while the groups of their m-tile pass.  Both operands keep
-// 16-byte piece c of row R (one MXFP4 block) at slot c ^ R of the row's 256 bytes, so that 16 rows are
-// read without bank conflicts.  Lane (r, g) takes blocks 4g .. 4g+3 of its row, one an MFMA step: its
-// four scale bytes are one word, and the instruction picks the byte.
+// 16-byte piece c of row R (one MXFP4 block) at slot c ^ R of the row's 256 bytes, so that the 16 rows of
+// one g are read from 16 different slots.  (Lanes of two g's still meet in a slot: half of the LDS cycles are
+// conflicts by the counter.  LDS is busy for 6 to 18% of the kernel's cycles.)  Lane (r, g) takes blocks 4g .. 4g+3
+// of its row, one an MFMA step: its four scale bytes are one word, and the instruction picks the byte.
 //
 // At the end of a group the waves leave their partial sums in LDS (two buffers, by the group's parity) and
 // one of them adds the four in wave order and stores.
 //
-// Where the token rows of the whole K fit LDS four times beside the rings (K up to 2048), K is not split:
+// Where the token rows of the whole K fit LDS four times beside the rings (K up to 2560), K is not split:
 // every wave takes groups of its own and keeps its own copy of the token rows, and nothing is shared
 // or waited for.  With K = 2048 split in four a wave has one slot between two barriers: the down projection
 // of a 512-token prompt (384 experts, 7168 x 2048) took 814 us, and 632 without the split (528, 5.8 TB/s, with
@@ -101,7 +102,8 @@ __device__ __forceinline__ f32x4 mx_mfma16(u32x4 a, u32x4 b, f32x4 c, uint32_t s
 // spreads any work over all CUs.  Measured, dense (us, tile kernel / small kernel): 64 rows x 4096 x 7168
 // 42.7 / 15.0, 256 x 4096 x 7168 61.2 / 44.5, 400 x 4096 x 7168 67.0 / 69.5, 400 x 7168 x 2048 24.9 / 32.6.
 // slots: what the small kernel would stream for them, 0.74 ns each; tiles: of the tile kernel, 256 at a
-// time, 1.45, 1.6 or 2.1 us a stage (64, 128 or 256 token rows).
+// time, 1.45, 1.6 or 2.1 us a stage (64, 128 or 256 token rows).  A grouped call is weighed as a whole, with every
+// stage at its largest expert's time; the figures are of dense calls.
 struct MxLoad {
   int64_t slots, tiles;
   int rows;  // the largest expert's
@@ -388,7 +390,8 @@ __global__ __launch_bounds__(kMxSplit* kWave, 1) void mx_small_kernel(MxGemmArgs
 //
 // A stage holds 128 code bytes a row of either operand (a load instruction covers 8 rows; with 128
 // contiguous bytes a row it takes 19 cycles, with 64 bytes 28), block c of row R at slot
-// c ^ mx_swz(R), which the 16-byte reads of 32 rows meet without bank conflicts.  Scales come in
+// c ^ mx_swz(R), so that 16 rows' reads of one block meet the 16 slots of two rows once each (26% of the
+// LDS cycles are still conflicts by the counter; which accesses they come from is not known).  Scales come in
 // stages of 512 elements, 16 bytes a row: 64 rows cost a load instruction 97 cycles whatever it
 // brings of each.
 //

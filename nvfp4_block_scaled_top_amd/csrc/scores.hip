@@ -304,7 +304,9 @@ hipError_t launch_router_scores(const RouterScoreArgs& a0, int dtype, hipStream_
 // z = 37 on (or such a distance to a softmax's other logits): for a sigmoid it is sigmoid(-z_e), and a
 // softmax's g'_e - sum_j g'_j s_j is taken relative to the expert x of the largest logit, the only one whose score
 // may be near 1, as (g'_e - g'_x) - sum_{i != x} (g'_i - g'_x) s_i, and g_j - sum_i g_i n_i relative to the slot of
-// the largest chosen logit (one renormalised weight alone: 0 exactly).  One wave per token, lane l holding experts l + 64 i; the
+// the largest chosen logit (one renormalised weight alone: 0 exactly).  8192 tokens x 384 experts, k = 6, float32:
+// 8.5 us with sigmoid scores, 8.4 with a renormalised softmax, 12.5 with softmax weights kept as they are (a launch
+// takes 2.2, the bytes 2.7 to 4).  One wave per token, lane l holding experts l + 64 i; the
 // chosen experts' scores are computed one per lane.
 template <typename T>
 __device__ __forceinline__ T round_logit(double v);
