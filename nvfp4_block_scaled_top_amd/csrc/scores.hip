@@ -119,8 +119,9 @@ constexpr double kFarScores = 0x1p-60;
 
 // Key of a chosen lane's logit, 0 for the others; the wave's largest is relative_score's `top`.
 __device__ __forceinline__ uint32_t chosen_key(float z, bool chosen) { return chosen ? sort_key(z) : 0u; }
-// e^(z - the largest chosen logit), 0 for the other lanes: chosen scores up to a common factor, where the scores themselves lose
-// bits or underflow.  Softmax scores are that, and so are sigmoids below 2^-60, which are e^z to float64's last bit.
+// e^(z - the largest chosen logit), 0 for the other lanes: chosen scores up to a common factor, where the scores
+// themselves lose bits or underflow.  Softmax scores are that, and so are sigmoids below 2^-60, which are e^z to
+// float64's last bit.
 __device__ __forceinline__ double relative_score(const ExpConstants& ec, float z, bool chosen, uint32_t top) {
   return chosen && z > -__builtin_huge_valf() ? exp_f64(ec, (double)z - (double)unsort_key(top)) : 0.0;
 }
