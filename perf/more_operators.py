@@ -34,8 +34,8 @@ def listed():
         # backward of a small layer on a short batch, odd widths
         dict(name="grouped_grad_t61", op="grouped_grad", T=61, E=8, local=8, k=2, K=520, N=1032, dtype="f16", dw="f16",
              gather=False, zipf=False),
-        # backward of gate+up in a training step, the GPU's share of 384 experts, float32 weight gradients
-        dict(name="grouped_grad_t4096", op="grouped_grad", T=4096, E=384, local=48, k=6, K=7168, N=4096, dtype="bf16",
+        # backward of gate+up in a training step over 48 experts, skewed routing, float32 weight gradients
+        dict(name="grouped_grad_t4096", op="grouped_grad", T=4096, E=48, local=48, k=6, K=7168, N=4096, dtype="bf16",
              dw="f32", gather=True, zipf=True),
         # activations of a decode step
         dict(name="quantize_decode_8x7168", op="quantize", rows=8, cols=7168, dtype="bf16"),
