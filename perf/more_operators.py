@@ -192,7 +192,7 @@ def _run_own(s):
         mm.moe_grouped_gemm(s["x"], s["w"], s["offsets"], s["counts"], s["out"],
                             row_token=s["row_token"] if s["gather"] else None, max_rows_per_expert=s["T"])
     elif op == "grouped_grad":
-        mm.moe_grouped_gemm_dgrad(s["dy"], s["w"], s["offsets"], s["counts"], s["dx"], max_rows_per_expert=s["T"])
+        mm.moe_grouped_gemm_dgrad(s["dy"], s["w"], s["offsets"], s["counts"], s["dx"])
         mm.moe_grouped_gemm_wgrad(s["dy"], s["x"], s["offsets"], s["counts"], s["dweight"],
                                   row_token=s["row_token"] if s["gather"] else None)
         return {"dx": s["dx"], "dweight": s["dweight"]}
