@@ -26,8 +26,8 @@
  *     MEGAMOE_ERR_WORKSPACE   workspace_bytes is smaller than the matching *_workspace_bytes()
  *     MEGAMOE_ERR_LAUNCH      a kernel launch failed (hipGetLastError after the launch)
  *     MEGAMOE_ERR_DEVICE      the current device is not gfx950
- *     MEGAMOE_ERR_ALIGN       a pointer is not aligned as its function asks (the scored router and
- *                             the MXFP4 calls)
+ *     MEGAMOE_ERR_ALIGN       a pointer is not aligned as its function asks (the scored router, the
+ *                             MXFP4, int8 and 16-bit calls)
  * - Data errors on the device are defined away: a top-k id outside
  *   [expert_begin, expert_begin + num_experts) is "not local" and is dropped.
  * - Layouts are row-major.  NVFP4 tensors are three parts:
@@ -42,6 +42,10 @@
  *     scales uint8 [rows, K/32] one E8M0 block scale per 32 consecutive K elements: 2^(byte - 127),
  *                               255 = NaN; the real value of element i is
  *                               e2m1(code_i) * 2^(scale_block(i) - 127).
+ *   int8 tensors are two parts:
+ *     codes  int8  [rows, K]
+ *     scales float [rows]       one scale a row (a token's, or a weight channel's); the real value of
+ *                               element i is code_i * scale.
  * - Expert weights: W13 codes [E, 2I, H/2], scales [E, 2I, H/16], gs [E]; rows 0..I-1 are the
  *   gate projection and rows I..2I-1 the up projection.  W2 codes [E, H, I/2], scales
  *   [E, H, I/16], gs [E].  bf16 tensors are passed as raw 16-bit storage.
@@ -64,9 +68,10 @@ extern "C" {
 #define MEGAMOE_ERR_DEVICE (-5)
 #define MEGAMOE_ERR_ALIGN (-6)
 
-/* Element types of the arguments that come in two. */
+/* Element types of the arguments that come in several; each function states the ones it takes. */
 #define MEGAMOE_DTYPE_BF16 0
 #define MEGAMOE_DTYPE_F32 1
+#define MEGAMOE_DTYPE_F16 2
 
 /* Scores of moe_router_scores. */
 #define MEGAMOE_SCORE_SOFTMAX 0
@@ -678,6 +683,115 @@ int32_t moe_grouped_gemm_l2_mxfp4(const uint8_t* h_codes, const uint8_t* h_scale
                                   const uint8_t* w2_codes, const uint8_t* w2_scales, int32_t E, int32_t H,
                                   int32_t I, int64_t M_cap, int32_t max_rows_per_expert, void* y_bf16,
                                   void* stream);
+
+/* ------------------------------------------------------------------------------------------
+ * int8_quantize_act, int8_dequantize - bf16, fp16 or float32 to int8 with a scale a row, and back.
+ *
+ * Per row: scale = fl32(amax / 127); an element's code is the whole number nearest to the exact
+ * quotient 127 x / amax, ties to even (so within +-127).  Results are bit-exact with that definition.
+ * A row of zeros gets scale 0 and zero codes; a row with an infinity or a NaN a NaN scale and zero
+ * codes.  int8_dequantize writes code * scale, rounded to float32 and then to dtype.
+ *
+ * x            [rows, cols], dtype MEGAMOE_DTYPE_BF16, MEGAMOE_DTYPE_F16 or MEGAMOE_DTYPE_F32.
+ * row_valid    nullable int32 [rows]: rows with row_valid[r] < 0 are not read and get scale 0 and zero
+ *              codes (pass row_token to quantize permuted rows).
+ * codes        int8 [rows, cols];  scales float [rows];  out [rows, cols] in dtype.
+ * Weights [N, K] are quantized by the same call, a scale for each of their N output channels.
+ * Limits: rows >= 0, cols > 0, below 2^30 and a multiple of 16, fewer than 2^37 elements; x, codes and
+ * out aligned to 16 bytes, scales and row_valid to 4; no output overlapping an input.
+ * ---------------------------------------------------------------------------------------- */
+int32_t int8_quantize_act(const void* x, int32_t dtype, int64_t rows, int64_t cols, const int32_t* row_valid,
+                          int8_t* codes, float* scales, void* stream);
+int32_t int8_dequantize(const int8_t* codes, const float* scales, int64_t rows, int64_t cols, int32_t dtype,
+                        void* out, void* stream);
+
+/* ------------------------------------------------------------------------------------------
+ * int8_linear, int8_linear_gate_up_silu - dense products of 8-bit integers with a scale for each token
+ * and each channel.
+ *
+ *   out[m, n] = a_scales[m] * w_scales[n] * sum_k a_codes[m, k] * w_codes[n, k]
+ *   h[m, i]   = SiLU(g) * u,  g / u = the same with rows i and I+i of w13
+ * The sum is exact (int32); it is rounded to float32, multiplied by the channel's scale, then by the
+ * token's, each rounded to float32, and the result rounded once to dtype.
+ * a_codes int8 [M, K], a_scales float [M] (e.g. from int8_quantize_act).
+ * w_codes int8 [N, K], w_scales float [N];  w13 [2I, K], [2I], rows 0..I-1 gate, I..2I-1 up.
+ * dtype        of out [M, N] and h [M, I]: MEGAMOE_DTYPE_BF16 or MEGAMOE_DTYPE_F16.
+ * Limits: 0 <= M < 2^31, 16 <= K < 2^17 and a multiple of 16, N and I >= 8, multiples of 8 and below
+ * 2^22, A below 2^36 bytes; codes and outputs aligned to 16 bytes, scales to 4; the output overlaps no input.
+ * With M == 0 the call enqueues nothing.
+ * ---------------------------------------------------------------------------------------- */
+int32_t int8_linear(const int8_t* a_codes, const float* a_scales, int64_t M, int32_t K, const int8_t* w_codes,
+                    const float* w_scales, int32_t N, int32_t dtype, void* out, void* stream);
+int32_t int8_linear_gate_up_silu(const int8_t* a_codes, const float* a_scales, int64_t M, int32_t K,
+                                 const int8_t* w13_codes, const float* w13_scales, int32_t I, int32_t dtype,
+                                 void* h, void* stream);
+
+/* ------------------------------------------------------------------------------------------
+ * moe_grouped_gemm_l1_silu_int8, moe_grouped_gemm_l2_int8 - the experts' products on int8 weights and
+ * activations: the operations of moe_grouped_gemm_l1_silu and moe_grouped_gemm_l2 with the scales of
+ * int8_linear.  For each expert e and each of its rows r
+ * (padded_offsets[e] <= r < padded_offsets[e] + counts[e]), t = row_token[r]:
+ *   h[r, i] = bf16( SiLU(g) * u ),  g / u = x_scales[t] * w13_scales[e, i or I+i] * sum_k x[t, k] * W13[e, i or I+i, k]
+ *   y[r, n] = bf16( h_scales[r] * w2_scales[e, n] * sum_k h[r, k] * W2[e, n, k] )
+ * Rows that hold no assignment are not written, experts with no rows are never read.
+ *
+ * x_codes int8 [T, H], x_scales float [T];  h_codes int8 [M_cap, I], h_scales float [M_cap]
+ *              (int8_quantize_act of h with row_valid = row_token).
+ * row_token, padded_offsets, counts   as written by moe_route_permute (its sched is not read).
+ * w13 int8 [E, 2I, H], float [E, 2I];  w2 int8 [E, H, I], float [E, H].
+ * M_cap        rows of h and y: megamoe_row_capacity(T, k, E, P).
+ * max_rows_per_expert  a bound on counts[e] the caller expects, or 0 if none: it may change which
+ *              kernels launch, never the results; a bound that is too low costs time only.
+ * h_bf16 bf16 [M_cap, I];  y_bf16 bf16 [M_cap, H].
+ * Limits: E as for moe_route_permute; H, I and alignment as K, N and alignment of int8_linear; x and h below
+ * 2^36 bytes (T is not an argument: T <= M_cap with M_cap as above).  With M_cap == 0 the row arrays may be
+ * NULL and the call enqueues nothing.
+ * ---------------------------------------------------------------------------------------- */
+int32_t moe_grouped_gemm_l1_silu_int8(const int8_t* x_codes, const float* x_scales, const int32_t* row_token,
+                                      const int32_t* padded_offsets, const int32_t* counts,
+                                      const int8_t* w13_codes, const float* w13_scales, int32_t E, int32_t H,
+                                      int32_t I, int64_t M_cap, int32_t max_rows_per_expert, void* h_bf16,
+                                      void* stream);
+int32_t moe_grouped_gemm_l2_int8(const int8_t* h_codes, const float* h_scales, const int32_t* padded_offsets,
+                                 const int32_t* counts, const int8_t* w2_codes, const float* w2_scales, int32_t E,
+                                 int32_t H, int32_t I, int64_t M_cap, int32_t max_rows_per_expert, void* y_bf16,
+                                 void* stream);
+
+/* ------------------------------------------------------------------------------------------
+ * moe_grouped_gemm, moe_grouped_gemm_dgrad, moe_grouped_gemm_wgrad - the experts' product on
+ * unquantized weights, experts of ragged sizes, and its gradients.
+ *
+ * For each expert e and each of its rows r (padded_offsets[e] <= r < padded_offsets[e] + counts[e]),
+ * s = row_token[r], or r without row_token:
+ *   y[r, n]     = sum_k x[s, k] * W[e, n, k]
+ *   dx[r, k]    = sum_n dy[r, n] * W[e, n, k]          (by row r: a token's gradient is the sum over its
+ *                 rows, e.g. moe_combine of dx with weights of 1)
+ *   dw[e, n, k] = sum over the expert's rows r of dy[r, n] * x[s, k], added to what dw holds with accumulate
+ * with FP32 accumulation and one rounding to the output's type (accumulate: of the float32 sum of the
+ * old value and the FP32 total).  Results do not change from call to call.  Rows of y and dx that hold no
+ * assignment are not written and rows of x and dy that hold none are not read; experts with no rows are
+ * not read, and their dw is set to 0 (with accumulate: left as it is).
+ *
+ * dtype        of x, dy, w, y and dx: MEGAMOE_DTYPE_BF16 or MEGAMOE_DTYPE_F16.
+ * x [T, K] with row_token (token ids of x's rows), else [M_cap, K];  dy, y [M_cap, N];  dx [M_cap, K];
+ * w [E, N, K];  dw [E, N, K] in dw_dtype: dtype or MEGAMOE_DTYPE_F32.
+ * row_token (nullable), padded_offsets, counts   as written by moe_route_permute with any padding (its
+ *              sched is not read).
+ * max_rows_per_expert  as for moe_grouped_gemm_l2_mxfp4.
+ * Limits: E as for moe_route_permute; K and N >= 8, multiples of 8 and below 2^22; 0 <= M_cap < 2^31,
+ * x and dy below 2^36 bytes each (T <= M_cap); pointers aligned to 16 bytes, the tables to 4; no output
+ * overlaps an input.  With M_cap == 0 the row arrays may be NULL; y and dx are then not written, dw as above.
+ * ---------------------------------------------------------------------------------------- */
+int32_t moe_grouped_gemm(const void* x, int32_t dtype, const int32_t* row_token, const int32_t* padded_offsets,
+                         const int32_t* counts, const void* w, int32_t E, int32_t K, int32_t N, int64_t M_cap,
+                         int32_t max_rows_per_expert, void* y, void* stream);
+int32_t moe_grouped_gemm_dgrad(const void* dy, int32_t dtype, const int32_t* padded_offsets, const int32_t* counts,
+                               const void* w, int32_t E, int32_t K, int32_t N, int64_t M_cap, void* dx,
+                               void* stream);
+int32_t moe_grouped_gemm_wgrad(const void* dy, const void* x, int32_t dtype, const int32_t* row_token,
+                               const int32_t* padded_offsets, const int32_t* counts, int32_t E, int32_t K,
+                               int32_t N, int64_t M_cap, int32_t dw_dtype, int32_t accumulate, void* dw,
+                               void* stream);
 
 /* ------------------------------------------------------------------------------------------
  * moe_combine - routing-weighted combine of the expert outputs back into token order.

@@ -18,7 +18,7 @@ LIB_PATH = os.path.join(PKG_DIR, LIB_NAME)
 ARCH = "gfx950"
 
 SOURCES = ["router.hip", "scores.hip", "route.hip", "quant.hip", "gemm.hip", "dense.hip", "mxfp4.hip", "mxgemm.hip",
-           "combine.hip", "api.cpp"]
+           "int8.hip", "grouped.hip", "combine.hip", "api.cpp"]
 
 # Device code: gfx950 only, no fast-math (the quantizer relies on IEEE division, fma and rint),
 # and packed fp32 instructions disabled.

@@ -719,4 +719,131 @@ int32_t moe_grouped_gemm_l2_mxfp4(const uint8_t* h_codes, const uint8_t* h_scale
   return mx_gemm(a, false, M_cap, max_rows_per_expert, stream);
 }
 
+// ---- 8-bit integers and 16-bit experts -----------------------------------------------------------
+
+static bool any_dtype_ok(int32_t d) { return dtype_ok(d) || d == MEGAMOE_DTYPE_F16; }
+static bool half_dtype_ok(int32_t d) { return d == MEGAMOE_DTYPE_BF16 || d == MEGAMOE_DTYPE_F16; }
+
+static bool int8_matrix_ok(int64_t rows, int64_t cols) {
+  return rows >= 0 && cols > 0 && cols % 16 == 0 && cols < (1 << 30) && rows < ((int64_t)1 << 37) / cols;
+}
+
+int32_t int8_quantize_act(const void* x, int32_t dtype, int64_t rows, int64_t cols, const int32_t* row_valid,
+                          int8_t* codes, float* scales, void* stream) {
+  if (!int8_matrix_ok(rows, cols) || !any_dtype_ok(dtype)) return MEGAMOE_ERR_SHAPE;
+  if (rows > 0 && (!x || !codes || !scales)) return MEGAMOE_ERR_NULL;
+  if (!aligned(x, 16) || !aligned(codes, 16) || !aligned(scales, 4) || !aligned(row_valid, 4)) return MEGAMOE_ERR_ALIGN;
+  const int32_t dev = check_device();
+  if (dev != MEGAMOE_OK) return dev;
+  return launch_status(launch_int8_quant(x, dtype, rows, cols, row_valid, codes, scales,
+                                         static_cast<hipStream_t>(stream)));
+}
+
+int32_t int8_dequantize(const int8_t* codes, const float* scales, int64_t rows, int64_t cols, int32_t dtype,
+                        void* out, void* stream) {
+  if (!int8_matrix_ok(rows, cols) || !any_dtype_ok(dtype)) return MEGAMOE_ERR_SHAPE;
+  if (rows > 0 && (!codes || !scales || !out)) return MEGAMOE_ERR_NULL;
+  if (!aligned(codes, 16) || !aligned(out, 16) || !aligned(scales, 4)) return MEGAMOE_ERR_ALIGN;
+  const int32_t dev = check_device();
+  if (dev != MEGAMOE_OK) return dev;
+  return launch_status(launch_int8_dequant(codes, scales, rows, cols, dtype, out, static_cast<hipStream_t>(stream)));
+}
+
+// Sizes of the products: K reduced and N output columns, both in elements.
+static bool product_shape_ok(int32_t E, int32_t K, int32_t N, int64_t rows) {
+  // (a row is below 2^24 bytes: the kernels address 256 of them with 32 bits)
+  return E >= 1 && E <= MEGAMOE_MAX_EXPERTS && K >= 8 && K % 8 == 0 && K < (1 << 22) && N >= 8 && N % 8 == 0 &&
+         N < (1 << 22) && rows >= 0 && rows < (int64_t)1 << 31;
+}
+
+// Checks and launch shared by the products.  rows: rows of the output buffer.
+static int32_t grouped_gemm(const GroupedArgs& a, bool l1, int64_t rows, int32_t max_rows_per_expert, void* stream) {
+  const bool i8 = a.dtype == kOperandI8;
+  if (!product_shape_ok(a.E, a.K, a.N, rows) || max_rows_per_expert < 0 || !half_dtype_ok(a.out_dtype) ||
+      (!i8 && a.out_dtype != a.dtype))
+    return MEGAMOE_ERR_SHAPE;
+  // int8: sums of K products of at most 2^14 stay below 2^31
+  if (i8 && (a.K % 16 != 0 || a.K >= (1 << 17))) return MEGAMOE_ERR_SHAPE;
+  // row offsets are 32-bit counts of 16 bytes
+  if (rows * ((int64_t)a.K * (i8 ? 1 : 2)) >= (int64_t)1 << 36) return MEGAMOE_ERR_SHAPE;
+  if (!a.w || (i8 && !a.w_scales)) return MEGAMOE_ERR_NULL;
+  if (rows > 0 && (!a.a || !a.out || (i8 && !a.a_scales))) return MEGAMOE_ERR_NULL;
+  if (!aligned(a.a, 16) || !aligned(a.w, 16) || !aligned(a.out, 16) || !aligned(a.a_scales, 4) ||
+      !aligned(a.w_scales, 4) || !aligned(a.row_token, 4) || !aligned(a.padded_offsets, 4) || !aligned(a.counts, 4))
+    return MEGAMOE_ERR_ALIGN;
+  const int32_t dev = check_device();
+  if (dev != MEGAMOE_OK) return dev;
+  if (rows == 0) return MEGAMOE_OK;  // no rows: nothing to compute or write
+  return launch_status(launch_grouped(a, l1, max_rows_per_expert, static_cast<hipStream_t>(stream)));
+}
+
+int32_t int8_linear(const int8_t* a_codes, const float* a_scales, int64_t M, int32_t K, const int8_t* w_codes,
+                    const float* w_scales, int32_t N, int32_t dtype, void* out, void* stream) {
+  const GroupedArgs a{a_codes, a_scales, nullptr, nullptr, nullptr, w_codes, w_scales, 1, K, N, M, out, kOperandI8,
+                      dtype, false};
+  return grouped_gemm(a, false, M, 0, stream);
+}
+
+int32_t int8_linear_gate_up_silu(const int8_t* a_codes, const float* a_scales, int64_t M, int32_t K,
+                                 const int8_t* w13_codes, const float* w13_scales, int32_t I, int32_t dtype, void* h,
+                                 void* stream) {
+  const GroupedArgs a{a_codes, a_scales, nullptr, nullptr, nullptr, w13_codes, w13_scales, 1, K, I, M, h, kOperandI8,
+                      dtype, false};
+  return grouped_gemm(a, true, M, 0, stream);
+}
+
+int32_t moe_grouped_gemm_l1_silu_int8(const int8_t* x_codes, const float* x_scales, const int32_t* row_token,
+                                      const int32_t* padded_offsets, const int32_t* counts, const int8_t* w13_codes,
+                                      const float* w13_scales, int32_t E, int32_t H, int32_t I, int64_t M_cap,
+                                      int32_t max_rows_per_expert, void* h_bf16, void* stream) {
+  if (!padded_offsets || !counts || (M_cap > 0 && !row_token)) return MEGAMOE_ERR_NULL;
+  const GroupedArgs a{x_codes, x_scales, row_token, padded_offsets, counts, w13_codes, w13_scales, E, H, I, 0, h_bf16,
+                      kOperandI8, MEGAMOE_DTYPE_BF16, false};
+  return grouped_gemm(a, true, M_cap, max_rows_per_expert, stream);
+}
+
+int32_t moe_grouped_gemm_l2_int8(const int8_t* h_codes, const float* h_scales, const int32_t* padded_offsets,
+                                 const int32_t* counts, const int8_t* w2_codes, const float* w2_scales, int32_t E,
+                                 int32_t H, int32_t I, int64_t M_cap, int32_t max_rows_per_expert, void* y_bf16,
+                                 void* stream) {
+  if (!padded_offsets || !counts) return MEGAMOE_ERR_NULL;
+  const GroupedArgs a{h_codes, h_scales, nullptr, padded_offsets, counts, w2_codes, w2_scales, E, I, H, 0, y_bf16,
+                      kOperandI8, MEGAMOE_DTYPE_BF16, false};
+  return grouped_gemm(a, false, M_cap, max_rows_per_expert, stream);
+}
+
+int32_t moe_grouped_gemm(const void* x, int32_t dtype, const int32_t* row_token, const int32_t* padded_offsets,
+                         const int32_t* counts, const void* w, int32_t E, int32_t K, int32_t N, int64_t M_cap,
+                         int32_t max_rows_per_expert, void* y, void* stream) {
+  if (!padded_offsets || !counts) return MEGAMOE_ERR_NULL;
+  const GroupedArgs a{x, nullptr, row_token, padded_offsets, counts, w, nullptr, E, K, N, 0, y, dtype, dtype, false};
+  return grouped_gemm(a, false, M_cap, max_rows_per_expert, stream);
+}
+
+int32_t moe_grouped_gemm_dgrad(const void* dy, int32_t dtype, const int32_t* padded_offsets, const int32_t* counts,
+                               const void* w, int32_t E, int32_t K, int32_t N, int64_t M_cap, void* dx,
+                               void* stream) {
+  if (!padded_offsets || !counts) return MEGAMOE_ERR_NULL;
+  const GroupedArgs a{dy, nullptr, nullptr, padded_offsets, counts, w, nullptr, E, N, K, 0, dx, dtype, dtype, true};
+  return grouped_gemm(a, false, M_cap, 0, stream);
+}
+
+int32_t moe_grouped_gemm_wgrad(const void* dy, const void* x, int32_t dtype, const int32_t* row_token,
+                               const int32_t* padded_offsets, const int32_t* counts, int32_t E, int32_t K, int32_t N,
+                               int64_t M_cap, int32_t dw_dtype, int32_t accumulate, void* dw, void* stream) {
+  if (!product_shape_ok(E, K, N, M_cap) || !half_dtype_ok(dtype) || (dw_dtype != dtype && dw_dtype != MEGAMOE_DTYPE_F32))
+    return MEGAMOE_ERR_SHAPE;
+  if (M_cap * ((int64_t)K * 2) >= (int64_t)1 << 36 || M_cap * ((int64_t)N * 2) >= (int64_t)1 << 36)
+    return MEGAMOE_ERR_SHAPE;
+  if (!padded_offsets || !counts || !dw || (M_cap > 0 && (!dy || !x))) return MEGAMOE_ERR_NULL;
+  if (!aligned(dy, 16) || !aligned(x, 16) || !aligned(dw, 16) || !aligned(row_token, 4) ||
+      !aligned(padded_offsets, 4) || !aligned(counts, 4))
+    return MEGAMOE_ERR_ALIGN;
+  const int32_t dev = check_device();
+  if (dev != MEGAMOE_OK) return dev;
+  if (M_cap == 0 && accumulate) return MEGAMOE_OK;  // nothing to add
+  const GroupedWgradArgs a{dy, x, row_token, padded_offsets, counts, E, K, N, dw, dtype, dw_dtype, accumulate != 0};
+  return launch_status(launch_grouped_wgrad(a, static_cast<hipStream_t>(stream)));
+}
+
 }  // extern "C"

@@ -165,6 +165,43 @@ struct MxGemmArgs {
 // max_rows: the caller's bound on an expert's rows, 0 = none.
 hipError_t launch_mx_gemm(const MxGemmArgs& a, bool l1, int64_t max_rows, hipStream_t stream);
 
+// ---- 8-bit integers ----------------------------------------------------------------------------
+hipError_t launch_int8_quant(const void* x, int dtype, int64_t rows, int64_t cols, const int32_t* row_valid,
+                             int8_t* codes, float* scales, hipStream_t stream);
+hipError_t launch_int8_dequant(const int8_t* codes, const float* scales, int64_t rows, int64_t cols, int dtype,
+                               void* out, hipStream_t stream);
+
+// ---- 16-bit and 8-bit integer products -----------------------------------------------------------
+constexpr int kOperandI8 = 100;  // beside MEGAMOE_DTYPE_* as a product's operand type
+struct GroupedArgs {
+  const void* a;                  // rows [*, K], gathered through row_token when given
+  const float* a_scales;          // int8: [*]
+  const int32_t* row_token;
+  const int32_t* padded_offsets;  // NULL with counts: one group of M rows
+  const int32_t* counts;
+  const void* w;                  // [E, N or 2N, K]; across: [E, K, N]
+  const float* w_scales;          // int8: [E, N or 2N]
+  int32_t E, K, N;                // K reduced, N output columns
+  int64_t M;                      // rows of the one group without tables
+  void* out;                      // [*, N]
+  int32_t dtype, out_dtype;
+  bool across;                    // the rows' gradient: weights are read across their rows
+};
+// max_rows: the caller's bound on an expert's rows, 0 = none.
+hipError_t launch_grouped(const GroupedArgs& a, bool l1, int64_t max_rows, hipStream_t stream);
+struct GroupedWgradArgs {
+  const void* dy;  // [*, N]
+  const void* x;   // [*, K], gathered through row_token when given
+  const int32_t* row_token;
+  const int32_t* padded_offsets;
+  const int32_t* counts;
+  int32_t E, K, N;
+  void* dw;        // [E, N, K]
+  int32_t dtype, dw_dtype;
+  bool accumulate;
+};
+hipError_t launch_grouped_wgrad(const GroupedWgradArgs& a, hipStream_t stream);
+
 // ---- dense layers (one group of M rows) -------------------------------------------------------
 // int32 workspace layout: counts [1], padded offsets [2], tile table [sched_len(1)], then the
 // identity row map [M] (gate+up only).

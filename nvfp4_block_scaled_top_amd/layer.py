@@ -353,11 +353,17 @@ class MXMoELayer:
         self.route_ws = torch.empty(max(mm.megamoe_route_workspace_bytes(T, k, E), 4), **u8)
         self.topk_ids = torch.empty(T, k, **i32)                      # written by forward_scores
         self.topk_weights = torch.empty(T, k, dtype=torch.float32, device=device)
-        self.x_codes, self.x_scales = torch.empty(T, H // 2, **u8), torch.empty(T, H // 32, **u8)
+        self.x_codes, self.x_scales = self._operand(T, H, device)
         self.h = torch.empty(self.M_cap, I, **bf16)
-        self.h_codes, self.h_scales = torch.empty(self.M_cap, I // 2, **u8), torch.empty(self.M_cap, I // 32, **u8)
+        self.h_codes, self.h_scales = self._operand(self.M_cap, I, device)
         self.y = torch.empty(self.M_cap, H, **bf16)
         self.out = torch.empty(T, H, **bf16)
+
+    @staticmethod
+    def _operand(rows: int, cols: int, device):
+        """Codes and scales of a quantized [rows, cols] tensor."""
+        u8 = dict(dtype=torch.uint8, device=device)
+        return torch.empty(rows, cols // 2, **u8), torch.empty(rows, cols // 32, **u8)
 
     def experts(self, x: torch.Tensor, topk_weights: torch.Tensor, w: MXMoEWeights, stream=None) -> torch.Tensor:
         """The steps after routing: x [T, H] bf16 -> out [T, H] bf16."""
@@ -386,3 +392,62 @@ class MXMoELayer:
                             self.counts, self.expert_offsets, self.padded_offsets, self.row_token, self.token_rows,
                             self.sched, self.route_ws, bias=bias, stream=stream, **router)
         return self.experts(x, self.topk_weights, w, stream)
+
+
+@dataclasses.dataclass
+class Int8MoEWeights:
+    """int8 expert weights with a scale for each output channel."""
+    w13_codes: torch.Tensor   # int8 [E, 2I, H]
+    w13_scales: torch.Tensor  # float32 [E, 2I]
+    w2_codes: torch.Tensor    # int8 [E, H, I]
+    w2_scales: torch.Tensor   # float32 [E, H]
+
+    @property
+    def num_experts(self) -> int:
+        return self.w13_codes.shape[0]
+
+    @property
+    def hidden(self) -> int:
+        return self.w13_codes.shape[2]
+
+    @property
+    def intermediate(self) -> int:
+        return self.w13_codes.shape[1] // 2
+
+    def nbytes_expert(self) -> int:
+        """Bytes of one expert (codes and scales)."""
+        return sum(t[0].numel() * t.element_size()
+                   for t in (self.w13_codes, self.w13_scales, self.w2_codes, self.w2_scales))
+
+    @staticmethod
+    def empty(E: int, H: int, I: int, device="cuda") -> "Int8MoEWeights":
+        i8, f32 = dict(dtype=torch.int8, device=device), dict(dtype=torch.float32, device=device)
+        return Int8MoEWeights(torch.empty(E, 2 * I, H, **i8), torch.empty(E, 2 * I, **f32), torch.empty(E, H, I, **i8),
+                              torch.empty(E, H, **f32))
+
+
+def quantize_expert_int8_into(weights: Int8MoEWeights, e: int, w13: torch.Tensor, w2: torch.Tensor) -> None:
+    """Quantize one expert's bf16, float16 or float32 matrices on the GPU, a scale for each output channel."""
+    mm.int8_quantize_act(w13, weights.w13_codes[e], weights.w13_scales[e])
+    mm.int8_quantize_act(w2, weights.w2_codes[e], weights.w2_scales[e])
+
+
+class Int8MoELayer(MXMoELayer):
+    """The routed-expert layer on int8 weights (a scale for each channel) and int8 activations (a scale for
+    each token): the steps and the forward calls of MXMoELayer."""
+
+    @staticmethod
+    def _operand(rows: int, cols: int, device):
+        return (torch.empty(rows, cols, dtype=torch.int8, device=device),
+                torch.empty(rows, dtype=torch.float32, device=device))
+
+    def experts(self, x: torch.Tensor, topk_weights: torch.Tensor, w: Int8MoEWeights, stream=None) -> torch.Tensor:
+        """The steps after routing: x [T, H] bf16 -> out [T, H] bf16."""
+        mm.int8_quantize_act(x, self.x_codes, self.x_scales, stream=stream)
+        mm.moe_grouped_gemm_l1_silu_int8(self.x_codes, self.x_scales, self.row_token, self.padded_offsets, self.counts,
+                                         w.w13_codes, w.w13_scales, self.h, max_rows_per_expert=self.T, stream=stream)
+        mm.int8_quantize_act(self.h, self.h_codes, self.h_scales, row_valid=self.row_token, stream=stream)
+        mm.moe_grouped_gemm_l2_int8(self.h_codes, self.h_scales, self.padded_offsets, self.counts, w.w2_codes,
+                                    w.w2_scales, self.y, max_rows_per_expert=self.T, stream=stream)
+        mm.moe_combine(self.y, self.token_rows, topk_weights, self.out, stream=stream)
+        return self.out

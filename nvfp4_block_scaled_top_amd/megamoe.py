@@ -40,6 +40,11 @@ SCORES = {"softmax": 0, "sigmoid": 1}
 #: Element types of the calls that take two (MEGAMOE_DTYPE_*); bf16 may be viewed as int16.
 DTYPES = {torch.bfloat16: 0, torch.int16: 0, torch.float32: 1}
 
+#: Those of the int8 calls (a quantizer takes all of them, a product writes the two of 16 bits) and of the
+#: 16-bit experts' products.
+ANY_DTYPES = {**DTYPES, torch.float16: 2}
+HALF_DTYPES = {torch.bfloat16: 0, torch.int16: 0, torch.float16: 2}
+
 #: Exported symbols and their C signatures (restype, argtypes), as declared in include/megamoe.h.
 _P = ctypes.c_void_p
 _I32, _I64, _SZ, _F = ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float
@@ -61,6 +66,15 @@ SIGNATURES = {
     "mxfp4_linear_gate_up_silu": (_I32, [_P, _P, _I64, _I32, _P, _P, _I32, _P, _P]),
     "moe_grouped_gemm_l1_silu_mxfp4": (_I32, [_P, _P, _P, _P, _P, _P, _P, _I32, _I32, _I32, _I64, _I32, _P, _P]),
     "moe_grouped_gemm_l2_mxfp4": (_I32, [_P, _P, _P, _P, _P, _P, _I32, _I32, _I32, _I64, _I32, _P, _P]),
+    "int8_quantize_act": (_I32, [_P, _I32, _I64, _I64, _P, _P, _P, _P]),
+    "int8_dequantize": (_I32, [_P, _P, _I64, _I64, _I32, _P, _P]),
+    "int8_linear": (_I32, [_P, _P, _I64, _I32, _P, _P, _I32, _I32, _P, _P]),
+    "int8_linear_gate_up_silu": (_I32, [_P, _P, _I64, _I32, _P, _P, _I32, _I32, _P, _P]),
+    "moe_grouped_gemm_l1_silu_int8": (_I32, [_P, _P, _P, _P, _P, _P, _P, _I32, _I32, _I32, _I64, _I32, _P, _P]),
+    "moe_grouped_gemm_l2_int8": (_I32, [_P, _P, _P, _P, _P, _P, _I32, _I32, _I32, _I64, _I32, _P, _P]),
+    "moe_grouped_gemm": (_I32, [_P, _I32, _P, _P, _P, _P, _I32, _I32, _I32, _I64, _I32, _P, _P]),
+    "moe_grouped_gemm_dgrad": (_I32, [_P, _I32, _P, _P, _P, _I32, _I32, _I32, _I64, _P, _P]),
+    "moe_grouped_gemm_wgrad": (_I32, [_P, _P, _I32, _P, _P, _P, _I32, _I32, _I32, _I64, _I32, _I32, _P, _P]),
     "moe_route_quantize": (_I32, [_P, _I32, _I32, _I32, _I32, _I32, _I32, _P, _P, _P, _P, _P, _P, _P, _SZ, _P, _I64,
                                   _P, _P, _P, _P, _P, _SZ, _P]),
     "moe_grouped_gemm_l1_silu_nvfp4": (_I32, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I32, _I32, _I32, _I64, _I32,
@@ -515,3 +529,134 @@ def moe_grouped_gemm_l2_mxfp4(h_codes, h_scales, padded_offsets, counts, w2_code
         _arg("padded_offsets", padded_offsets, _INT, (E + 1,), dev), _arg("counts", counts, _INT, (E,), dev),
         _arg("w2_codes", w2_codes, _U8, (E, H, Ih), dev), _arg("w2_scales", w2_scales, _U8, (E, H, Ih // 16), dev), E, H,
         2 * Ih, M_cap, max_rows_per_expert, _arg("y_bf16", y_bf16, _BF16, (M_cap, H), dev), st))
+
+
+# ---- 8-bit integers ------------------------------------------------------------------------------
+
+_I8 = (torch.int8,)
+
+
+def int8_quantize_act(x, codes, scales, row_valid=None, stream=None):
+    """x [rows, cols] bf16 (also viewed as int16), float16 or float32 -> codes int8 [rows, cols], scales
+    float32 [rows]."""
+    rows, cols = x.shape
+    dev, st = _on(x, stream)
+    _check("int8_quantize_act", lib().int8_quantize_act(
+        _arg("x", x, ANY_DTYPES, (rows, cols), dev), ANY_DTYPES[x.dtype], rows, cols,
+        None if row_valid is None else _arg("row_valid", row_valid, _INT, (rows,), dev),
+        _arg("codes", codes, _I8, (rows, cols), dev), _arg("scales", scales, _F32, (rows,), dev), st))
+
+
+def int8_dequantize(codes, scales, out, stream=None):
+    """out [rows, cols] bf16, float16 or float32."""
+    rows, cols = codes.shape
+    dev, st = _on(codes, stream)
+    _check("int8_dequantize", lib().int8_dequantize(
+        _arg("codes", codes, _I8, (rows, cols), dev), _arg("scales", scales, _F32, (rows,), dev), rows, cols,
+        ANY_DTYPES.get(out.dtype, -1), _arg("out", out, ANY_DTYPES, (rows, cols), dev), st))
+
+
+def int8_linear(a_codes, a_scales, w_codes, w_scales, out, stream=None):
+    """out [M, N] bf16 or float16."""
+    M, K = a_codes.shape
+    N = w_codes.shape[0]
+    dev, st = _on(a_codes, stream)
+    _check("int8_linear", lib().int8_linear(
+        _arg("a_codes", a_codes, _I8, (M, K), dev), _arg("a_scales", a_scales, _F32, (M,), dev), M, K,
+        _arg("w_codes", w_codes, _I8, (N, K), dev), _arg("w_scales", w_scales, _F32, (N,), dev), N,
+        HALF_DTYPES.get(out.dtype, -1), _arg("out", out, HALF_DTYPES, (M, N), dev), st))
+
+
+def int8_linear_gate_up_silu(a_codes, a_scales, w13_codes, w13_scales, h, stream=None):
+    """h [M, I] bf16 or float16."""
+    M, K = a_codes.shape
+    I = h.shape[1]
+    dev, st = _on(a_codes, stream)
+    _check("int8_linear_gate_up_silu", lib().int8_linear_gate_up_silu(
+        _arg("a_codes", a_codes, _I8, (M, K), dev), _arg("a_scales", a_scales, _F32, (M,), dev), M, K,
+        _arg("w13_codes", w13_codes, _I8, (2 * I, K), dev), _arg("w13_scales", w13_scales, _F32, (2 * I,), dev), I,
+        HALF_DTYPES.get(h.dtype, -1), _arg("h", h, HALF_DTYPES, (M, I), dev), st))
+
+
+def _gathered_bytes(name, t):
+    """Row offsets are 32-bit counts of 16 bytes; the library is not told how many rows a gathered tensor has."""
+    if _nbytes(t) >= 1 << 36:
+        raise MegaMoEError(f"{name} has {_nbytes(t)} bytes, expected less than 2^36")
+
+
+def moe_grouped_gemm_l1_silu_int8(x_codes, x_scales, row_token, padded_offsets, counts, w13_codes, w13_scales, h_bf16,
+                                  max_rows_per_expert=0, stream=None):
+    """row_token, padded_offsets and counts as moe_route_permute wrote them (row_token holds token ids
+    of x_codes' rows); h_bf16 [M_cap, I]."""
+    T, H = x_codes.shape
+    E, I2, _ = w13_codes.shape
+    M_cap, I = h_bf16.shape
+    _gathered_bytes("x_codes", x_codes)
+    dev, st = _on(x_codes, stream)
+    _check("moe_grouped_gemm_l1_silu_int8", lib().moe_grouped_gemm_l1_silu_int8(
+        _arg("x_codes", x_codes, _I8, (T, H), dev), _arg("x_scales", x_scales, _F32, (T,), dev),
+        _arg("row_token", row_token, _INT, (M_cap,), dev), _arg("padded_offsets", padded_offsets, _INT, (E + 1,), dev),
+        _arg("counts", counts, _INT, (E,), dev), _arg("w13_codes", w13_codes, _I8, (E, 2 * I, H), dev),
+        _arg("w13_scales", w13_scales, _F32, (E, 2 * I), dev), E, H, I, M_cap, max_rows_per_expert,
+        _arg("h_bf16", h_bf16, _BF16, (M_cap, I), dev), st))
+
+
+def moe_grouped_gemm_l2_int8(h_codes, h_scales, padded_offsets, counts, w2_codes, w2_scales, y_bf16,
+                             max_rows_per_expert=0, stream=None):
+    M_cap, I = h_codes.shape
+    E, H, _ = w2_codes.shape
+    dev, st = _on(h_codes, stream)
+    _check("moe_grouped_gemm_l2_int8", lib().moe_grouped_gemm_l2_int8(
+        _arg("h_codes", h_codes, _I8, (M_cap, I), dev), _arg("h_scales", h_scales, _F32, (M_cap,), dev),
+        _arg("padded_offsets", padded_offsets, _INT, (E + 1,), dev), _arg("counts", counts, _INT, (E,), dev),
+        _arg("w2_codes", w2_codes, _I8, (E, H, I), dev), _arg("w2_scales", w2_scales, _F32, (E, H), dev), E, H, I, M_cap,
+        max_rows_per_expert, _arg("y_bf16", y_bf16, _BF16, (M_cap, H), dev), st))
+
+
+# ---- experts in 16 bits --------------------------------------------------------------------------
+
+def moe_grouped_gemm(x, w, padded_offsets, counts, y, row_token=None, max_rows_per_expert=0, stream=None):
+    """y[r] = x[row_token[r] or r] @ w[e].T for the rows r of each expert e.  x [T or M_cap, K], w [E, N, K] and
+    y [M_cap, N], all bf16 (also viewed as int16) or all float16."""
+    rows, K = x.shape
+    E, N, _ = w.shape
+    M_cap = y.shape[0]
+    _gathered_bytes("x", x)
+    dev, st = _on(x, stream)
+    dt = (x.dtype,)
+    _check("moe_grouped_gemm", lib().moe_grouped_gemm(
+        _arg("x", x, HALF_DTYPES, (rows if row_token is not None else M_cap, K), dev), HALF_DTYPES[x.dtype],
+        None if row_token is None else _arg("row_token", row_token, _INT, (M_cap,), dev),
+        _arg("padded_offsets", padded_offsets, _INT, (E + 1,), dev), _arg("counts", counts, _INT, (E,), dev),
+        _arg("w", w, dt, (E, N, K), dev), E, K, N, M_cap, max_rows_per_expert, _arg("y", y, dt, (M_cap, N), dev), st))
+
+
+def moe_grouped_gemm_dgrad(dy, w, padded_offsets, counts, dx, stream=None):
+    """Gradient of moe_grouped_gemm with respect to its rows: dx[r] = dy[r] @ w[e].  dy [M_cap, N], w [E, N, K],
+    dx [M_cap, K]; a gathered x's gradient is the sum of the rows that read it."""
+    M_cap, N = dy.shape
+    E, _, K = w.shape
+    dev, st = _on(dy, stream)
+    dt = (dy.dtype,)
+    _check("moe_grouped_gemm_dgrad", lib().moe_grouped_gemm_dgrad(
+        _arg("dy", dy, HALF_DTYPES, (M_cap, N), dev), HALF_DTYPES[dy.dtype],
+        _arg("padded_offsets", padded_offsets, _INT, (E + 1,), dev), _arg("counts", counts, _INT, (E,), dev),
+        _arg("w", w, dt, (E, N, K), dev), E, K, N, M_cap, _arg("dx", dx, dt, (M_cap, K), dev), st))
+
+
+def moe_grouped_gemm_wgrad(dy, x, padded_offsets, counts, dw, row_token=None, accumulate=False, stream=None):
+    """Gradient of moe_grouped_gemm with respect to the weights: dw[e] (+)= dy[rows of e].T @ x[their sources].
+    dw [E, N, K] in the type of dy and x, or float32."""
+    M_cap, N = dy.shape
+    rows, K = x.shape
+    E = dw.shape[0]
+    _gathered_bytes("x", x)
+    dev, st = _on(dy, stream)
+    dt = (dy.dtype,)
+    _check("moe_grouped_gemm_wgrad", lib().moe_grouped_gemm_wgrad(
+        _arg("dy", dy, HALF_DTYPES, (M_cap, N), dev),
+        _arg("x", x, dt, (rows if row_token is not None else M_cap, K), dev), HALF_DTYPES[dy.dtype],
+        None if row_token is None else _arg("row_token", row_token, _INT, (M_cap,), dev),
+        _arg("padded_offsets", padded_offsets, _INT, (E + 1,), dev), _arg("counts", counts, _INT, (E,), dev), E, K, N,
+        M_cap, ANY_DTYPES.get(dw.dtype, -1), int(accumulate), _arg("dw", dw, (dy.dtype, torch.float32), (E, N, K), dev),
+        st))
