@@ -1,97 +1,762 @@
 // Products of 16-bit and 8-bit integer operands, dense and grouped over experts of ragged sizes, and the
 // 16-bit product's gradients.
+//
+//   rows      out[r, n]  = sum_k a[src(r), k] * w[e, n, k]        (gate+up: SiLU of one half times the other)
+//   across    out[r, n]  = sum_k a[r, k] * w[e, k, n]             (the rows' gradient)
+//   weights   dw[e,n,k]  = sum over the expert's rows r of dy[r, n] * x[src(r), k]
+//
+// The matrix instruction's A operand is the side whose index is contiguous in the output (weights, or x), its B
+// operand the other (token rows, or dy): a lane then ends with four consecutive columns of one output row.  Lane
+// (r, g) of a 16-row fragment holds 16 bytes of its row, the same 16 bytes of K on both sides.
+#include <atomic>
+
 #include "device_common.h"
 #include "internal.h"
+#include "lds_dma.h"
 
 namespace megamoe {
 
-typedef __bf16 bf16s;
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+
+constexpr int kGtDevices = 64;
+constexpr int kGtPlain = 0, kGtGateUp = 1, kGtAcross = 2;  // operations of gt_kernel
+constexpr int kGtGrid = 256;                        // one workgroup a CU
+constexpr int kGtWaves = 4, kGtThreads = kGtWaves * kWave;
+constexpr int kGtCols = 256, kGtRows = 256;         // A-side and B-side rows of the largest tile
+constexpr int kGtStage = 128;                       // bytes of K a stage (64 or 128 elements)
+constexpr int kGtSide = kGtCols * kGtStage;         // LDS bytes of a stage's A side
+constexpr int kGtLds = 160 * 1024;
+constexpr int kGtBand = 8;                          // m-tiles walked together, for L2 reuse of the weights
+// The kernels have no static LDS: addresses start at 0.  At the end: two list lengths, m-tile prefix int32 [E + 1],
+// two lists uint16 [E].
+constexpr int kGtLists = kGtLds - 8224;
+static_assert(8 + 4 * (MEGAMOE_MAX_EXPERTS + 1) + 4 * MEGAMOE_MAX_EXPERTS <= kGtLds - kGtLists, "the lists fit");
+
+__device__ const uint32_t g_zeros[4] = {0u, 0u, 0u, 0u};  // what a load brings beyond the reduced dimension
 
 __device__ __forceinline__ float g_silu(float g) {
   return g * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-g * 1.4426950408889634f));
 }
 
+// Workgroup barrier that no LDS access is moved across.  Vector memory loads stay in flight.
+__device__ __forceinline__ void g_barrier() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+__device__ __forceinline__ void g_wait_lds() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
+  asm volatile("" ::: "memory");
+}
+
+// A word of a table that the kernel does not write, from a wave-uniform address: a scalar load, which does not wait
+// for the vector loads in flight.
+__device__ __forceinline__ int g_scalar(const int32_t* p) {
+  const uint64_t at = scalar_addr(reinterpret_cast<const uint8_t*>(p));
+  return *reinterpret_cast<const __attribute__((address_space(4))) int32_t*>(at);
+}
+
+// What follows from the lane is computed where it is used, not held in registers through a loop.
+__device__ __forceinline__ int g_here(int v) {
+  asm volatile("" : "+v"(v));
+  return v;
+}
+
+// Operand types: the accumulator and the 16x16 matrix instruction over 64 bytes of K (16x16x32 or 16x16x64).  Inline
+// assembly keeps the accumulators in accumulation registers, all 256 of them in the largest tile: left to itself the
+// compiler moves them to and fro (408 moves beside 64 products).  What it does not know of these instructions is
+// kept by hand: an accumulator is met again after at least 16 others, and g_settle stands between the products
+// and any other write or read of it.
 template <int kDtype>
-__device__ __forceinline__ float g_load(const void* p, int64_t i) {
-  if constexpr (kDtype == kOperandI8) return (float)static_cast<const int8_t*>(p)[i];
-  else if constexpr (kDtype == MEGAMOE_DTYPE_BF16) return bf16_bits_to_f32(static_cast<const uint16_t*>(p)[i]);
-  else return (float)static_cast<const _Float16*>(p)[i];
+struct GType {
+  typedef f32x4 acc;
+  static constexpr int kBytes = 2;
+  static __device__ __forceinline__ void mfma(u32x4 a, u32x4 b, acc& c) {
+    if constexpr (kDtype == MEGAMOE_DTYPE_BF16) asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b));
+    else asm volatile("v_mfma_f32_16x16x32_f16 %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b));
+  }
+};
+template <>
+struct GType<kOperandI8> {
+  typedef i32x4 acc;
+  static constexpr int kBytes = 1;
+  static __device__ __forceinline__ void mfma(u32x4 a, u32x4 b, acc& c) {
+    asm volatile("v_mfma_i32_16x16x64_i8 %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b));
+  }
+};
+// Accumulators in front of other instructions than the products: a result can be read 18 cycles after its
+// instruction, and is read by the next one 2 after a write.
+template <typename A, int n>
+__device__ __forceinline__ void g_settle(A (&c)[n]) {
+  static_assert(n == 4 || n == 8, "fragments of a wave");
+  if constexpr (n == 8)
+    asm volatile("s_nop 15\n\ts_nop 7" : "+a"(c[0]), "+a"(c[1]), "+a"(c[2]), "+a"(c[3]), "+a"(c[4]), "+a"(c[5]), "+a"(c[6]), "+a"(c[7]));
+  else
+    asm volatile("s_nop 15\n\ts_nop 7" : "+a"(c[0]), "+a"(c[1]), "+a"(c[2]), "+a"(c[3]));
 }
 
-__device__ __forceinline__ void g_store(void* p, int64_t i, int dtype, float v) {
-  if (dtype == MEGAMOE_DTYPE_F32) static_cast<float*>(p)[i] = v;
-  else if (dtype == MEGAMOE_DTYPE_BF16) static_cast<uint16_t*>(p)[i] = (uint16_t)f32_to_bf16_any(v);
-  else static_cast<_Float16*>(p)[i] = (_Float16)v;
+__device__ __forceinline__ u32x4 lds_read16(uint32_t at) {
+  return *reinterpret_cast<const __attribute__((address_space(3))) u32x4*>(at);
 }
-__device__ __forceinline__ float g_old(const void* p, int64_t i, int dtype) {
-  return dtype == MEGAMOE_DTYPE_F32 ? static_cast<const float*>(p)[i]
-         : dtype == MEGAMOE_DTYPE_BF16 ? bf16_bits_to_f32(static_cast<const uint16_t*>(p)[i])
-                                       : (float)static_cast<const _Float16*>(p)[i];
+template <typename T>
+__device__ __forceinline__ T lds_read(uint32_t at) {
+  return *reinterpret_cast<const __attribute__((address_space(3))) T*>(at);
 }
 
-// One output element a thread; the reduced dimension from memory.
-template <int kDtype, bool kL1>
-__global__ __launch_bounds__(256) void g_rows_kernel(GroupedArgs p) {
-  const int e = blockIdx.y;
-  const int64_t cnt = p.counts ? p.counts[e] : p.M, first = p.padded_offsets ? p.padded_offsets[e] : 0;
-  const int col = blockIdx.x * 16 + threadIdx.x % 16;
-  if (col >= p.N) return;
-  for (int64_t r = blockIdx.z * 16 + threadIdx.x / 16; r < cnt; r += 16 * gridDim.z) {
-    const int64_t row = first + r, src = p.row_token ? p.row_token[row] : row;
-    float z[2];
-    for (int up = 0; up < (kL1 ? 2 : 1); ++up) {
-      // weights [E, N or 2N, K], or [E, K, N] where they are read across
-      const int64_t wrow = ((int64_t)e * (kL1 ? 2 : 1) + up) * p.N + col;
-      float acc = 0.0f;
-      int iacc = 0;
-      for (int k = 0; k < p.K; ++k) {
-        const float x = g_load<kDtype>(p.a, src * p.K + k);
-        const float w = p.across ? g_load<kDtype>(p.w, ((int64_t)e * p.K + k) * p.N + col) : g_load<kDtype>(p.w, wrow * p.K + k);
-        if constexpr (kDtype == kOperandI8) iacc += (int)x * (int)w;
-        else acc += x * w;
-      }
-      if constexpr (kDtype == kOperandI8) acc = (float)iacc * p.w_scales[wrow] * p.a_scales[src];
-      z[up] = acc;
+// A 16-row fragment of a side that lies across: LDS holds 64 rows of the reduced dimension, 512 bytes (256
+// columns) each.  The transposing read gives lane i of 16 lanes column i of the four rows by 16 columns whose
+// 8-byte pieces the lanes point at: two of them make the lane's eight values of K.
+__device__ __forceinline__ u32x4 lds_read_across(uint32_t at) {
+  typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+  const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(reinterpret_cast<lds_s16x4*>(at));
+  const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(reinterpret_cast<lds_s16x4*>(at + 4 * 512));
+  const u32x2 l = __builtin_bit_cast(u32x2, lo), h = __builtin_bit_cast(u32x2, hi);
+  return u32x4{l[0], l[1], h[0], h[1]};
+}
+
+__device__ __forceinline__ uint32_t g_pack2(float a, float b, bool f16) {
+  return f16 ? __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{a, b}, f16x2))
+             : __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{a, b}, bf16x2));
+}
+// Two 16-column blocks of an output row, four consecutive columns of each a lane (g = lane / 16: columns 4g) ->
+// eight consecutive ones: of block g % 2, from column 8 (g / 2) on.
+__device__ __forceinline__ u32x4 g_gather8(u32x2 lo, u32x2 hi) {
+  const auto a = __builtin_amdgcn_permlane16_swap(lo[0], hi[0], false, false);
+  const auto b = __builtin_amdgcn_permlane16_swap(lo[1], hi[1], false, false);
+  return u32x4{a[0], b[0], a[1], b[1]};
+}
+
+// ============================================================================================
+// rows, gate+up and across: 256 weight rows x BM token rows a tile, BM = 64 WB = 256, or 128 or 64 for an
+// expert's last rows when they fit; one persistent workgroup of 4 waves a CU takes all tiles of 256 rows, then
+// those of 128, then those of 64.
+//
+// A stage is 128 bytes of K of every row.  Stages go from global memory straight into a ring of LDS slots (2 of
+// 64 KB, or 3 of the lower tiles' 48 or 40) and run on across tiles.  A stage is two steps of 64 bytes; a step's
+// operands are read from LDS while the step before is multiplied.  Between the two steps of stage s a wave has
+// read all of s: it waits for its loads of stage s + 1, and one barrier makes everyone's visible and says that
+// s's slot is free, into which the second step requests the stage after the ring's last.
+// ============================================================================================
+template <int WB>
+struct GtShape {
+  static constexpr int WM = WB == 1 ? 1 : 2, WN = kGtWaves / WM;  // waves along token rows, weight rows
+  static constexpr int MF = 4 * WB / WM, NF = 16 / WN;            // a wave's fragments of either side
+  static constexpr int D = WB == 4 ? 2 : 3;                       // slots
+  static constexpr int kSlot = kGtSide + 64 * WB * kGtStage;
+  static constexpr int kLoads = 8 + 2 * WB;                       // load instructions a wave and stage
+  // LDS behind the slots: the tokens of two tiles' rows, the scales of D + 1 tiles
+  static constexpr int kRowsAt = D * kSlot, kScalesAt = kRowsAt + 2 * 64 * WB * 4;
+  static constexpr int kScaleBuf = 4 * (kGtCols + 64 * WB);
+  static_assert(kScalesAt + (D + 1) * kScaleBuf <= kGtLists, "the LDS layout fits");
+};
+
+struct GtTile {
+  int e, nt, left;  // expert, n-tile, real rows from row0 on
+  int64_t row0;
+};
+
+template <int kOp, int kDtype, int WB, typename Find>
+__device__ __forceinline__ void gt_phase(const GroupedArgs& p, int64_t t0, int64_t total, const Find& find) {
+  typedef GtShape<WB> S;
+  typedef GType<kDtype> T;
+  constexpr bool kL1 = kOp == kGtGateUp, kAcross = kOp == kGtAcross, kI8 = kDtype == kOperandI8;
+  constexpr int cols = kL1 ? kGtCols / 2 : kGtCols;  // output columns of a tile
+  constexpr int WN = S::WN, MF = S::MF, NF = S::NF, D = S::D, L = S::kLoads;
+  if (t0 >= total) return;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), lane = lane_id();
+  const int64_t RB = (int64_t)p.K * T::kBytes;                    // bytes of a row of K
+  const int64_t NB = (int64_t)p.N * T::kBytes;                    // across: bytes of a weight row
+  const int nks = (int)((RB + kGtStage - 1) / kGtStage);
+  const uint8_t* const pad = reinterpret_cast<const uint8_t*>(g_zeros);
+  const int piece = (lane & 7) ^ (lane >> 4);  // of 8 rows of an even load instruction (odd: ^ 4)
+
+  // ---- loads -------------------------------------------------------------------------------------
+  GtTile ld;
+  int64_t lt = t0;
+  int lks = 0, lslot = 0, lseq = 0;
+  const uint8_t *w_at = nullptr, *w_up = nullptr, *a_at = nullptr;  // of the stage to request
+  uint32_t w_off[8], a_off[2 * WB];
+  const auto fetch_rows = [&](int64_t t, int buf) __attribute__((always_inline)) {  // tokens of tile t's rows
+    if (!kAcross && p.row_token != nullptr && wave < WB && t < total) {
+      const GtTile x = find(t);
+      const int R = 64 * wave + g_here(lane);
+      dma4(reinterpret_cast<const uint8_t*>(p.row_token + x.row0 + (R < x.left ? R : x.left - 1)),
+           S::kRowsAt + 4 * (64 * WB * buf + 64 * wave));
     }
-    g_store(p.out, row * p.N + col, p.out_dtype, kL1 ? g_silu(z[0]) * z[1] : z[0]);
+  };
+  // Source of the tile's token row R, and weight row (output column) of its row R; rows past the tile's end read
+  // its last row, columns past the last one the last: what they feed is not stored.
+  const auto a_row = [&](int R) __attribute__((always_inline)) -> uint32_t {
+    if (!kAcross && p.row_token != nullptr) return lds_read<uint32_t>(S::kRowsAt + 4 * (64 * WB * (lseq & 1) + R));
+    return (uint32_t)((int)ld.row0 + (R < ld.left ? R : ld.left - 1));
+  };
+  const auto w_col = [&](int R) __attribute__((always_inline)) {
+    constexpr int per = kGtCols / WN;  // rows of a wave: kL1: the first half gate, the second up
+    const int c = ld.nt * cols + (kL1 ? R / per * (per / 2) + R % (per / 2) : R);
+    return c < p.N ? c : p.N - 1;
+  };
+  const auto enter = [&]() __attribute__((always_inline)) {  // tile lt
+    const int ln = g_here(lane);
+    ld = find(lt);
+    a_at = static_cast<const uint8_t*>(p.a);
+#pragma unroll
+    for (int j = 0; j < 2 * WB; ++j) {
+      a_off[j] = a_row(16 * WB * wave + 8 * j + ln / 8) * (uint32_t)(RB / 16) + (piece ^ ((j & 1) << 2));
+    }
+    if constexpr (kAcross) {
+      w_at = static_cast<const uint8_t*>(p.w) + (int64_t)ld.e * p.K * NB + (int64_t)ld.nt * cols * T::kBytes;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int n = 2 * j + (ln >> 5), c = (ln & 31) ^ (((n & 3) | ((j >> 2) << 2)) << 1);
+        const int last = p.N / 8 - 1 - ld.nt * (cols / 8);
+        w_off[j] = (uint32_t)(16 * wave + n) * (uint32_t)NB + 16 * (c < last ? c : last);
+      }
+    } else {
+      const int64_t c0 = (int64_t)ld.nt * cols;
+      w_at = static_cast<const uint8_t*>(p.w) + ((int64_t)ld.e * (kL1 ? 2 : 1) * p.N + c0) * RB;
+      w_up = w_at + (int64_t)p.N * RB;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        w_off[j] = (uint32_t)(w_col(64 * wave + 8 * j + ln / 8) - (int)c0) * (uint32_t)RB + 16 * (piece ^ ((j & 1) << 2));
+      }
+    }
+    if constexpr (kI8) {  // the tile's scales: weight rows by all waves, token rows by WB of them
+      const uint32_t to = S::kScalesAt + (lseq % (D + 1)) * S::kScaleBuf;
+      const int R = 64 * wave + ln;
+      const bool up = kL1 && R % (kGtCols / WN) >= kGtCols / WN / 2;
+      dma4(reinterpret_cast<const uint8_t*>(p.w_scales + (int64_t)ld.e * (kL1 ? 2 : 1) * p.N + (up ? p.N : 0) + w_col(R)),
+           to + 256 * wave);
+      if (wave < WB) dma4(reinterpret_cast<const uint8_t*>(p.a_scales + a_row(R)), to + 4 * kGtCols + 256 * wave);
+    }
+    fetch_rows(lt + kGtGrid, (lseq + 1) & 1);
+    ++lseq;
+  };
+  // Load j of the stage at (lt, lks) into slot lslot: weights, then token rows.
+  const auto load = [&](int j) __attribute__((always_inline)) {
+    const uint32_t slot = lslot * S::kSlot;
+    const int left = (int)((RB - (int64_t)lks * kGtStage) / 16);  // pieces of K from this stage on
+    if (j < 8) {
+      const bool up = kL1 && (WN == 2 ? wave & 1 : j >= 4);
+      const uint8_t* src = (up ? w_up : w_at) + w_off[j];
+      const int k = kAcross ? 2 * wave + (2 * j + (lane >> 5)) / 8 : piece ^ ((j & 1) << 2);
+      src = k < left ? src : pad;
+      // the lower tiles are mostly an expert's only ones: its weights are read once, past the caches
+      if constexpr (WB < 4) dma16nt(src, slot + 1024 * (8 * wave + j));
+      else dma16(src, slot + 1024 * (8 * wave + j));
+    } else {
+      const int i = j - 8;
+      const uint8_t* src = a_at + (uint64_t)a_off[i] * 16;
+      src = (piece ^ ((i & 1) << 2)) < left ? src : pad;
+      dma16(src, slot + kGtSide + 1024 * (2 * WB * wave + i));
+    }
+  };
+  const auto loaded = [&]() __attribute__((always_inline)) {
+    a_at += kGtStage;
+    w_at += kAcross ? 64 * NB : kGtStage;
+    if constexpr (kL1) w_up += kGtStage;
+    lslot = lslot + 1 == D ? 0 : lslot + 1;
+    if (++lks == nks) {
+      lks = 0;
+      lt += kGtGrid;
+    }
+  };
+
+  // ---- operands ------------------------------------------------------------------------------------
+  const int wm = wave / WN, wn = wave % WN, r = lane & 15, g = lane >> 4;
+  const uint32_t along = r * kGtStage + 16 * (g ^ ((r >> 1) & 7));
+  const uint32_t b_base = kGtSide + wm * (16 * MF) * kGtStage + along;
+  const int jj = (lane & 15) >> 2;
+  const uint32_t a_base = kAcross ? (8 * g + jj) * 512 + (((NF * wn) ^ (jj | ((g & 1) << 2))) * 32) + (lane & 3) * 8
+                                  : wn * (16 * NF) * kGtStage + along;
+  u32x4 a[2][NF], b[2][MF];
+  const auto read_a = [&](uint32_t slot, int st, int f) __attribute__((always_inline)) {
+    if constexpr (kAcross) a[st][f] = lds_read_across(slot + (a_base ^ (f * 32)) + st * 32 * 512);
+    else a[st][f] = lds_read16(slot + (a_base ^ (st * 64)) + f * 16 * kGtStage);
+  };
+  const auto read_b = [&](uint32_t slot, int st, int m) __attribute__((always_inline)) {
+    b[st][m] = lds_read16(slot + (b_base ^ (st * 64)) + m * 16 * kGtStage);
+  };
+  const auto read_one = [&](uint32_t slot, int st, int i) __attribute__((always_inline)) {
+    if (i < MF) read_b(slot, st, i);
+    else read_a(slot, st, i - MF);
+  };
+
+  g_barrier();  // the phase before has been read from LDS
+  fetch_rows(lt, 0);
+  wait_vmcnt<0>();
+  g_barrier();
+  int issued = 0;
+  for (; issued < D && lt < total; ++issued) {
+    if (lks == 0) {
+      if (issued > 0) {  // its rows were asked for with the tile before
+        wait_vmcnt<0>();
+        g_barrier();
+      }
+      enter();
+    }
+#pragma unroll
+    for (int j = 0; j < L; ++j) load(j);
+    loaded();
+  }
+  if (issued == D) wait_vmcnt<(D - 1) * L>();
+  else wait_vmcnt<0>();
+  g_barrier();
+#pragma unroll
+  for (int i = 0; i < MF + NF; ++i) read_one(0, 0, i);
+
+  int ahead = issued;  // stages requested and not yet multiplied
+  int slot = 0, seq = 0;
+  for (int64_t t = t0; t < total; t += kGtGrid) {
+    typename T::acc acc[MF][NF];
+#pragma unroll
+    for (int m = 0; m < MF; ++m)
+#pragma unroll
+      for (int f = 0; f < NF; ++f)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) acc[m][f][q] = 0;
+#pragma unroll
+    for (int m = 0; m < MF; ++m) g_settle(acc[m]);
+    for (int ks = 0; ks < nks; ++ks) {
+      const int nslot = slot + 1 == D ? 0 : slot + 1;
+      constexpr int kGroups = NF > 4 ? NF - 2 : NF - 1, kPer = (MF + NF + kGroups - 1) / kGroups;
+#pragma unroll
+      for (int f = 0; f < NF; ++f) {
+#pragma unroll
+        for (int i = f * kPer; i < (f + 1) * kPer && i < MF + NF; ++i) read_one(slot * S::kSlot, 1, i);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int m = 0; m < MF; ++m) T::mfma(a[0][f], b[0][m], acc[m][f]);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      g_wait_lds();
+      if (ahead == D) wait_vmcnt<(D - 2) * L>();
+      else wait_vmcnt<0>();
+      g_barrier();
+      --ahead;
+      const bool more = lt < total, next = ahead > 0;
+      if (more && lks == 0) enter();
+      constexpr int kLoadsPer = (2 * L + NF - 1) / NF;  // in the first half of the step
+#pragma unroll
+      for (int f = 0; f < NF; ++f) {
+        if (next) {
+#pragma unroll
+          for (int i = f * kPer; i < (f + 1) * kPer && i < MF + NF; ++i) read_one(nslot * S::kSlot, 0, i);
+        }
+        if (more) {
+#pragma unroll
+          for (int j = f * kLoadsPer; j < (f + 1) * kLoadsPer && j < L; ++j) load(j);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int m = 0; m < MF; ++m) T::mfma(a[1][f], b[1][m], acc[m][f]);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      if (more) {
+        loaded();
+        ++ahead;
+      }
+      slot = nslot;
+    }
+
+    // Output: row 16 m + r of the wave, columns 16 f + 4 g ..+3 of block f.
+    const GtTile cur = find(t);
+    const uint32_t sc = S::kScalesAt + (seq % (D + 1)) * S::kScaleBuf;
+    ++seq;
+    const bool f16 = p.out_dtype == MEGAMOE_DTYPE_F16;
+    constexpr int kOutF = kL1 ? NF / 2 : NF;  // column blocks of a wave
+    const int le = g_here(lane), r = le & 15, g = le >> 4;
+    const int c0 = cur.nt * cols + wn * 16 * kOutF + 16 * (g & 1) + 8 * (g >> 1);
+#pragma unroll
+    for (int m = 0; m < MF; ++m) {
+      __builtin_amdgcn_sched_barrier(0);  // an output row at a time in registers
+      g_settle(acc[m]);
+      const int R = (wm * MF + m) * 16 + r;
+      float sa = 0.0f;
+      if constexpr (kI8) sa = lds_read<float>(sc + 4 * (kGtCols + R));
+      uint16_t* const out = static_cast<uint16_t*>(p.out) + (cur.row0 + R) * (int64_t)p.N;
+      u32x2 half[2];
+#pragma unroll
+      for (int f = 0; f < kOutF; ++f) {
+        f32x4 z, u;
+        const auto value = [&](int blk) __attribute__((always_inline)) {
+          if constexpr (kI8) {
+            const f32x4 sw = lds_read<f32x4>(sc + 4 * (wn * 16 * NF + 16 * blk + 4 * g));
+            f32x4 v;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) v[q] = (float)acc[m][blk][q] * sw[q] * sa;
+            return v;
+          } else {
+            return acc[m][blk];
+          }
+        };
+        z = value(f);
+        if constexpr (kL1) {
+          u = value(f + NF / 2);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) z[q] = g_silu(z[q]) * u[q];
+        }
+        half[f & 1] = u32x2{g_pack2(z[0], z[1], f16), g_pack2(z[2], z[3], f16)};
+        if (f & 1) {
+          const u32x4 v = g_gather8(half[0], half[1]);
+          const int c = c0 + 16 * (f - 1);
+          if (R < cur.left && c < p.N) __builtin_nontemporal_store(v, reinterpret_cast<u32x4*>(out + c));
+        }
+      }
+    }
   }
 }
 
-template <int kDtype>
-__global__ __launch_bounds__(256) void g_weights_kernel(GroupedWgradArgs p) {
-  const int e = blockIdx.z;
-  const int64_t first = p.padded_offsets[e];
-  const int k = blockIdx.x * 16 + threadIdx.x % 16, n = blockIdx.y * 16 + threadIdx.x / 16;
-  if (k >= p.K || n >= p.N) return;
-  float acc = 0.0f;
-  for (int r = 0; r < p.counts[e]; ++r) {
-    const int64_t row = first + r, src = p.row_token ? p.row_token[row] : row;
-    acc += g_load<kDtype>(p.dy, row * p.N + n) * g_load<kDtype>(p.x, src * p.K + k);
+template <int kOp, int kDtype>
+__global__ __launch_bounds__(kGtThreads, 1) void gt_kernel(GroupedArgs p) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t s_gt[];
+  int* const s_n = reinterpret_cast<int*>(s_gt + kGtLists);
+  int* const pref = s_n + 2;                                              // 256-row m-tiles before each expert [E + 1]
+  uint16_t* const list2 = reinterpret_cast<uint16_t*>(pref + p.E + 1);    // experts with a last tile of 128 rows
+  uint16_t* const list1 = list2 + p.E;                                    // of 64
+  const int E = p.E, lane = lane_id();
+  if (threadIdx.x < kWave) {
+    int carry = 0, n2 = 0, n1 = 0;
+    const uint64_t below = ((uint64_t)1 << lane) - 1;
+    for (int c = 0; c < E; c += kWave) {
+      const int cnt = c + lane < E ? p.counts ? p.counts[c + lane] : (int)p.M : 0, rest = cnt % kGtRows;
+      const int own = cnt / kGtRows + (rest > 128 ? 1 : 0);
+      int incl = own;
+#pragma unroll
+      for (int o = 1; o < kWave; o <<= 1) {
+        const int t = __shfl_up(incl, o, kWave);
+        if (lane >= o) incl += t;
+      }
+      if (c + lane < E) pref[c + lane] = carry + incl - own;
+      carry += __shfl(incl, kWave - 1, kWave);
+      const bool in2 = rest > 64 && rest <= 128, in1 = rest > 0 && rest <= 64 && (cnt > p.small_rows);
+      const uint64_t b2 = __ballot(in2), b1 = __ballot(in1);
+      if (in2) list2[n2 + __popcll(b2 & below)] = (uint16_t)(c + lane);
+      if (in1) list1[n1 + __popcll(b1 & below)] = (uint16_t)(c + lane);
+      n2 += __popcll(b2);
+      n1 += __popcll(b1);
+    }
+    if (lane == 0) {
+      pref[E] = carry;
+      s_n[0] = n2;
+      s_n[1] = n1;
+    }
   }
-  const int64_t at = ((int64_t)e * p.N + n) * p.K + k;
-  g_store(p.dw, at, p.dw_dtype, p.accumulate ? g_old(p.dw, at, p.dw_dtype) + acc : acc);
+  __syncthreads();
+  constexpr int cols = kOp == kGtGateUp ? kGtCols / 2 : kGtCols;
+  const int ntn = (p.N + cols - 1) / cols;
+  const int64_t total4 = (int64_t)__builtin_amdgcn_readfirstlane(pref[E]) * ntn;
+  const int64_t total2 = (int64_t)__builtin_amdgcn_readfirstlane(s_n[0]) * ntn;
+  const int64_t total1 = (int64_t)__builtin_amdgcn_readfirstlane(s_n[1]) * ntn;
+  const auto count = [&](int e) { return p.counts ? g_scalar(p.counts + e) : (int)p.M; };
+  const auto offset = [&](int e) { return (int64_t)(p.padded_offsets ? g_scalar(p.padded_offsets + e) : 0); };
+  // 256-row tile t: its expert by two steps of 64 comparisons (at most 1024 experts).
+  const auto find4 = [&](int64_t t) __attribute__((always_inline)) {
+    const int step = (E + kWave - 1) / kWave;
+    const int at = lane * step;
+    const int chunk = __popcll(__ballot(at < E && (int64_t)pref[at < E ? at : 0] * ntn <= t)) - 1;
+    const int at2 = chunk * step + lane;
+    const int e = __builtin_amdgcn_readfirstlane(
+        chunk * step - 1 + __popcll(__ballot(lane < step && at2 < E && (int64_t)pref[at2 < E ? at2 : 0] * ntn <= t)));
+    const int first = __builtin_amdgcn_readfirstlane(pref[e]);
+    const int mts = __builtin_amdgcn_readfirstlane(pref[e + 1]) - first;
+    const int64_t local = t - (int64_t)first * ntn;
+    const int band = (int)(local / ((int64_t)kGtBand * ntn)), in = (int)(local % ((int64_t)kGtBand * ntn));
+    const int width = min(kGtBand, mts - band * kGtBand);
+    const int mt = band * kGtBand + in % width;
+    const int cnt = count(e);
+    return GtTile{e, in / width, cnt - mt * kGtRows, offset(e) + (int64_t)mt * kGtRows};
+  };
+  const auto find_last = [&](const uint16_t* list, int64_t t) __attribute__((always_inline)) {
+    const int e = __builtin_amdgcn_readfirstlane((int)list[t / ntn]);
+    const int cnt = count(e), mt = cnt / kGtRows;
+    return GtTile{e, (int)(t % ntn), cnt - mt * kGtRows, offset(e) + (int64_t)mt * kGtRows};
+  };
+  // XCD b % 8 takes 32 tiles in a row of every 256: they share rows and weights in its L2.  The lists follow each
+  // other, so that a workgroup that has one tile more of one list has one less of the next.
+  const int64_t wg = (blockIdx.x % 8) * (kGtGrid / 8) + blockIdx.x / 8;
+  const auto first = [&](int64_t before) { return (wg - before % kGtGrid + kGtGrid) % kGtGrid; };
+  gt_phase<kOp, kDtype, 4>(p, wg, total4, find4);
+  gt_phase<kOp, kDtype, 2>(p, first(total4), total2, [&](int64_t t) { return find_last(list2, t); });
+  gt_phase<kOp, kDtype, 1>(p, first(total4 + total2), total1, [&](int64_t t) { return find_last(list1, t); });
 }
 
-template <bool kL1>
-static void launch_rows(const GroupedArgs& a, dim3 grid, hipStream_t s) {
-  if (a.dtype == kOperandI8) hipLaunchKernelGGL((g_rows_kernel<kOperandI8, kL1>), grid, dim3(256), 0, s, a);
-  else if (a.dtype == MEGAMOE_DTYPE_BF16) hipLaunchKernelGGL((g_rows_kernel<MEGAMOE_DTYPE_BF16, kL1>), grid, dim3(256), 0, s, a);
-  else hipLaunchKernelGGL((g_rows_kernel<MEGAMOE_DTYPE_F16, kL1>), grid, dim3(256), 0, s, a);
+// ============================================================================================
+// weights: 256 columns of x by 256 columns of dy a tile, both read across: the expert's rows are the reduced
+// dimension, 64 a stage.  The ring, the barrier and the steps are those above.
+// ============================================================================================
+constexpr int kGwSlot = 2 * kGtSide;
+constexpr int kGwTokens = 2 * kGwSlot;               // LDS: the waves' tokens of two stages' rows
+constexpr int kGwLds = kGwTokens + kGtWaves * 2 * 64 * 4;
+
+template <int kDtype, bool kGather>
+__global__ __launch_bounds__(kGtThreads, 1) void gt_weights_kernel(GroupedWgradArgs p) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t s_gt[];
+  typedef GType<kDtype> T;
+  constexpr int MF = 8, NF = 8, L = 16;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), lane = lane_id();
+  const int64_t KB = (int64_t)p.K * 2, NB = (int64_t)p.N * 2;
+  const int ntk = (p.K + kGtCols - 1) / kGtCols, ntn = (p.N + kGtRows - 1) / kGtRows;
+  const int per = ntk * ntn;
+  const int64_t total = (int64_t)p.E * per;
+  const uint8_t* const pad = reinterpret_cast<const uint8_t*>(g_zeros);
+
+  struct Tile {
+    int e, kt, nt, cnt;
+    int64_t row0;
+  };
+  const auto find = [&](int64_t t) __attribute__((always_inline)) {
+    Tile x;
+    x.e = (int)(t / per);
+    const int in = (int)(t % per), band = in / (kGtBand * ntk), ib = in % (kGtBand * ntk);
+    const int width = min(kGtBand, ntn - band * kGtBand);
+    x.nt = band * kGtBand + ib % width;
+    x.kt = ib / width;
+    x.cnt = g_scalar(p.counts + x.e);
+    x.row0 = g_scalar(p.padded_offsets + x.e);
+    return x;
+  };
+  const auto stages = [&](const Tile& x) { return x.cnt > 0 ? (x.cnt + 63) / 64 : 1; };
+
+  const int64_t t0 = (blockIdx.x % 8) * (kGtGrid / 8) + blockIdx.x / 8;
+  if (t0 >= total) return;
+  const int row = 16 * wave + (lane >> 5);  // of a stage's 64, of load instruction 0
+  Tile ld = find(t0), ldn = ld;
+  int64_t lt = t0;
+  int lks = 0, lnks = 0, lslot = 0, lq = 0;  // lq: parity of the stage's tokens
+  uint32_t x_off[8], y_off[8];
+  const uint8_t *x_at = nullptr, *y_at = nullptr;
+  const uint32_t tok_at = kGwTokens + wave * 2 * 64 * 4;
+  const auto fetch = [&](const Tile& x, int ks, int q) __attribute__((always_inline)) {  // tokens of the stage's rows
+    if (kGather && x.cnt > 0) {
+      const int R = 64 * ks + g_here(lane);
+      dma4(reinterpret_cast<const uint8_t*>(p.row_token + x.row0 + (R < x.cnt ? R : x.cnt - 1)), tok_at + 256 * (q & 1));
+    }
+  };
+  const auto enter = [&]() __attribute__((always_inline)) {
+    const int ln = g_here(lane);
+    lnks = stages(ld);
+    if (lt + kGtGrid < total) ldn = find(lt + kGtGrid);
+    x_at = static_cast<const uint8_t*>(p.x) + (int64_t)ld.kt * kGtCols * 2 + (kGather ? 0 : ld.row0 * KB);
+    y_at = static_cast<const uint8_t*>(p.dy) + (int64_t)ld.nt * kGtRows * 2 + ld.row0 * NB;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int n = 2 * j + (ln >> 5), piece = (ln & 31) ^ (((n & 3) | ((j >> 2) << 2)) << 1);
+      const int lk = p.K / 8 - 1 - ld.kt * 32, lnn = p.N / 8 - 1 - ld.nt * 32;
+      x_off[j] = 16 * (piece < lk ? piece : lk) + (kGather ? 0u : (uint32_t)(16 * wave + n) * (uint32_t)KB);
+      y_off[j] = 16 * (piece < lnn ? piece : lnn) + (uint32_t)(16 * wave + n) * (uint32_t)NB;
+    }
+  };
+  uint32_t tok[8];
+  const auto begin = [&]() __attribute__((always_inline)) {  // of the stage at (lt, lks)
+    if (lks == 0) enter();
+    if (kGather) {
+      const int ln = g_here(lane);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) tok[j] = lds_read<uint32_t>(tok_at + 256 * (lq & 1) + 4 * (16 * wave + 2 * j + (ln >> 5)));
+      if (lks + 1 < lnks) fetch(ld, lks + 1, lq + 1);
+      else if (lt + kGtGrid < total) fetch(ldn, 0, lq + 1);
+    }
+  };
+  const auto load = [&](int j) __attribute__((always_inline)) {
+    const int i = j & 7;
+    const uint32_t to = lslot * kGwSlot + (j < 8 ? 0 : kGtSide) + 1024 * (8 * wave + i);
+    const uint8_t* src = j < 8 ? x_at + x_off[i] : y_at + y_off[i];
+    if (kGather && j < 8) src += (uint64_t)tok[i] * (uint64_t)(uint32_t)KB;
+    dma16(row + 2 * i < ld.cnt - 64 * lks ? src : pad, to);
+  };
+  const auto loaded = [&]() __attribute__((always_inline)) {
+    if (!kGather) x_at += 64 * KB;
+    y_at += 64 * NB;
+    lslot ^= 1;
+    ++lq;
+    if (++lks == lnks) {
+      lks = 0;
+      lt += kGtGrid;
+      ld = ldn;
+    }
+  };
+
+  const int wm = wave / 2, wn = wave % 2, g = lane >> 4, jj = (lane & 15) >> 2;
+  const uint32_t lane_at = (8 * g + jj) * 512 + ((jj | ((g & 1) << 2)) * 32) + (lane & 3) * 8;
+  const uint32_t a_base = lane_at ^ (wn * 256), b_base = kGtSide + (lane_at ^ (wm * 256));
+  u32x4 a[2][NF], b[2][MF];
+  const auto read_one = [&](int slot, int st, int i) __attribute__((always_inline)) {
+    if (i < MF) b[st][i] = lds_read_across(slot * kGwSlot + (b_base ^ (i * 32)) + st * 32 * 512);
+    else a[st][i - MF] = lds_read_across(slot * kGwSlot + (a_base ^ ((i - MF) * 32)) + st * 32 * 512);
+  };
+
+  fetch(ld, 0, 0);
+  int ahead = 0;
+  for (; ahead < 2 && lt < total; ++ahead) {
+    wait_vmcnt<0>();  // the stage's tokens (the wave's own)
+    asm volatile("" ::: "memory");
+    begin();
+#pragma unroll
+    for (int j = 0; j < L; ++j) load(j);
+    loaded();
+  }
+  if (ahead == 2) wait_vmcnt<L>();
+  else wait_vmcnt<0>();
+  g_barrier();
+#pragma unroll
+  for (int i = 0; i < MF + NF; ++i) read_one(0, 0, i);
+
+  int slot = 0;
+  for (int64_t t = t0; t < total; t += kGtGrid) {
+    const Tile cur = find(t);
+    const int nks = stages(cur);
+    f32x4 acc[MF][NF];
+#pragma unroll
+    for (int m = 0; m < MF; ++m)
+#pragma unroll
+      for (int f = 0; f < NF; ++f)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) acc[m][f][q] = 0.0f;
+#pragma unroll
+    for (int m = 0; m < MF; ++m) g_settle(acc[m]);
+    for (int ks = 0; ks < nks; ++ks) {
+      constexpr int kPer = 3;
+#pragma unroll
+      for (int f = 0; f < NF; ++f) {
+#pragma unroll
+        for (int i = f * kPer; i < (f + 1) * kPer && i < MF + NF; ++i) read_one(slot, 1, i);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int m = 0; m < MF; ++m) T::mfma(a[0][f], b[0][m], acc[m][f]);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      g_wait_lds();
+      wait_vmcnt<0>();
+      g_barrier();
+      --ahead;
+      const bool more = lt < total, next = ahead > 0;
+      if (more) begin();
+#pragma unroll
+      for (int f = 0; f < NF; ++f) {
+        if (next) {
+#pragma unroll
+          for (int i = f * kPer; i < (f + 1) * kPer && i < MF + NF; ++i) read_one(slot ^ 1, 0, i);
+        }
+        if (more) {
+#pragma unroll
+          for (int j = f * 4; j < (f + 1) * 4 && j < L; ++j) load(j);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int m = 0; m < MF; ++m) T::mfma(a[1][f], b[1][m], acc[m][f]);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      if (more) {
+        loaded();
+        ++ahead;
+      }
+      slot ^= 1;
+    }
+    if (cur.cnt == 0 && p.accumulate) continue;
+    const bool f32 = p.dw_dtype == MEGAMOE_DTYPE_F32, f16 = p.dw_dtype == MEGAMOE_DTYPE_F16;
+    const int k0 = cur.kt * kGtCols + wn * 128;
+    const int le = g_here(lane), r = le & 15, g = le >> 4;
+#pragma unroll
+    for (int m = 0; m < MF; ++m) {
+      __builtin_amdgcn_sched_barrier(0);
+      g_settle(acc[m]);
+      const int n = cur.nt * kGtRows + wm * 128 + 16 * m + r;
+      const int64_t at = ((int64_t)cur.e * p.N + n) * p.K;
+      if (f32) {
+        float* const out = static_cast<float*>(p.dw) + at;
+#pragma unroll
+        for (int f = 0; f < NF; ++f) {
+          const int k = k0 + 16 * f + 4 * g;
+          if (n < p.N && k < p.K) {
+            f32x4 z = acc[m][f];
+            if (p.accumulate) z += *reinterpret_cast<const f32x4*>(out + k);
+            __builtin_nontemporal_store(z, reinterpret_cast<f32x4*>(out + k));
+          }
+        }
+      } else {
+        uint16_t* const out = static_cast<uint16_t*>(p.dw) + at;
+#pragma unroll
+        for (int f = 0; f < NF; f += 2) {
+          f32x4 z[2] = {acc[m][f], acc[m][f + 1]};
+          if (p.accumulate) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const int k = k0 + 16 * (f + h) + 4 * g;
+              if (n < p.N && k < p.K) {
+                const u32x2 old = *reinterpret_cast<const u32x2*>(out + k);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                  const uint32_t bits = (old[q / 2] >> (16 * (q & 1))) & 0xFFFFu;
+                  const uint16_t b16 = (uint16_t)bits;
+                  z[h][q] += f16 ? (float)__builtin_bit_cast(_Float16, b16) : bf16_bits_to_f32(bits);
+                }
+              }
+            }
+          }
+          const u32x4 v = g_gather8(u32x2{g_pack2(z[0][0], z[0][1], f16), g_pack2(z[0][2], z[0][3], f16)},
+                                    u32x2{g_pack2(z[1][0], z[1][1], f16), g_pack2(z[1][2], z[1][3], f16)});
+          const int k = k0 + 16 * f + 16 * (g & 1) + 8 * (g >> 1);
+          if (n < p.N && k < p.K) __builtin_nontemporal_store(v, reinterpret_cast<u32x4*>(out + k));
+        }
+      }
+    }
+  }
 }
 
-hipError_t launch_grouped(const GroupedArgs& a, bool l1, int64_t max_rows, hipStream_t stream) {
-  (void)max_rows;
-  const dim3 grid((a.N + 15) / 16, a.E, 64);
-  if (l1) launch_rows<true>(a, grid, stream);
-  else launch_rows<false>(a, grid, stream);
+// The dynamic LDS limit of a kernel, raised once a device.
+template <typename F>
+static hipError_t gt_allow_lds(F* kernel, std::atomic<bool> (&done)[kGtDevices]) {
+  int dev = 0;
+  hipError_t err = hipGetDevice(&dev);
+  if (err != hipSuccess) return err;
+  if (dev < kGtDevices && done[dev].load(std::memory_order_acquire)) return hipSuccess;
+  err = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, kGtLds);
+  if (err == hipSuccess && dev < kGtDevices) done[dev].store(true, std::memory_order_release);
+  return err;
+}
+
+template <int kOp, int kDtype>
+static hipError_t launch_gt(const GroupedArgs& a, hipStream_t stream) {
+  static std::atomic<bool> done[kGtDevices];
+  const hipError_t err = gt_allow_lds(gt_kernel<kOp, kDtype>, done);
+  if (err != hipSuccess) return err;
+  hipLaunchKernelGGL((gt_kernel<kOp, kDtype>), dim3(kGtGrid), dim3(kGtThreads), kGtLds, stream, a);
   return hipGetLastError();
+}
+
+template <int kDtype, bool kGather>
+static hipError_t launch_gt_weights(const GroupedWgradArgs& a, hipStream_t stream) {
+  static std::atomic<bool> done[kGtDevices];
+  const hipError_t err = gt_allow_lds(gt_weights_kernel<kDtype, kGather>, done);
+  if (err != hipSuccess) return err;
+  hipLaunchKernelGGL((gt_weights_kernel<kDtype, kGather>), dim3(kGtGrid), dim3(kGtThreads), kGwLds, stream, a);
+  return hipGetLastError();
+}
+
+hipError_t launch_grouped(const GroupedArgs& a0, bool l1, int64_t max_rows, hipStream_t stream) {
+  GroupedArgs a = a0;
+  (void)max_rows;
+  a.small_rows = 0;
+  if (a.across)
+    return a.dtype == MEGAMOE_DTYPE_BF16 ? launch_gt<kGtAcross, MEGAMOE_DTYPE_BF16>(a, stream)
+                                         : launch_gt<kGtAcross, MEGAMOE_DTYPE_F16>(a, stream);
+  if (a.dtype == kOperandI8)
+    return l1 ? launch_gt<kGtGateUp, kOperandI8>(a, stream) : launch_gt<kGtPlain, kOperandI8>(a, stream);
+  return a.dtype == MEGAMOE_DTYPE_BF16 ? launch_gt<kGtPlain, MEGAMOE_DTYPE_BF16>(a, stream)
+                                       : launch_gt<kGtPlain, MEGAMOE_DTYPE_F16>(a, stream);
 }
 
 hipError_t launch_grouped_wgrad(const GroupedWgradArgs& a, hipStream_t stream) {
-  const dim3 grid((a.K + 15) / 16, (a.N + 15) / 16, a.E);
-  if (a.dtype == MEGAMOE_DTYPE_BF16) hipLaunchKernelGGL((g_weights_kernel<MEGAMOE_DTYPE_BF16>), grid, dim3(256), 0, stream, a);
-  else hipLaunchKernelGGL((g_weights_kernel<MEGAMOE_DTYPE_F16>), grid, dim3(256), 0, stream, a);
-  return hipGetLastError();
+  if (a.row_token != nullptr)
+    return a.dtype == MEGAMOE_DTYPE_BF16 ? launch_gt_weights<MEGAMOE_DTYPE_BF16, true>(a, stream)
+                                         : launch_gt_weights<MEGAMOE_DTYPE_F16, true>(a, stream);
+  return a.dtype == MEGAMOE_DTYPE_BF16 ? launch_gt_weights<MEGAMOE_DTYPE_BF16, false>(a, stream)
+                                       : launch_gt_weights<MEGAMOE_DTYPE_F16, false>(a, stream);
 }
 
 }  // namespace megamoe
