@@ -9,6 +9,7 @@
 // operand the other (token rows, or dy): a lane then ends with four consecutive columns of one output row.  Lane
 // (r, g) of a 16-row fragment holds 16 bytes of its row, the same 16 bytes of K on both sides.
 #include <atomic>
+#include <utility>
 
 #include "device_common.h"
 #include "internal.h"
@@ -25,7 +26,7 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 constexpr int kGtDevices = 64;
 constexpr int kGtPlain = 0, kGtGateUp = 1, kGtAcross = 2;  // operations of gt_kernel
 constexpr int kGtGrid = 256;                        // one workgroup a CU
-constexpr int kGtWaves = 4, kGtThreads = kGtWaves * kWave;
+constexpr int kGtWaves = 8, kGtThreads = kGtWaves * kWave;
 constexpr int kGtCols = 256, kGtRows = 256;         // A-side and B-side rows of the largest tile
 constexpr int kGtStage = 128;                       // bytes of K a stage (64 or 128 elements)
 constexpr int kGtSide = kGtCols * kGtStage;         // LDS bytes of a stage's A side
@@ -70,7 +71,7 @@ __device__ __forceinline__ int g_here(int v) {
 // Operand types: the accumulator and the 16x16 matrix instruction over 64 bytes of K (16x16x32 or 16x16x64).  Inline
 // assembly keeps the accumulators in accumulation registers, all 256 of them in the largest tile: left to itself the
 // compiler moves them to and fro (408 moves beside 64 products).  What it does not know of these instructions is
-// kept by hand: an accumulator is met again after at least 16 others, and g_settle stands between the products
+// kept by hand: an accumulator is met again after at least 7 others, and g_settle stands between the products
 // and any other write or read of it.
 template <int kDtype>
 struct GType {
@@ -93,8 +94,10 @@ struct GType<kOperandI8> {
 // instruction, and is read by the next one 2 after a write.
 template <typename A, int n>
 __device__ __forceinline__ void g_settle(A (&c)[n]) {
-  static_assert(n == 4 || n == 8, "fragments of a wave");
-  if constexpr (n == 8)
+  static_assert(n == 2 || n == 4 || n == 8, "fragments of a wave");
+  if constexpr (n == 2)
+    asm volatile("s_nop 15\n\ts_nop 7" : "+a"(c[0]), "+a"(c[1]));
+  else if constexpr (n == 8)
     asm volatile("s_nop 15\n\ts_nop 7" : "+a"(c[0]), "+a"(c[1]), "+a"(c[2]), "+a"(c[3]), "+a"(c[4]), "+a"(c[5]), "+a"(c[6]), "+a"(c[7]));
   else
     asm volatile("s_nop 15\n\ts_nop 7" : "+a"(c[0]), "+a"(c[1]), "+a"(c[2]), "+a"(c[3]));
@@ -102,6 +105,16 @@ __device__ __forceinline__ void g_settle(A (&c)[n]) {
 
 __device__ __forceinline__ u32x4 lds_read16(uint32_t at) {
   return *reinterpret_cast<const __attribute__((address_space(3))) u32x4*>(at);
+}
+__device__ __forceinline__ void lds_write16(uint32_t at, u32x4 v) {
+  *reinterpret_cast<__attribute__((address_space(3))) u32x4*>(at) = v;
+}
+__device__ __forceinline__ u32x4 g_read16(uint64_t at) {
+  return *reinterpret_cast<const __attribute__((address_space(1))) u32x4*>(at);
+}
+__device__ __forceinline__ u32x4 g_read16(const uint8_t* base, uint32_t off) {  // wave-uniform base
+  return *reinterpret_cast<const __attribute__((address_space(1))) u32x4*>(
+      reinterpret_cast<const __attribute__((address_space(1))) uint8_t*>(scalar_addr(base)) + off);
 }
 template <typename T>
 __device__ __forceinline__ T lds_read(uint32_t at) {
@@ -131,6 +144,42 @@ __device__ __forceinline__ u32x4 g_gather8(u32x2 lo, u32x2 hi) {
   return u32x4{a[0], b[0], a[1], b[1]};
 }
 
+// A step: the products of one 64-byte piece of K, with the next step's operands read from LDS (read(i)) and a
+// stage's loads requested (load(j)) between them, each behind a product of its own: a wave has its SIMD to itself and
+// issues in order, so what stands between two products is free only within the first one's 16 cycles.  Reads and
+// loads are out after three quarters of the products.
+template <int V>
+struct GTag {
+  static constexpr int value = V;
+};
+template <typename F, int... V>
+__device__ __forceinline__ void gt_each(const F& f, std::integer_sequence<int, V...>) {
+  (f(GTag<V>{}), ...);
+}
+template <typename T, int MF, int NF, int kReads, int kLoads, typename Read, typename Load>
+__device__ __forceinline__ void gt_step(typename T::acc (&acc)[MF][NF], const u32x4 (&a)[NF], const u32x4 (&b)[MF],
+                                        const Read& read, const Load& load) {
+  constexpr int span = MF * NF * 3 / 4;
+  gt_each(
+      [&](auto tag) __attribute__((always_inline)) {
+        constexpr int at = decltype(tag)::value;
+        T::mfma(a[at / MF], b[at % MF], acc[at % MF][at / MF]);
+        __builtin_amdgcn_sched_barrier(0);
+        // item i of n stands behind product i * span / n, loads one later
+        constexpr int r0 = (at * kReads + span - 1) / span, r1 = ((at + 1) * kReads + span - 1) / span;
+#pragma unroll
+        for (int i = r0; i < (r1 < kReads ? r1 : kReads); ++i) read(i);
+        constexpr int l0 = ((at - 1) * kLoads + span - 1) / span, l1 = (at * kLoads + span - 1) / span;
+#pragma unroll
+        for (int j = at > 0 ? l0 : 0; j < (at == 0 ? 0 : l1 < kLoads ? l1 : kLoads); ++j) load(j);
+        __builtin_amdgcn_sched_barrier(0);
+      },
+      std::make_integer_sequence<int, MF * NF>{});
+}
+struct GtNothing {
+  __device__ __forceinline__ void operator()(int) const {}
+};
+
 // ============================================================================================
 // rows, gate+up and across: 256 weight rows x BM token rows a tile, BM = 64 WB = 256, or 128 or 64 for an
 // expert's last rows when they fit; one persistent workgroup of 4 waves a CU takes all tiles of 256 rows, then
@@ -144,15 +193,16 @@ __device__ __forceinline__ u32x4 g_gather8(u32x2 lo, u32x2 hi) {
 // ============================================================================================
 template <int WB>
 struct GtShape {
-  static constexpr int WM = WB == 1 ? 1 : 2, WN = kGtWaves / WM;  // waves along token rows, weight rows
+  static constexpr int WM = WB == 4 ? 4 : 2, WN = kGtWaves / WM;  // waves along token rows, weight rows
   static constexpr int MF = 4 * WB / WM, NF = 16 / WN;            // a wave's fragments of either side
   static constexpr int D = WB == 4 ? 2 : 3;                       // slots
+  static constexpr int kBufs = D + 1;                             // tiles whose scales are in LDS at a time
   static constexpr int kSlot = kGtSide + 64 * WB * kGtStage;
-  static constexpr int kLoads = 8 + 2 * WB;                       // load instructions a wave and stage
-  // LDS behind the slots: the tokens of two tiles' rows, the scales of D + 1 tiles
+  static constexpr int kLoads = 4 + WB;                           // load instructions a wave and stage
+  // LDS behind the slots: the tokens of two tiles' rows, the scales of kBufs tiles
   static constexpr int kRowsAt = D * kSlot, kScalesAt = kRowsAt + 2 * 64 * WB * 4;
   static constexpr int kScaleBuf = 4 * (kGtCols + 64 * WB);
-  static_assert(kScalesAt + (D + 1) * kScaleBuf <= kGtLists, "the LDS layout fits");
+  static_assert(kScalesAt + kBufs * kScaleBuf <= kGtLists, "the LDS layout fits");
 };
 
 struct GtTile {
@@ -172,15 +222,15 @@ __device__ __forceinline__ void gt_phase(const GroupedArgs& p, int64_t t0, int64
   const int64_t RB = (int64_t)p.K * T::kBytes;                    // bytes of a row of K
   const int64_t NB = (int64_t)p.N * T::kBytes;                    // across: bytes of a weight row
   const int nks = (int)((RB + kGtStage - 1) / kGtStage);
-  const uint8_t* const pad = reinterpret_cast<const uint8_t*>(g_zeros);
   const int piece = (lane & 7) ^ (lane >> 4);  // of 8 rows of an even load instruction (odd: ^ 4)
 
   // ---- loads -------------------------------------------------------------------------------------
   GtTile ld;
   int64_t lt = t0;
-  int lks = 0, lslot = 0, lseq = 0;
-  const uint8_t *w_at = nullptr, *w_up = nullptr, *a_at = nullptr;  // of the stage to request
-  uint32_t w_off[8], a_off[2 * WB];
+  int lks = 0, lseq = 0;
+  const uint8_t* w_at = nullptr;                   // of the stage to request
+  uint32_t w_off[kAcross ? 2 : 4];                 // across: of even and odd load instructions
+  uint64_t a_at[WB];
   const auto fetch_rows = [&](int64_t t, int buf) __attribute__((always_inline)) {  // tokens of tile t's rows
     if (!kAcross && p.row_token != nullptr && wave < WB && t < total) {
       const GtTile x = find(t);
@@ -200,66 +250,93 @@ __device__ __forceinline__ void gt_phase(const GroupedArgs& p, int64_t t0, int64
     const int c = ld.nt * cols + (kL1 ? R / per * (per / 2) + R % (per / 2) : R);
     return c < p.N ? c : p.N - 1;
   };
+  const auto is_up = [&](int R) { return R % (kGtCols / WN) >= kGtCols / WN / 2; };
+  const auto a_piece = [&](int i) { return piece ^ (((WB * wave + i) & 1) << 2); };
+  const auto uniform = [](const uint8_t* at) __attribute__((always_inline)) {
+    return reinterpret_cast<const uint8_t*>(scalar_addr(at));
+  };
   const auto enter = [&]() __attribute__((always_inline)) {  // tile lt
     const int ln = g_here(lane);
     ld = find(lt);
-    a_at = static_cast<const uint8_t*>(p.a);
 #pragma unroll
-    for (int j = 0; j < 2 * WB; ++j) {
-      a_off[j] = a_row(16 * WB * wave + 8 * j + ln / 8) * (uint32_t)(RB / 16) + (piece ^ ((j & 1) << 2));
-    }
+    for (int i = 0; i < WB; ++i)
+      a_at[i] = reinterpret_cast<uint64_t>(p.a) + (uint64_t)a_row(8 * (WB * wave + i) + ln / 8) * (uint64_t)(uint32_t)RB +
+                16 * a_piece(i);
     if constexpr (kAcross) {
-      w_at = static_cast<const uint8_t*>(p.w) + (int64_t)ld.e * p.K * NB + (int64_t)ld.nt * cols * T::kBytes;
+      w_at = uniform(static_cast<const uint8_t*>(p.w) + ((int64_t)ld.e * p.K + 8 * wave) * NB + (int64_t)ld.nt * cols * T::kBytes);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int n = 2 * j + (ln >> 5), c = (ln & 31) ^ (((n & 3) | ((j >> 2) << 2)) << 1);
+      for (int q = 0; q < 2; ++q) {
+        const int c = (ln & 31) ^ (((2 * q + (ln >> 5)) | ((wave & 1) << 2)) << 1);
         const int last = p.N / 8 - 1 - ld.nt * (cols / 8);
-        w_off[j] = (uint32_t)(16 * wave + n) * (uint32_t)NB + 16 * (c < last ? c : last);
+        w_off[q] = (uint32_t)(ln >> 5) * (uint32_t)NB + 16 * (c < last ? c : last);
       }
-    } else {
-      const int64_t c0 = (int64_t)ld.nt * cols;
-      w_at = static_cast<const uint8_t*>(p.w) + ((int64_t)ld.e * (kL1 ? 2 : 1) * p.N + c0) * RB;
-      w_up = w_at + (int64_t)p.N * RB;
+    } else {  // (gate+up: a wave's rows are all gate's or all up's)
+      const int64_t c0 = (int64_t)ld.nt * cols + (kL1 && is_up(32 * wave) ? p.N : 0);
+      w_at = uniform(static_cast<const uint8_t*>(p.w) + ((int64_t)ld.e * (kL1 ? 2 : 1) * p.N + c0) * RB);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        w_off[j] = (uint32_t)(w_col(64 * wave + 8 * j + ln / 8) - (int)c0) * (uint32_t)RB + 16 * (piece ^ ((j & 1) << 2));
-      }
+      for (int j = 0; j < 4; ++j)
+        w_off[j] = (uint32_t)(w_col(32 * wave + 8 * j + ln / 8) - ld.nt * cols) * (uint32_t)RB + 16 * (piece ^ ((j & 1) << 2));
     }
-    if constexpr (kI8) {  // the tile's scales: weight rows by all waves, token rows by WB of them
-      const uint32_t to = S::kScalesAt + (lseq % (D + 1)) * S::kScaleBuf;
-      const int R = 64 * wave + ln;
-      const bool up = kL1 && R % (kGtCols / WN) >= kGtCols / WN / 2;
-      dma4(reinterpret_cast<const uint8_t*>(p.w_scales + (int64_t)ld.e * (kL1 ? 2 : 1) * p.N + (up ? p.N : 0) + w_col(R)),
-           to + 256 * wave);
-      if (wave < WB) dma4(reinterpret_cast<const uint8_t*>(p.a_scales + a_row(R)), to + 4 * kGtCols + 256 * wave);
+    if constexpr (kI8) {  // the tile's scales: weight rows by four waves, token rows by WB others
+      const uint32_t to = S::kScalesAt + (lseq % S::kBufs) * S::kScaleBuf;
+      const int R = 64 * (wave & 3) + ln;
+      if (wave < 4)
+        dma4(reinterpret_cast<const uint8_t*>(p.w_scales + (int64_t)ld.e * (kL1 ? 2 : 1) * p.N + (kL1 && is_up(R) ? p.N : 0) + w_col(R)),
+             to + 256 * wave);
+      else if (wave - 4 < WB)
+        dma4(reinterpret_cast<const uint8_t*>(p.a_scales + a_row(R)), to + 4 * kGtCols + 256 * (wave - 4));
     }
     fetch_rows(lt + kGtGrid, (lseq + 1) & 1);
     ++lseq;
   };
-  // Load j of the stage at (lt, lks) into slot lslot: weights, then token rows.
-  const auto load = [&](int j) __attribute__((always_inline)) {
-    const uint32_t slot = lslot * S::kSlot;
-    const int left = (int)((RB - (int64_t)lks * kGtStage) / 16);  // pieces of K from this stage on
-    if (j < 8) {
-      const bool up = kL1 && (WN == 2 ? wave & 1 : j >= 4);
-      const uint8_t* src = (up ? w_up : w_at) + w_off[j];
-      const int k = kAcross ? 2 * wave + (2 * j + (lane >> 5)) / 8 : piece ^ ((j & 1) << 2);
-      src = k < left ? src : pad;
+  bool done = false;  // with nothing left the last stage is loaded again, and not used
+  const auto last_stage = [&]() { return lks + 1 == nks && lt + kGtGrid >= total; };
+  // Load j of the stage at (lt, lks): weights, then token rows.
+  const auto load = [&](int j, uint64_t a_step, int slot) __attribute__((always_inline)) {
+    if (j < 4) {
+      const uint8_t* const base = kAcross ? w_at + 2 * j * NB : w_at;
+      const uint32_t off = w_off[kAcross ? j & 1 : j], to = slot * S::kSlot + 1024 * (4 * wave + j);
       // the lower tiles are mostly an expert's only ones: its weights are read once, past the caches
-      if constexpr (WB < 4) dma16nt(src, slot + 1024 * (8 * wave + j));
-      else dma16(src, slot + 1024 * (8 * wave + j));
+      if constexpr (WB < 4) dma16snt(base, off, to);
+      else dma16s(base, off, to);
     } else {
-      const int i = j - 8;
-      const uint8_t* src = a_at + (uint64_t)a_off[i] * 16;
-      src = (piece ^ ((i & 1) << 2)) < left ? src : pad;
-      dma16(src, slot + kGtSide + 1024 * (2 * WB * wave + i));
+      dma16(reinterpret_cast<const uint8_t*>(a_at[j - 4]), slot * S::kSlot + kGtSide + 1024 * (WB * wave + j - 4));
+      a_at[j - 4] += a_step;
     }
   };
+  // A row's last stage, when K ends inside it: lanes whose piece lies behind the end load the stage's first piece
+  // instead (across: waves whose weight rows do, the first rows), and clear() writes zeros over what they brought,
+  // before the barrier that shows it.
+  const bool ragged = (RB & (kGtStage - 1)) != 0;
+  const int left = (int)((RB & (kGtStage - 1)) / 16);  // pieces (across: eights of weight rows) in the last stage
+  const auto trim = [&]() __attribute__((always_inline)) {
+    if constexpr (kAcross) {
+      if (wave >= left) w_at -= 8 * wave * NB;
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if ((piece ^ ((j & 1) << 2)) >= left) w_off[j] -= 16 * (piece ^ ((j & 1) << 2));
+    }
+#pragma unroll
+    for (int i = 0; i < WB; ++i)
+      if (a_piece(i) >= left) a_at[i] -= 16 * a_piece(i);
+  };
+  const auto clear = [&](uint32_t slot) __attribute__((always_inline)) {
+    const uint32_t to = slot + 16 * g_here(lane);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if ((kAcross ? wave : piece ^ ((j & 1) << 2)) >= left) lds_write16(to + 1024 * (4 * wave + j), u32x4{0u, 0u, 0u, 0u});
+#pragma unroll
+    for (int i = 0; i < WB; ++i)
+      if (a_piece(i) >= left) lds_write16(to + kGtSide + 1024 * (WB * wave + i), u32x4{0u, 0u, 0u, 0u});
+  };
+  const auto tail_stage = [&]() { return ragged && lks + 1 == nks; };
   const auto loaded = [&]() __attribute__((always_inline)) {
-    a_at += kGtStage;
+    if (last_stage()) {
+      done = true;
+      return;
+    }
     w_at += kAcross ? 64 * NB : kGtStage;
-    if constexpr (kL1) w_up += kGtStage;
-    lslot = lslot + 1 == D ? 0 : lslot + 1;
     if (++lks == nks) {
       lks = 0;
       lt += kGtGrid;
@@ -274,42 +351,48 @@ __device__ __forceinline__ void gt_phase(const GroupedArgs& p, int64_t t0, int64
   const uint32_t a_base = kAcross ? (8 * g + jj) * 512 + (((NF * wn) ^ (jj | ((g & 1) << 2))) * 32) + (lane & 3) * 8
                                   : wn * (16 * NF) * kGtStage + along;
   u32x4 a[2][NF], b[2][MF];
-  const auto read_a = [&](uint32_t slot, int st, int f) __attribute__((always_inline)) {
-    if constexpr (kAcross) a[st][f] = lds_read_across(slot + (a_base ^ (f * 32)) + st * 32 * 512);
-    else a[st][f] = lds_read16(slot + (a_base ^ (st * 64)) + f * 16 * kGtStage);
+  // Operands of step st of a slot: bases in registers, so that a read is one instruction.
+  uint32_t ra, rb;
+  const auto aim = [&](int slot, int st) __attribute__((always_inline)) {
+    rb = (b_base ^ (st * 64)) + slot * S::kSlot;
+    ra = (kAcross ? a_base : a_base ^ (st * 64)) + slot * S::kSlot;
+    asm volatile("" : "+v"(ra), "+v"(rb));
   };
-  const auto read_b = [&](uint32_t slot, int st, int m) __attribute__((always_inline)) {
-    b[st][m] = lds_read16(slot + (b_base ^ (st * 64)) + m * 16 * kGtStage);
-  };
-  const auto read_one = [&](uint32_t slot, int st, int i) __attribute__((always_inline)) {
-    if (i < MF) read_b(slot, st, i);
-    else read_a(slot, st, i - MF);
+  const auto read_one = [&](int st, int i) __attribute__((always_inline)) {
+    if (i < MF) b[st][i] = lds_read16(rb + i * 16 * kGtStage);
+    else if constexpr (kAcross) a[st][i - MF] = lds_read_across((ra ^ ((i - MF) * 32)) + st * 32 * 512);
+    else a[st][i - MF] = lds_read16(ra + (i - MF) * 16 * kGtStage);
   };
 
-  g_barrier();  // the phase before has been read from LDS
+  g_wait_lds();
+  g_barrier();  // the phase before is done with LDS
   fetch_rows(lt, 0);
   wait_vmcnt<0>();
   g_barrier();
   int issued = 0;
-  for (; issued < D && lt < total; ++issued) {
-    if (lks == 0) {
+  const auto first_loads = [&]() __attribute__((always_inline)) {
+    if (!done && lks == 0) {
       if (issued > 0) {  // its rows were asked for with the tile before
         wait_vmcnt<0>();
         g_barrier();
       }
       enter();
     }
+    if (!done && tail_stage()) trim();
+    const uint64_t a_step = last_stage() ? 0 : kGtStage;
 #pragma unroll
-    for (int j = 0; j < L; ++j) load(j);
+    for (int j = 0; j < L; ++j) load(j, a_step, issued);
     loaded();
-  }
-  if (issued == D) wait_vmcnt<(D - 1) * L>();
-  else wait_vmcnt<0>();
+  };
+  for (; issued < D; ++issued) first_loads();
+  wait_vmcnt<(D - 1) * L>();
+  if (ragged && nks == 1) clear(0);
+  g_wait_lds();
   g_barrier();
+  aim(0, 0);
 #pragma unroll
-  for (int i = 0; i < MF + NF; ++i) read_one(0, 0, i);
+  for (int i = 0; i < MF + NF; ++i) read_one(0, i);
 
-  int ahead = issued;  // stages requested and not yet multiplied
   int slot = 0, seq = 0;
   for (int64_t t = t0; t < total; t += kGtGrid) {
     typename T::acc acc[MF][NF];
@@ -323,49 +406,25 @@ __device__ __forceinline__ void gt_phase(const GroupedArgs& p, int64_t t0, int64
     for (int m = 0; m < MF; ++m) g_settle(acc[m]);
     for (int ks = 0; ks < nks; ++ks) {
       const int nslot = slot + 1 == D ? 0 : slot + 1;
-      constexpr int kGroups = NF > 4 ? NF - 2 : NF - 1, kPer = (MF + NF + kGroups - 1) / kGroups;
-#pragma unroll
-      for (int f = 0; f < NF; ++f) {
-#pragma unroll
-        for (int i = f * kPer; i < (f + 1) * kPer && i < MF + NF; ++i) read_one(slot * S::kSlot, 1, i);
-        __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-        for (int m = 0; m < MF; ++m) T::mfma(a[0][f], b[0][m], acc[m][f]);
-        __builtin_amdgcn_sched_barrier(0);
-      }
+      aim(slot, 1);
+      gt_step<T, MF, NF, MF + NF, 0>(acc, a[0], b[0], [&](int i) __attribute__((always_inline)) { read_one(1, i); }, GtNothing{});
+      wait_vmcnt<(D - 2) * L>();  // the next stage's
+      if (ragged && (ks + 2 == nks || nks == 1)) clear(nslot * S::kSlot);
       g_wait_lds();
-      if (ahead == D) wait_vmcnt<(D - 2) * L>();
-      else wait_vmcnt<0>();
       g_barrier();
-      --ahead;
-      const bool more = lt < total, next = ahead > 0;
-      if (more && lks == 0) enter();
-      constexpr int kLoadsPer = (2 * L + NF - 1) / NF;  // in the first half of the step
-#pragma unroll
-      for (int f = 0; f < NF; ++f) {
-        if (next) {
-#pragma unroll
-          for (int i = f * kPer; i < (f + 1) * kPer && i < MF + NF; ++i) read_one(nslot * S::kSlot, 0, i);
-        }
-        if (more) {
-#pragma unroll
-          for (int j = f * kLoadsPer; j < (f + 1) * kLoadsPer && j < L; ++j) load(j);
-        }
-        __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-        for (int m = 0; m < MF; ++m) T::mfma(a[1][f], b[1][m], acc[m][f]);
-        __builtin_amdgcn_sched_barrier(0);
-      }
-      if (more) {
-        loaded();
-        ++ahead;
-      }
+      if (!done && lks == 0) enter();
+      if (!done && tail_stage()) trim();
+      const uint64_t a_step = last_stage() ? 0 : kGtStage;
+      aim(nslot, 0);
+      gt_step<T, MF, NF, MF + NF, L>(acc, a[1], b[1], [&](int i) __attribute__((always_inline)) { read_one(0, i); },
+                                     [&](int j) __attribute__((always_inline)) { load(j, a_step, slot); });
+      if (!done) loaded();
       slot = nslot;
     }
 
     // Output: row 16 m + r of the wave, columns 16 f + 4 g ..+3 of block f.
     const GtTile cur = find(t);
-    const uint32_t sc = S::kScalesAt + (seq % (D + 1)) * S::kScaleBuf;
+    const uint32_t sc = S::kScalesAt + (seq % S::kBufs) * S::kScaleBuf;
     ++seq;
     const bool f16 = p.out_dtype == MEGAMOE_DTYPE_F16;
     constexpr int kOutF = kL1 ? NF / 2 : NF;  // column blocks of a wave
@@ -409,6 +468,7 @@ __device__ __forceinline__ void gt_phase(const GroupedArgs& p, int64_t t0, int64
       }
     }
   }
+  wait_vmcnt<0>();  // no load is on its way into LDS when the phase, or the workgroup, ends
 }
 
 template <int kOp, int kDtype>
@@ -497,7 +557,7 @@ template <int kDtype, bool kGather>
 __global__ __launch_bounds__(kGtThreads, 1) void gt_weights_kernel(GroupedWgradArgs p) {
   extern __shared__ __attribute__((aligned(16))) uint8_t s_gt[];
   typedef GType<kDtype> T;
-  constexpr int MF = 8, NF = 8, L = 16;
+  constexpr int MF = 4, NF = 8, L = 8;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), lane = lane_id();
   const int64_t KB = (int64_t)p.K * 2, NB = (int64_t)p.N * 2;
   const int ntk = (p.K + kGtCols - 1) / kGtCols, ntn = (p.N + kGtRows - 1) / kGtRows;
@@ -524,11 +584,11 @@ __global__ __launch_bounds__(kGtThreads, 1) void gt_weights_kernel(GroupedWgradA
 
   const int64_t t0 = (blockIdx.x % 8) * (kGtGrid / 8) + blockIdx.x / 8;
   if (t0 >= total) return;
-  const int row = 16 * wave + (lane >> 5);  // of a stage's 64, of load instruction 0
+  const auto row = [&]() __attribute__((always_inline)) { return 8 * wave + (g_here(lane) >> 5); };  // of a stage's 64, of load 0
   Tile ld = find(t0), ldn = ld;
   int64_t lt = t0;
-  int lks = 0, lnks = 0, lslot = 0, lq = 0;  // lq: parity of the stage's tokens
-  uint32_t x_off[8], y_off[8];
+  int lks = 0, lnks = 0, lq = 0;  // lq: parity of the stage's tokens
+  uint32_t x_off[2], y_off[2];  // of even and odd load instructions
   const uint8_t *x_at = nullptr, *y_at = nullptr;
   const uint32_t tok_at = kGwTokens + wave * 2 * 64 * 4;
   const auto fetch = [&](const Tile& x, int ks, int q) __attribute__((always_inline)) {  // tokens of the stage's rows
@@ -541,38 +601,51 @@ __global__ __launch_bounds__(kGtThreads, 1) void gt_weights_kernel(GroupedWgradA
     const int ln = g_here(lane);
     lnks = stages(ld);
     if (lt + kGtGrid < total) ldn = find(lt + kGtGrid);
-    x_at = static_cast<const uint8_t*>(p.x) + (int64_t)ld.kt * kGtCols * 2 + (kGather ? 0 : ld.row0 * KB);
-    y_at = static_cast<const uint8_t*>(p.dy) + (int64_t)ld.nt * kGtRows * 2 + ld.row0 * NB;
+    x_at = static_cast<const uint8_t*>(p.x) + (int64_t)ld.kt * kGtCols * 2 + (kGather ? 0 : (ld.row0 + 8 * wave) * KB);
+    y_at = static_cast<const uint8_t*>(p.dy) + (int64_t)ld.nt * kGtRows * 2 + (ld.row0 + 8 * wave) * NB;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int n = 2 * j + (ln >> 5), piece = (ln & 31) ^ (((n & 3) | ((j >> 2) << 2)) << 1);
+    for (int q = 0; q < 2; ++q) {
+      const int c = (ln & 31) ^ (((2 * q + (ln >> 5)) | ((wave & 1) << 2)) << 1);
       const int lk = p.K / 8 - 1 - ld.kt * 32, lnn = p.N / 8 - 1 - ld.nt * 32;
-      x_off[j] = 16 * (piece < lk ? piece : lk) + (kGather ? 0u : (uint32_t)(16 * wave + n) * (uint32_t)KB);
-      y_off[j] = 16 * (piece < lnn ? piece : lnn) + (uint32_t)(16 * wave + n) * (uint32_t)NB;
+      x_off[q] = 16 * (c < lk ? c : lk) + (kGather ? 0u : (uint32_t)(ln >> 5) * (uint32_t)KB);
+      y_off[q] = 16 * (c < lnn ? c : lnn) + (uint32_t)(ln >> 5) * (uint32_t)NB;
     }
   };
-  uint32_t tok[8];
+  uint32_t tok[4];
+  bool done = false;  // with nothing left the last stage is loaded again, into registers that no one reads
   const auto begin = [&]() __attribute__((always_inline)) {  // of the stage at (lt, lks)
     if (lks == 0) enter();
     if (kGather) {
-      const int ln = g_here(lane);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) tok[j] = lds_read<uint32_t>(tok_at + 256 * (lq & 1) + 4 * (16 * wave + 2 * j + (ln >> 5)));
       if (lks + 1 < lnks) fetch(ld, lks + 1, lq + 1);
       else if (lt + kGtGrid < total) fetch(ldn, 0, lq + 1);
     }
   };
-  const auto load = [&](int j) __attribute__((always_inline)) {
-    const int i = j & 7;
-    const uint32_t to = lslot * kGwSlot + (j < 8 ? 0 : kGtSide) + 1024 * (8 * wave + i);
-    const uint8_t* src = j < 8 ? x_at + x_off[i] : y_at + y_off[i];
-    if (kGather && j < 8) src += (uint64_t)tok[i] * (uint64_t)(uint32_t)KB;
-    dma16(row + 2 * i < ld.cnt - 64 * lks ? src : pad, to);
+  // Load j of the stage: dy, then x.  tail: the expert's rows end in it.
+  const auto load = [&](int j, bool tail, int slot) __attribute__((always_inline)) {
+    const int i = j & 3;
+    const uint32_t to = slot * kGwSlot + (j < 4 ? kGtSide : 0) + 1024 * (4 * wave + i);
+    const auto in = [&]() __attribute__((always_inline)) { return row() + 2 * i < ld.cnt - 64 * lks; };
+    if (j >= 4 && kGather) {
+      const uint8_t* src = x_at + ((uint64_t)tok[i] * (uint64_t)(uint32_t)KB + x_off[i & 1]);
+      if (__builtin_expect(tail, 0)) src = in() ? src : pad;
+      dma16(src, to);
+    } else {
+      const uint8_t* const base = j < 4 ? y_at + 2 * i * NB : x_at + 2 * i * KB;
+      const uint32_t off = (j < 4 ? y_off : x_off)[i & 1];
+      if (__builtin_expect(tail, 0)) dma16(in() ? base + off : pad, to);
+      else dma16s(base, off, to);
+    }
+    if (kGather && j < 4)  // row j's token, four loads before it is used
+      tok[j] = lds_read<uint32_t>(tok_at + 256 * (lq & 1) + 4 * (row() + 2 * j));
   };
+  const auto tail_stage = [&]() { return ld.cnt - 64 * lks < 64; };
   const auto loaded = [&]() __attribute__((always_inline)) {
+    if (lks + 1 == lnks && lt + kGtGrid >= total) {
+      done = true;
+      return;
+    }
     if (!kGather) x_at += 64 * KB;
     y_at += 64 * NB;
-    lslot ^= 1;
     ++lq;
     if (++lks == lnks) {
       lks = 0;
@@ -581,30 +654,35 @@ __global__ __launch_bounds__(kGtThreads, 1) void gt_weights_kernel(GroupedWgradA
     }
   };
 
-  const int wm = wave / 2, wn = wave % 2, g = lane >> 4, jj = (lane & 15) >> 2;
-  const uint32_t lane_at = (8 * g + jj) * 512 + ((jj | ((g & 1) << 2)) * 32) + (lane & 3) * 8;
-  const uint32_t a_base = lane_at ^ (wn * 256), b_base = kGtSide + (lane_at ^ (wm * 256));
+  const int wm = wave / 2, wn = wave % 2, g = lane >> 4, jj = (lane & 15) >> 2;  // 64 rows of dy by 128 of x a wave
+  const uint32_t v = jj | ((g & 1) << 2), lane_at = (8 * g + jj) * 512 + (lane & 3) * 8;
+  const uint32_t a_base = lane_at + wn * 256 + v * 32, b_base = kGtSide + lane_at + ((4 * wm) ^ v) * 32;
   u32x4 a[2][NF], b[2][MF];
-  const auto read_one = [&](int slot, int st, int i) __attribute__((always_inline)) {
-    if (i < MF) b[st][i] = lds_read_across(slot * kGwSlot + (b_base ^ (i * 32)) + st * 32 * 512);
-    else a[st][i - MF] = lds_read_across(slot * kGwSlot + (a_base ^ ((i - MF) * 32)) + st * 32 * 512);
+  uint32_t ra, rb;
+  const auto aim = [&](int slot) __attribute__((always_inline)) {
+    ra = a_base + slot * kGwSlot;
+    rb = b_base + slot * kGwSlot;
+    asm volatile("" : "+v"(ra), "+v"(rb));
+  };
+  const auto read_one = [&](int st, int i) __attribute__((always_inline)) {
+    if (i < MF) b[st][i] = lds_read_across((rb ^ (i * 32)) + st * 32 * 512);
+    else a[st][i - MF] = lds_read_across((ra ^ ((i - MF) * 32)) + st * 32 * 512);
   };
 
   fetch(ld, 0, 0);
-  int ahead = 0;
-  for (; ahead < 2 && lt < total; ++ahead) {
+  for (int n = 0; n < 2; ++n) {
     wait_vmcnt<0>();  // the stage's tokens (the wave's own)
     asm volatile("" ::: "memory");
-    begin();
+    if (!done) begin();
 #pragma unroll
-    for (int j = 0; j < L; ++j) load(j);
-    loaded();
+    for (int j = 0; j < L; ++j) load(j, tail_stage(), n);
+    if (!done) loaded();
   }
-  if (ahead == 2) wait_vmcnt<L>();
-  else wait_vmcnt<0>();
+  wait_vmcnt<L>();
   g_barrier();
+  aim(0);
 #pragma unroll
-  for (int i = 0; i < MF + NF; ++i) read_one(0, 0, i);
+  for (int i = 0; i < MF + NF; ++i) read_one(0, i);
 
   int slot = 0;
   for (int64_t t = t0; t < total; t += kGtGrid) {
@@ -620,41 +698,16 @@ __global__ __launch_bounds__(kGtThreads, 1) void gt_weights_kernel(GroupedWgradA
 #pragma unroll
     for (int m = 0; m < MF; ++m) g_settle(acc[m]);
     for (int ks = 0; ks < nks; ++ks) {
-      constexpr int kPer = 3;
-#pragma unroll
-      for (int f = 0; f < NF; ++f) {
-#pragma unroll
-        for (int i = f * kPer; i < (f + 1) * kPer && i < MF + NF; ++i) read_one(slot, 1, i);
-        __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-        for (int m = 0; m < MF; ++m) T::mfma(a[0][f], b[0][m], acc[m][f]);
-        __builtin_amdgcn_sched_barrier(0);
-      }
+      gt_step<T, MF, NF, MF + NF, 0>(acc, a[0], b[0], [&](int i) __attribute__((always_inline)) { read_one(1, i); }, GtNothing{});
       g_wait_lds();
       wait_vmcnt<0>();
       g_barrier();
-      --ahead;
-      const bool more = lt < total, next = ahead > 0;
-      if (more) begin();
-#pragma unroll
-      for (int f = 0; f < NF; ++f) {
-        if (next) {
-#pragma unroll
-          for (int i = f * kPer; i < (f + 1) * kPer && i < MF + NF; ++i) read_one(slot ^ 1, 0, i);
-        }
-        if (more) {
-#pragma unroll
-          for (int j = f * 4; j < (f + 1) * 4 && j < L; ++j) load(j);
-        }
-        __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-        for (int m = 0; m < MF; ++m) T::mfma(a[1][f], b[1][m], acc[m][f]);
-        __builtin_amdgcn_sched_barrier(0);
-      }
-      if (more) {
-        loaded();
-        ++ahead;
-      }
+      if (!done) begin();
+      const bool tail = tail_stage();
+      aim(slot ^ 1);
+      gt_step<T, MF, NF, MF + NF, L>(acc, a[1], b[1], [&](int i) __attribute__((always_inline)) { read_one(0, i); },
+                                     [&](int j) __attribute__((always_inline)) { load(j, tail, slot); });
+      if (!done) loaded();
       slot ^= 1;
     }
     if (cur.cnt == 0 && p.accumulate) continue;
@@ -665,7 +718,7 @@ __global__ __launch_bounds__(kGtThreads, 1) void gt_weights_kernel(GroupedWgradA
     for (int m = 0; m < MF; ++m) {
       __builtin_amdgcn_sched_barrier(0);
       g_settle(acc[m]);
-      const int n = cur.nt * kGtRows + wm * 128 + 16 * m + r;
+      const int n = cur.nt * kGtRows + wm * 64 + 16 * m + r;
       const int64_t at = ((int64_t)cur.e * p.N + n) * p.K;
       if (f32) {
         float* const out = static_cast<float*>(p.dw) + at;
@@ -706,6 +759,7 @@ __global__ __launch_bounds__(kGtThreads, 1) void gt_weights_kernel(GroupedWgradA
       }
     }
   }
+  wait_vmcnt<0>();  // no load is on its way into LDS when the workgroup ends
 }
 
 // The dynamic LDS limit of a kernel, raised once a device.
