@@ -81,6 +81,12 @@ struct GType {
     if constexpr (kDtype == MEGAMOE_DTYPE_BF16) asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b));
     else asm volatile("v_mfma_f32_16x16x32_f16 %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b));
   }
+  static __device__ __forceinline__ acc product(u32x4 a, u32x4 b, acc c) {  // (the compiler's own, for chains)
+    if constexpr (kDtype == MEGAMOE_DTYPE_BF16)
+      return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+    else
+      return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+  }
 };
 template <>
 struct GType<kOperandI8> {
@@ -88,6 +94,9 @@ struct GType<kOperandI8> {
   static constexpr int kBytes = 1;
   static __device__ __forceinline__ void mfma(u32x4 a, u32x4 b, acc& c) {
     asm volatile("v_mfma_i32_16x16x64_i8 %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b));
+  }
+  static __device__ __forceinline__ acc product(u32x4 a, u32x4 b, acc c) {
+    return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, a), __builtin_bit_cast(i32x4, b), c, 0, 0, 0);
   }
 };
 // Accumulators in front of other instructions than the products: a result can be read 18 cycles after its
@@ -762,6 +771,287 @@ __global__ __launch_bounds__(kGtThreads, 1) void gt_weights_kernel(GroupedWgradA
   wait_vmcnt<0>();  // no load is on its way into LDS when the workgroup ends
 }
 
+// ============================================================================================
+// Experts (or a dense call) of few rows: the weights' bytes are the work.
+//
+// Work unit: a group, 16 weight rows over the whole of K for one m-tile of up to kGsRows token rows; the groups of
+// all m-tiles are laid end to end and every workgroup (4 waves, one a CU) takes an equal range.  A wave streams its
+// part of the weight rows through an LDS ring of its own, 16 rows by 256 bytes a slot with the m-tile's token rows
+// beside them (they come from the L2), by direct loads: no barrier, no registers, and the ring runs on across groups,
+// m-tiles and experts.  kSplit: the 4 waves split K; at a group's end they leave their sums in LDS and one of them
+// adds the four in wave order.  Otherwise every wave takes groups of its own.
+//
+// Both operands keep 16-byte piece c of row R at place c ^ R of the row's 256 bytes: the 16 rows of one piece are
+// read from 16 different places.
+// ============================================================================================
+constexpr int kGsRows = 16, kGsWaves = 4, kGsChunk = 256, kGsMaxSlots = 8;
+constexpr int kGsWeights = 16 * kGsChunk;                                         // LDS bytes of a slot's weights
+constexpr int kGsRed = 2 * kGsWaves * kWave * 16;
+constexpr int kGsLists = (2 * MEGAMOE_MAX_EXPERTS + 4 * (MEGAMOE_MAX_EXPERTS + 1) + 4 + 15) / 16 * 16;  // experts, m-tile prefix
+constexpr int kGsSplitChunks = 8;  // K of so many chunks is split over the waves
+constexpr int kGsScales = 256;                                                     // int8: of a slot
+
+__host__ __device__ constexpr int gs_slot_bytes(bool i8, int mrows) {
+  return kGsWeights + mrows * kGsChunk + (i8 ? kGsScales : 0);
+}
+
+// Waits until at most `after` (<= K) later slots' loads are outstanding for this wave, of at least 5 each.
+template <int K>
+__device__ __forceinline__ void gs_wait_slots(int after) {
+  if constexpr (K > 0) {
+    if (after < K) {
+      gs_wait_slots<K - 1>(after);
+      return;
+    }
+  }
+  wait_vmcnt<5 * K>();
+}
+
+// Sum of a value over the lanes up to this one.
+__device__ __forceinline__ int gs_scan(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);  // row_shr 1, 2, 4, 8
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);  // row_bcast 15 into rows 1 and 3
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);  // row_bcast 31 into rows 2 and 3
+  return v;
+}
+
+template <bool kL1, int kDtype, bool kSplit>
+__global__ __launch_bounds__(kGsWaves* kWave, 1) void gs_kernel(GroupedArgs p, int slots, int mrows) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t s_gt[];
+  typedef GType<kDtype> T;
+  constexpr bool kI8 = kDtype == kOperandI8;
+  const int lane = lane_id(), r = lane & 15, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  int* const pref = reinterpret_cast<int*>(s_gt);                          // m-tiles before each listed expert
+  uint16_t* const list = reinterpret_cast<uint16_t*>(pref + MEGAMOE_MAX_EXPERTS + 2);
+  const int slot_bytes = gs_slot_bytes(kI8, mrows);
+  const uint32_t red_at = kGsLists, ring_at = kGsLists + (kSplit ? kGsRed : 0) + wave * slots * slot_bytes;
+  const int64_t RB = (int64_t)p.K * T::kBytes;
+  const int nch = (int)((RB + kGsChunk - 1) / kGsChunk), rest = (int)(RB / 16 - (int64_t)(nch - 1) * 16);  // pieces of the last
+
+  // The experts that this kernel takes and their m-tiles.
+  int listed = 1;
+  if (p.counts != nullptr) {
+    if (wave == 0) {
+      int n = 0, tiles = 0;
+      for (int c = 0; c < p.E; c += kWave) {
+        const int cnt = c + lane < p.E ? p.counts[c + lane] : 0;
+        const int own = cnt > 0 && (cnt <= p.small_rows || p.small_all) ? (cnt + mrows - 1) / mrows : 0;
+        const int incl = gs_scan(own);
+        const uint64_t any = __ballot(own > 0);
+        const int at = n + __popcll(any & (((uint64_t)1 << lane) - 1));
+        if (own > 0) {
+          list[at] = (uint16_t)(c + lane);
+          pref[at] = tiles + incl - own;
+        }
+        n += __popcll(any);
+        tiles += __builtin_amdgcn_readlane(incl, kWave - 1);
+      }
+      if (lane == 0) {
+        pref[n] = tiles;
+        pref[MEGAMOE_MAX_EXPERTS + 1] = n;
+      }
+    }
+    __syncthreads();
+    listed = __builtin_amdgcn_readfirstlane(pref[MEGAMOE_MAX_EXPERTS + 1]);
+  }
+  const int64_t tiles = p.counts ? __builtin_amdgcn_readfirstlane(pref[listed]) : (p.M + mrows - 1) / mrows;
+  constexpr int unit = kL1 ? 8 : 16;  // output columns of a group
+  const int nt = (p.N + unit - 1) / unit;
+  const int64_t groups = tiles * nt;
+  // XCD b % 8 takes one contiguous eighth.
+  const int64_t wg = (blockIdx.x % 8) * (kGtGrid / 8) + blockIdx.x / 8;
+  const int64_t part = kSplit ? wg : wg * kGsWaves + wave, parts = kSplit ? kGtGrid : kGtGrid * kGsWaves;
+  const int64_t gb = part * groups / parts, ge = (part + 1) * groups / parts;
+  if (gb >= ge) return;  // with the split, the whole workgroup
+  // this wave's chunks: one at least (the split takes K of four and more)
+  const int c0 = kSplit ? wave * nch / kGsWaves : 0, c1 = kSplit ? (wave + 1) * nch / kGsWaves : nch;
+
+  struct Place {
+    int i, e, cnt, mt, j;  // listed expert i = expert e of cnt rows, m-tile mt, weight block j
+  };
+  const auto expert = [&](Place& at) __attribute__((always_inline)) {
+    if (p.counts == nullptr) {
+      at.e = 0;
+      at.cnt = (int)p.M;
+    } else {
+      at.e = __builtin_amdgcn_readfirstlane((int)list[at.i]);
+      at.cnt = g_scalar(p.counts + at.e);
+    }
+  };
+  Place cur;
+  {
+    const int64_t m = gb / nt;
+    cur.j = (int)(gb % nt);
+    cur.i = 0;
+    if (p.counts != nullptr) {  // by two steps of 64 comparisons
+      const int step = (listed + kWave - 1) / kWave, at = lane * step;
+      const int chunk = __popcll(__ballot(at < listed && pref[at < listed ? at : 0] <= m)) - 1, at2 = chunk * step + lane;
+      cur.i = __builtin_amdgcn_readfirstlane(
+          chunk * step - 1 + __popcll(__ballot(lane < step && at2 < listed && pref[at2 < listed ? at2 : 0] <= m)));
+    }
+    cur.mt = (int)(m - (p.counts ? __builtin_amdgcn_readfirstlane(pref[cur.i]) : 0));
+    expert(cur);
+  }
+  const auto next = [&](Place& at) __attribute__((always_inline)) {  // true: another m-tile
+    if (++at.j < nt) return false;
+    at.j = 0;
+    if ((int64_t)(at.mt + 1) * mrows < at.cnt) {
+      ++at.mt;
+    } else {
+      at.mt = 0;
+      ++at.i;
+      expert(at);
+    }
+    return true;
+  };
+  const auto first_row = [&](const Place& at) __attribute__((always_inline)) {
+    return (p.padded_offsets ? g_scalar(p.padded_offsets + at.e) : 0) + (int64_t)at.mt * mrows;
+  };
+
+  // ---- the stream ----------------------------------------------------------------------------------
+  Place ld = cur;
+  int ld_c = c0, ld_slot = 0, ld_quads = 0;
+  int64_t ld_left = (ge - gb) * (c1 - c0);  // slots still to be requested
+  uint64_t w_at = 0, a_at[4] = {0, 0, 0, 0}, s_at = 0;
+  // Loads of 4 rows a 1 KB: lane l brings a piece of row 4 q + l / 16, whose place is l % 16.
+  const auto row_of = [&](int R) __attribute__((always_inline)) -> int64_t {  // weight row of row R of the group
+    if constexpr (kL1) return ((int64_t)ld.e * 2 + ((R >> 1) & 1)) * p.N + ld.j * 8 + (R >> 2) * 2 + (R & 1);
+    const int n = ld.j * 16 + R;
+    return (int64_t)ld.e * p.N + (n < p.N ? n : p.N - 1);  // (not stored)
+  };
+  const auto group_src = [&]() __attribute__((always_inline)) {
+    w_at = reinterpret_cast<uint64_t>(p.w) + (uint64_t)(row_of(g) * RB);
+    if constexpr (kI8) {
+      if (lane < 16) s_at = reinterpret_cast<uint64_t>(p.w_scales + row_of(lane));
+    }
+  };
+  const auto tile_src = [&]() __attribute__((always_inline)) {
+    const int64_t row0 = first_row(ld);
+    const int left = ld.cnt - ld.mt * mrows < mrows ? ld.cnt - ld.mt * mrows : mrows;
+    int tok[kGsRows];
+#pragma unroll
+    for (int R = 0; R < kGsRows; ++R) {
+      const int64_t row = row0 + (R < left ? R : left - 1);
+      tok[R] = p.row_token ? g_scalar(p.row_token + row) : (int)row;
+    }
+    ld_quads = (left + 3) / 4;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int t = g == 0 ? tok[4 * q] : g == 1 ? tok[4 * q + 1] : g == 2 ? tok[4 * q + 2] : tok[4 * q + 3];
+      a_at[q] = reinterpret_cast<uint64_t>(p.a) + (uint64_t)(uint32_t)t * (uint64_t)RB;
+    }
+    if constexpr (kI8) {
+      int t = tok[0];
+#pragma unroll
+      for (int R = 1; R < kGsRows; ++R) t = r == R ? tok[R] : t;
+      if (lane >= 16) s_at = reinterpret_cast<uint64_t>(p.a_scales + (uint32_t)t);
+    }
+  };
+  const int64_t quad = (kL1 ? 2 : 4) * RB;  // from row R to row R + 4 of the group
+  const int last_rows = kL1 ? 16 : p.N - (nt - 1) * 16;  // (a multiple of 8) rows of the last block
+  const auto request = [&]() __attribute__((always_inline)) {
+    const uint32_t base = ring_at + ld_slot * slot_bytes;
+    const int pieces = ld_c + 1 == nch ? rest : 16;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      // a piece beyond K: the chunk's first instead; the compute skips it
+      const int piece = (lane & 15) ^ (4 * q + g), off = kGsChunk * ld_c + 16 * (piece < pieces ? piece : 0);
+      const int64_t rows = !kL1 && ld.j + 1 == nt && 4 * q >= last_rows ? 0 : q * quad;  // a block's missing rows: its first
+      dma16nt(reinterpret_cast<const uint8_t*>(w_at) + rows + off, base + 1024 * q);
+    }
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      if (q >= ld_quads) break;
+      const int piece = (lane & 15) ^ (4 * q + g), off = kGsChunk * ld_c + 16 * (piece < pieces ? piece : 0);
+      dma16(reinterpret_cast<const uint8_t*>(a_at[q]) + off, base + kGsWeights + 1024 * q);
+    }
+    if (kI8 && ld_c + 1 == c1) dma4(reinterpret_cast<const uint8_t*>(s_at), base + slot_bytes - kGsScales);
+    ld_slot = ld_slot + 1 == slots ? 0 : ld_slot + 1;
+    --ld_left;
+    if (++ld_c == c1) {
+      ld_c = c0;
+      if (ld_left > 0) {
+        if (next(ld)) tile_src();
+        group_src();
+      }
+    }
+  };
+  tile_src();
+  group_src();
+  for (int i = 0; i < slots && ld_left > 0; ++i) request();
+
+  int slot = 0;
+  int64_t row0 = first_row(cur);
+  for (int64_t gi = gb; gi < ge; ++gi) {
+    typename T::acc acc;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) acc[q] = 0;
+    const int left = cur.cnt - cur.mt * mrows < mrows ? cur.cnt - cur.mt * mrows : mrows;
+    const int rl = r < left ? r : left - 1;
+    f32x4 sw{0.f, 0.f, 0.f, 0.f};
+    float sa = 0.0f;
+    for (int c = c0; c < c1; ++c) {
+      const int64_t ahead = (ge - gi) * (c1 - c0) - (c - c0) - 1 - ld_left;  // slots requested after this one
+      gs_wait_slots<kGsMaxSlots - 1>((int)ahead);
+      asm volatile("" ::: "memory");
+      const uint32_t at = ring_at + slot * slot_bytes;
+      u32x4 wv[4], av[4];
+#pragma unroll
+      for (int st = 0; st < 4; ++st) {
+        wv[st] = lds_read16(at + r * kGsChunk + 16 * ((4 * g + st) ^ r));
+        av[st] = lds_read16(at + kGsWeights + rl * kGsChunk + 16 * ((4 * g + st) ^ rl));
+      }
+      if (kI8 && c + 1 == c1) {
+        sw = lds_read<f32x4>(at + slot_bytes - kGsScales + 16 * g);
+        sa = lds_read<float>(at + slot_bytes - kGsScales + 64 + 4 * r);
+      }
+      g_wait_lds();  // the slot's operands are in registers
+      slot = slot + 1 == slots ? 0 : slot + 1;
+      if (ld_left > 0) request();
+      if (c + 1 == nch && rest < 16) {
+#pragma unroll
+        for (int st = 0; st < 4; ++st)
+          if (4 * g + st >= rest) wv[st] = av[st] = u32x4{0u, 0u, 0u, 0u};
+      }
+#pragma unroll
+      for (int st = 0; st < 4; ++st) acc = T::product(wv[st], av[st], acc);
+    }
+    typename T::acc z = acc;
+    if constexpr (kSplit) {
+      typedef typename T::acc A;
+      const uint32_t red = red_at + (gi & 1) * kGsWaves * kWave * 16 + lane * 16;
+      lds_write16(red + wave * kWave * 16, __builtin_bit_cast(u32x4, acc));
+      g_wait_lds();  // the partial sums are written; the stream stays in flight
+      g_barrier();
+      if (wave == (int)(gi % kGsWaves)) {
+        z = __builtin_bit_cast(A, lds_read16(red));
+#pragma unroll
+        for (int k = 1; k < kGsWaves; ++k) z += __builtin_bit_cast(A, lds_read16(red + k * kWave * 16));
+      }
+    }
+    if (!kSplit || wave == (int)(gi % kGsWaves)) {
+      // lane: token row r of the m-tile, weight rows 4g .. 4g+3
+      f32x4 f;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) f[q] = kI8 ? (float)z[q] * sw[q] * sa : (float)z[q];
+      const bool f16 = p.out_dtype == MEGAMOE_DTYPE_F16;
+      if (r < left) {
+        uint16_t* const out = static_cast<uint16_t*>(p.out) + (row0 + r) * (int64_t)p.N;
+        if constexpr (kL1) {
+          *reinterpret_cast<uint32_t*>(out + cur.j * 8 + 2 * g) = g_pack2(g_silu(f[0]) * f[2], g_silu(f[1]) * f[3], f16);
+        } else if (cur.j * 16 + 4 * g < p.N) {
+          *reinterpret_cast<u32x2*>(out + cur.j * 16 + 4 * g) = u32x2{g_pack2(f[0], f[1], f16), g_pack2(f[2], f[3], f16)};
+        }
+      }
+    }
+    if (gi + 1 < ge && next(cur)) row0 = first_row(cur);
+  }
+}
+
 // The dynamic LDS limit of a kernel, raised once a device.
 template <typename F>
 static hipError_t gt_allow_lds(F* kernel, std::atomic<bool> (&done)[kGtDevices]) {
@@ -792,17 +1082,68 @@ static hipError_t launch_gt_weights(const GroupedWgradArgs& a, hipStream_t strea
   return hipGetLastError();
 }
 
+// How the stream kernel runs: K split or not, token rows of an m-tile, ring slots.
+struct GsPlan {
+  bool split;
+  int mrows, slots;
+  size_t lds;
+};
+static GsPlan gs_plan(const GroupedArgs& a, int64_t rows) {
+  GsPlan g;
+  const int64_t chunks = ((int64_t)a.K * (a.dtype == kOperandI8 ? 1 : 2) + kGsChunk - 1) / kGsChunk;
+  g.split = chunks >= kGsSplitChunks;
+  g.mrows = rows > 0 && rows <= 4 ? 4 : rows > 0 && rows <= 8 ? 8 : kGsRows;
+  const int slot = gs_slot_bytes(a.dtype == kOperandI8, g.mrows), fixed = kGsLists + (g.split ? kGsRed : 0);
+  g.slots = (kGtLds - fixed) / (kGsWaves * slot);
+  if (g.slots > kGsMaxSlots) g.slots = kGsMaxSlots;
+  g.lds = (size_t)(fixed + kGsWaves * g.slots * slot);
+  return g;
+}
+
+template <bool kL1, int kDtype, bool kSplit>
+static hipError_t launch_gs_as(const GroupedArgs& a, const GsPlan& plan, hipStream_t stream) {
+  static std::atomic<bool> done[kGtDevices];
+  const hipError_t err = gt_allow_lds(gs_kernel<kL1, kDtype, kSplit>, done);
+  if (err != hipSuccess) return err;
+  hipLaunchKernelGGL((gs_kernel<kL1, kDtype, kSplit>), dim3(kGtGrid), dim3(kGsWaves * kWave), plan.lds, stream, a, plan.slots,
+                     plan.mrows);
+  return hipGetLastError();
+}
+template <bool kL1, int kDtype>
+static hipError_t launch_gs(const GroupedArgs& a, const GsPlan& plan, hipStream_t stream) {
+  return plan.split ? launch_gs_as<kL1, kDtype, true>(a, plan, stream) : launch_gs_as<kL1, kDtype, false>(a, plan, stream);
+}
+
+template <bool kL1, int kDtype>
+static hipError_t launch_both(const GroupedArgs& a, const GsPlan& plan, bool small, bool large, hipStream_t stream) {
+  if (small) {
+    const hipError_t err = launch_gs<kL1, kDtype>(a, plan, stream);
+    if (err != hipSuccess) return err;
+  }
+  return large ? launch_gt<kL1 ? kGtGateUp : kGtPlain, kDtype>(a, stream) : hipSuccess;
+}
+
 hipError_t launch_grouped(const GroupedArgs& a0, bool l1, int64_t max_rows, hipStream_t stream) {
   GroupedArgs a = a0;
-  (void)max_rows;
   a.small_rows = 0;
   if (a.across)
     return a.dtype == MEGAMOE_DTYPE_BF16 ? launch_gt<kGtAcross, MEGAMOE_DTYPE_BF16>(a, stream)
                                          : launch_gt<kGtAcross, MEGAMOE_DTYPE_F16>(a, stream);
+  // A dense call knows its rows.  A grouped one launches both kernels, which take their experts from the counts,
+  // unless the caller's bound says that no expert has more rows than the stream kernel's; that then covers every
+  // expert, should the bound be wrong.
+  const bool dense = a.counts == nullptr;
+  const int64_t rows = dense ? a.M : max_rows;
+  const bool only_small = rows > 0 && rows <= kGsRows;
+  const GsPlan plan = gs_plan(a, rows);
+  a.small_rows = kGsRows;
+  a.small_all = only_small;
+  const bool small = dense ? only_small : true, large = !only_small;
   if (a.dtype == kOperandI8)
-    return l1 ? launch_gt<kGtGateUp, kOperandI8>(a, stream) : launch_gt<kGtPlain, kOperandI8>(a, stream);
-  return a.dtype == MEGAMOE_DTYPE_BF16 ? launch_gt<kGtPlain, MEGAMOE_DTYPE_BF16>(a, stream)
-                                       : launch_gt<kGtPlain, MEGAMOE_DTYPE_F16>(a, stream);
+    return l1 ? launch_both<true, kOperandI8>(a, plan, small, large, stream)
+              : launch_both<false, kOperandI8>(a, plan, small, large, stream);
+  return a.dtype == MEGAMOE_DTYPE_BF16 ? launch_both<false, MEGAMOE_DTYPE_BF16>(a, plan, small, large, stream)
+                                       : launch_both<false, MEGAMOE_DTYPE_F16>(a, plan, small, large, stream);
 }
 
 hipError_t launch_grouped_wgrad(const GroupedWgradArgs& a, hipStream_t stream) {
