@@ -31,6 +31,9 @@ constexpr int kGtCols = 256, kGtRows = 256;         // A-side and B-side rows of
 constexpr int kGtStage = 128;                       // bytes of K a stage (64 or 128 elements)
 constexpr int kGtSide = kGtCols * kGtStage;         // LDS bytes of a stage's A side
 constexpr int kGtLds = 160 * 1024;
+// ns of a tile, by its rows (of 256 columns, and of the tiles of 64 x 64): a stage of 128 bytes of K, and the rest.
+constexpr int64_t kGtNs4[2] = {1300, 4000}, kGtNs2[2] = {1150, 5000}, kGtNs1[2] = {1050, 5000}, kGtNsFine[2] = {250, 1500};
+constexpr int64_t kGtNsFineAlone = 330;  // of a stage where no two tiles of 64 rows share weights
 constexpr int kGtBand = 8;                          // m-tiles walked together, for L2 reuse of the weights
 // The kernels have no static LDS: addresses start at 0.  At the end: two list lengths, m-tile prefix int32 [E + 1],
 // two lists uint16 [E].
@@ -60,6 +63,17 @@ __device__ __forceinline__ void g_wait_lds() {
 __device__ __forceinline__ int g_scalar(const int32_t* p) {
   const uint64_t at = scalar_addr(reinterpret_cast<const uint8_t*>(p));
   return *reinterpret_cast<const __attribute__((address_space(4))) int32_t*>(at);
+}
+
+// Sum of a value over the lanes up to this one.
+__device__ __forceinline__ int g_scan(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);  // row_shr 1, 2, 4, 8
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);  // row_bcast 15 into rows 1 and 3
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);  // row_bcast 31 into rows 2 and 3
+  return v;
 }
 
 // What follows from the lane is computed where it is used, not held in registers through a loop.
@@ -480,6 +494,227 @@ __device__ __forceinline__ void gt_phase(const GroupedArgs& p, int64_t t0, int64
   wait_vmcnt<0>();  // no load is on its way into LDS when the phase, or the workgroup, ends
 }
 
+// ============================================================================================
+// The same products where tiles of 256 columns would leave most of the chip empty: 64 weight rows (gate+up: 32 of
+// each) x 64 token rows a tile, by the same workgroups of 8 waves.
+//
+// A stage is 256 bytes of K, 32 KB, and the ring holds four: with few products a stage, a tile waits for memory and for
+// the barrier (with stages of 128 bytes, 64 x 4096 x 7168 int8 took 26.9 us).  Waves 0-3 multiply a stage's first
+// 128 bytes of K, waves 4-7 its second, 32 x 32 each; at a tile's end the second four leave their sums in
+// LDS and the first four add and store.  One barrier a stage: behind it everyone's loads of the stage are visible and
+// the slot of the stage before is free.
+// ============================================================================================
+constexpr int kGfStage = 256, kGfSide = 64 * kGfStage, kGfSlot = 2 * kGfSide, kGfD = 4;
+constexpr int kGfRedAt = kGfD * kGfSlot, kGfRowsAt = kGfRedAt + 4 * kWave * 64, kGfScalesAt = kGfRowsAt + 2 * 64 * 4;
+constexpr int kGfScaleBuf = 4 * (64 + 64);
+static_assert(kGfScalesAt + (kGfD + 1) * kGfScaleBuf <= kGtLists, "the LDS layout fits");
+
+template <int kOp, int kDtype, typename Find>
+__device__ __forceinline__ void gt_fine_phase(const GroupedArgs& p, int64_t t0, int64_t total, const Find& find) {
+  typedef GType<kDtype> T;
+  constexpr bool kL1 = kOp == kGtGateUp, kAcross = kOp == kGtAcross, kI8 = kDtype == kOperandI8;
+  constexpr int cols = kL1 ? 32 : 64, D = kGfD, L = 4;
+  if (t0 >= total) return;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), lane = lane_id();
+  const int64_t RB = (int64_t)p.K * T::kBytes, NB = (int64_t)p.N * T::kBytes;
+  const int nks = (int)((RB + kGfStage - 1) / kGfStage);
+  const bool tokens = wave >= 4;  // whose rows this wave loads: 16 of the tile's weight rows or token rows
+  const int ww = wave & 3;
+  const auto piece = [&](int j) { return (lane & 15) ^ (4 * j + (lane >> 4)); };  // of load instruction j: 4 rows by 16
+
+  // ---- loads -------------------------------------------------------------------------------------
+  GtTile ld;
+  int64_t lt = t0;
+  int lks = 0, lseq = 0;
+  bool done = false;
+  uint64_t at[L];
+  const auto fetch_rows = [&](int64_t t, int buf) __attribute__((always_inline)) {
+    if (!kAcross && p.row_token != nullptr && wave == 0 && t < total) {
+      const GtTile x = find(t);
+      dma4(reinterpret_cast<const uint8_t*>(p.row_token + x.row0 + (lane < x.left ? lane : x.left - 1)),
+           kGfRowsAt + 4 * 64 * buf);
+    }
+  };
+  const auto a_row = [&](int R) __attribute__((always_inline)) -> uint32_t {
+    if (!kAcross && p.row_token != nullptr) return lds_read<uint32_t>(kGfRowsAt + 4 * (64 * (lseq & 1) + R));
+    return (uint32_t)((int)ld.row0 + (R < ld.left ? R : ld.left - 1));
+  };
+  // Weight row of the tile's row R: gate+up: 16 gate and 16 up rows for either half of the waves.
+  const auto w_row = [&](int R) __attribute__((always_inline)) -> int64_t {
+    const int c = ld.nt * cols + (kL1 ? R / 32 * 16 + R % 16 : R);
+    return (int64_t)ld.e * (kL1 ? 2 : 1) * p.N + (c < p.N ? c : p.N - 1) + (kL1 && (R & 16) ? p.N : 0);
+  };
+  const auto enter = [&]() __attribute__((always_inline)) {
+    ld = find(lt);
+#pragma unroll
+    for (int j = 0; j < L; ++j) {
+      const int R = 16 * ww + 4 * j + lane / 16;
+      if (tokens) {
+        at[j] = reinterpret_cast<uint64_t>(p.a) + (uint64_t)a_row(R) * (uint64_t)RB + 16 * piece(j);
+      } else if constexpr (kAcross) {  // 128 rows of the reduced dimension, 128 bytes each, 8 a load
+        const int R = 8 * (4 * ww + j) + lane / 8;
+        const int c = (lane & 7) ^ ((((R >> 1) & 1) | ((R >> 3) & 1) << 1) << 1), last = p.N / 8 - 1 - ld.nt * 8;
+        at[j] = reinterpret_cast<uint64_t>(p.w) + (uint64_t)(((int64_t)ld.e * p.K + R) * NB) + 128 * (uint64_t)ld.nt +
+                16 * (c < last ? c : last);
+      } else {
+        at[j] = reinterpret_cast<uint64_t>(p.w) + (uint64_t)(w_row(R) * RB) + 16 * piece(j);
+      }
+    }
+    if constexpr (kI8) {
+      const uint32_t to = kGfScalesAt + (lseq % (D + 1)) * kGfScaleBuf;
+      if (wave == 1) dma4(reinterpret_cast<const uint8_t*>(p.w_scales + w_row(lane)), to);
+      if (wave == 2) dma4(reinterpret_cast<const uint8_t*>(p.a_scales + a_row(lane)), to + 256);
+    }
+    fetch_rows(lt + kGtGrid, (lseq + 1) & 1);
+    ++lseq;
+  };
+  const bool ragged = (RB & (kGfStage - 1)) != 0;
+  const int left = (int)((RB & (kGfStage - 1)) / 16);
+  const auto last_stage = [&]() { return lks + 1 == nks && lt + kGtGrid >= total; };
+  const auto beyond = [&](int j) __attribute__((always_inline)) {  // what load j brings of a row's last stage lies behind its end
+    return (kAcross && !tokens ? 4 * ww + j : piece(j)) >= left;
+  };
+  // The next stage into a slot.  Behind a row's end: the stage's first piece (or rows) instead, cleared later.
+  const auto load = [&](int slot) __attribute__((always_inline)) {
+    if (!done && lks == 0) {
+      if (nks < D && lseq > 0) {  // its rows were asked for with the tile before, less than a ring ago
+        wait_vmcnt<0>();
+        g_barrier();
+      }
+      enter();
+    }
+    if (ragged && !done && lks + 1 == nks) {
+#pragma unroll
+      for (int j = 0; j < L; ++j)
+        if (beyond(j)) at[j] -= kAcross && !tokens ? (uint64_t)(8 * (4 * ww + j)) * (uint64_t)NB : (uint64_t)(16 * piece(j));
+    }
+    const uint64_t step = last_stage() ? 0 : kAcross && !tokens ? 128 * (uint64_t)NB : kGfStage;
+#pragma unroll
+    for (int j = 0; j < L; ++j) {
+      dma16(reinterpret_cast<const uint8_t*>(at[j]), slot * kGfSlot + (tokens ? kGfSide : 0) + 1024 * (4 * ww + j));
+      at[j] += step;
+    }
+    if (last_stage()) {
+      done = true;
+    } else if (++lks == nks) {
+      lks = 0;
+      lt += kGtGrid;
+    }
+  };
+  const auto clear = [&](int slot) __attribute__((always_inline)) {
+#pragma unroll
+    for (int j = 0; j < L; ++j)
+      if (beyond(j))
+        lds_write16(slot * kGfSlot + (tokens ? kGfSide : 0) + 1024 * (4 * ww + j) + 16 * lane, u32x4{0u, 0u, 0u, 0u});
+  };
+
+  g_wait_lds();
+  g_barrier();  // the phase before is done with LDS
+  fetch_rows(lt, 0);
+  wait_vmcnt<0>();
+  g_barrier();
+#pragma unroll 1
+  for (int i = 0; i < D - 1; ++i) load(i);
+
+  // ---- products ------------------------------------------------------------------------------------
+  const int half = wave >> 2, wm = ww >> 1, wn = ww & 1, r = lane & 15, g = lane >> 4, jj = r >> 2;
+  const uint32_t along = r * kGfStage + 16 * ((8 * half + g) ^ r);
+  const uint32_t b_at = kGfSide + wm * 32 * kGfStage + along;
+  const uint32_t a_at = kAcross ? (64 * half + 8 * g + jj) * 128 + (((2 * wn) ^ ((jj >> 1) | (g & 1) << 1)) * 32) + (lane & 3) * 8
+                                : wn * 32 * kGfStage + along;
+  int slot = 0, seq = 0;
+  for (int64_t t = t0; t < total; t += kGtGrid) {
+    typename T::acc acc[2][2];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) acc[i / 2][i % 2][q] = 0;
+    for (int ks = 0; ks < nks; ++ks) {
+      wait_vmcnt<(D - 2) * L>();
+      if (ragged && ks + 1 == nks) clear(slot);
+      g_wait_lds();
+      g_barrier();
+      u32x4 a[2][2], b[2][2];
+#pragma unroll
+      for (int st = 0; st < 2; ++st)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          b[st][i] = lds_read16(slot * kGfSlot + (b_at ^ (st * 64)) + i * 16 * kGfStage);
+          if constexpr (kAcross) {
+            const uint32_t from = slot * kGfSlot + (a_at ^ (i * 32)) + st * 32 * 128;
+            typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+            const u32x2 l = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(reinterpret_cast<lds_s16x4*>(from)));
+            const u32x2 h = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(reinterpret_cast<lds_s16x4*>(from + 4 * 128)));
+            a[st][i] = u32x4{l[0], l[1], h[0], h[1]};
+          } else {
+            a[st][i] = lds_read16(slot * kGfSlot + (a_at ^ (st * 64)) + i * 16 * kGfStage);
+          }
+        }
+      load(slot == 0 ? D - 1 : slot - 1);
+#pragma unroll
+      for (int st = 0; st < 2; ++st)
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+          for (int f = 0; f < 2; ++f) acc[m][f] = T::product(a[st][f], b[st][m], acc[m][f]);
+      slot = slot + 1 == D ? 0 : slot + 1;
+    }
+    const uint32_t red = kGfRedAt + (ww * kWave + lane) * 16;
+    if (half == 1) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) lds_write16(red + i * 4 * kWave * 16, __builtin_bit_cast(u32x4, acc[i / 2][i % 2]));
+    }
+    g_wait_lds();
+    g_barrier();
+    const uint32_t sc = kGfScalesAt + (seq % (D + 1)) * kGfScaleBuf;
+    ++seq;
+    if (half == 1) continue;
+    const GtTile cur = find(t);
+    const bool f16 = p.out_dtype == MEGAMOE_DTYPE_F16;
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+      const int R = wm * 32 + 16 * m + r;
+      f32x4 z[2];
+#pragma unroll
+      for (int f = 0; f < 2; ++f) {
+        const typename T::acc sum = acc[m][f] + __builtin_bit_cast(typename T::acc, lds_read16(red + (2 * m + f) * 4 * kWave * 16));
+        if constexpr (kI8) {
+          const f32x4 sw = lds_read<f32x4>(sc + 4 * (wn * 32 + 16 * f + 4 * g));
+          const float sa = lds_read<float>(sc + 256 + 4 * R);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) z[f][q] = (float)sum[q] * sw[q] * sa;
+        } else {
+          z[f] = sum;
+        }
+      }
+      uint16_t* const out = static_cast<uint16_t*>(p.out) + (cur.row0 + R) * (int64_t)p.N;
+      if constexpr (kL1) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) z[0][q] = g_silu(z[0][q]) * z[1][q];
+        const int c = cur.nt * cols + wn * 16 + 4 * g;
+        if (R < cur.left && c < p.N)
+          *reinterpret_cast<u32x2*>(out + c) = u32x2{g_pack2(z[0][0], z[0][1], f16), g_pack2(z[0][2], z[0][3], f16)};
+      } else {
+        const u32x4 v = g_gather8(u32x2{g_pack2(z[0][0], z[0][1], f16), g_pack2(z[0][2], z[0][3], f16)},
+                                  u32x2{g_pack2(z[1][0], z[1][1], f16), g_pack2(z[1][2], z[1][3], f16)});
+        const int c = cur.nt * cols + wn * 32 + 16 * (g & 1) + 8 * (g >> 1);
+        if (R < cur.left && c < p.N) *reinterpret_cast<u32x4*>(out + c) = v;
+      }
+    }
+  }
+  wait_vmcnt<0>();
+}
+
+// Whether the tiles of 64 take the call: the time of the fullest workgroup either way, of tiles of nks stages.
+__device__ __forceinline__ bool gt_fine(int64_t n4, int64_t n2, int64_t n1, int64_t fine, int nks) {
+  const int64_t t4 = nks * kGtNs4[0] + kGtNs4[1], t2 = nks * kGtNs2[0] + kGtNs2[1], t1 = nks * kGtNs1[0] + kGtNs1[1];
+  const int64_t one = n4 ? t4 : n2 ? t2 : t1;
+  const int64_t n = n4 + n2 + n1, rounds = (n + kGtGrid - 1) / kGtGrid;
+  int64_t all = n ? (n4 * t4 + n2 * t2 + n1 * t1) / n * rounds : 0;
+  if (all < one) all = one;
+  return (fine + kGtGrid - 1) / kGtGrid * (nks * (n4 || n2 ? kGtNsFine[0] : kGtNsFineAlone) + kGtNsFine[1]) < all;
+}
+
 template <int kOp, int kDtype>
 __global__ __launch_bounds__(kGtThreads, 1) void gt_kernel(GroupedArgs p) {
   extern __shared__ __attribute__((aligned(16))) uint8_t s_gt[];
@@ -488,43 +723,53 @@ __global__ __launch_bounds__(kGtThreads, 1) void gt_kernel(GroupedArgs p) {
   uint16_t* const list2 = reinterpret_cast<uint16_t*>(pref + p.E + 1);    // experts with a last tile of 128 rows
   uint16_t* const list1 = list2 + p.E;                                    // of 64
   const int E = p.E, lane = lane_id();
+  constexpr int cols = kOp == kGtGateUp ? kGtCols / 2 : kGtCols;
+  const int ntn = (p.N + cols - 1) / cols, ntf = (p.N + cols / 4 - 1) / (cols / 4);
   if (threadIdx.x < kWave) {
+    const auto rows_of = [&](int e) {
+      return e < E ? p.counts ? p.counts[e] : (int)p.M : 0;
+    };
+    const auto last = [&](int rest) { return rest > 128 ? 4 : rest > 64 ? 2 : rest > 0 ? 1 : 0; };  // tile of a last part
+    int own4 = 0, own2 = 0, own1 = 0, ownf = 0;
+    for (int c = lane; c < E; c += kWave) {
+      const int cnt = rows_of(c), l = last(cnt % kGtRows);
+      own4 += cnt / kGtRows + (l == 4);
+      own2 += l == 2;
+      own1 += l == 1;
+      ownf += (cnt + 63) / 64;
+    }
+    const bool fine = gt_fine((int64_t)wave_sum_i32(own4) * ntn, (int64_t)wave_sum_i32(own2) * ntn,
+                              (int64_t)wave_sum_i32(own1) * ntn, (int64_t)wave_sum_i32(ownf) * ntf,
+                              (int)(((int64_t)p.K * GType<kDtype>::kBytes + kGtStage - 1) / kGtStage));
     int carry = 0, n2 = 0, n1 = 0;
     const uint64_t below = ((uint64_t)1 << lane) - 1;
     for (int c = 0; c < E; c += kWave) {
-      const int cnt = c + lane < E ? p.counts ? p.counts[c + lane] : (int)p.M : 0, rest = cnt % kGtRows;
-      const int own = cnt / kGtRows + (rest > 128 ? 1 : 0);
-      int incl = own;
-#pragma unroll
-      for (int o = 1; o < kWave; o <<= 1) {
-        const int t = __shfl_up(incl, o, kWave);
-        if (lane >= o) incl += t;
-      }
+      const int cnt = rows_of(c + lane), l = last(cnt % kGtRows);
+      const int own = fine ? (cnt + 63) / 64 : cnt / kGtRows + (l == 4);
+      const int incl = g_scan(own);
       if (c + lane < E) pref[c + lane] = carry + incl - own;
-      carry += __shfl(incl, kWave - 1, kWave);
-      const bool in2 = rest > 64 && rest <= 128, in1 = rest > 0 && rest <= 64 && (cnt > p.small_rows);
-      const uint64_t b2 = __ballot(in2), b1 = __ballot(in1);
-      if (in2) list2[n2 + __popcll(b2 & below)] = (uint16_t)(c + lane);
-      if (in1) list1[n1 + __popcll(b1 & below)] = (uint16_t)(c + lane);
+      carry += __builtin_amdgcn_readlane(incl, kWave - 1);
+      const uint64_t b2 = __ballot(l == 2), b1 = __ballot(l == 1);
+      if (l == 2) list2[n2 + __popcll(b2 & below)] = (uint16_t)(c + lane);
+      if (l == 1) list1[n1 + __popcll(b1 & below)] = (uint16_t)(c + lane);
       n2 += __popcll(b2);
       n1 += __popcll(b1);
     }
     if (lane == 0) {
       pref[E] = carry;
-      s_n[0] = n2;
+      s_n[0] = fine ? -1 : n2;
       s_n[1] = n1;
     }
   }
   __syncthreads();
-  constexpr int cols = kOp == kGtGateUp ? kGtCols / 2 : kGtCols;
-  const int ntn = (p.N + cols - 1) / cols;
-  const int64_t total4 = (int64_t)__builtin_amdgcn_readfirstlane(pref[E]) * ntn;
+  const bool fine = __builtin_amdgcn_readfirstlane(s_n[0]) < 0;
+  const int64_t total4 = (int64_t)__builtin_amdgcn_readfirstlane(pref[E]) * (fine ? ntf : ntn);
   const int64_t total2 = (int64_t)__builtin_amdgcn_readfirstlane(s_n[0]) * ntn;
   const int64_t total1 = (int64_t)__builtin_amdgcn_readfirstlane(s_n[1]) * ntn;
   const auto count = [&](int e) { return p.counts ? g_scalar(p.counts + e) : (int)p.M; };
   const auto offset = [&](int e) { return (int64_t)(p.padded_offsets ? g_scalar(p.padded_offsets + e) : 0); };
-  // 256-row tile t: its expert by two steps of 64 comparisons (at most 1024 experts).
-  const auto find4 = [&](int64_t t) __attribute__((always_inline)) {
+  // Tile t of those of 256 (or 64) rows: its expert by two steps of 64 comparisons (at most 1024 experts).
+  const auto find_tile = [&](int64_t t, int rows, int ntn) __attribute__((always_inline)) {
     const int step = (E + kWave - 1) / kWave;
     const int at = lane * step;
     const int chunk = __popcll(__ballot(at < E && (int64_t)pref[at < E ? at : 0] * ntn <= t)) - 1;
@@ -537,9 +782,9 @@ __global__ __launch_bounds__(kGtThreads, 1) void gt_kernel(GroupedArgs p) {
     const int band = (int)(local / ((int64_t)kGtBand * ntn)), in = (int)(local % ((int64_t)kGtBand * ntn));
     const int width = min(kGtBand, mts - band * kGtBand);
     const int mt = band * kGtBand + in % width;
-    const int cnt = count(e);
-    return GtTile{e, in / width, cnt - mt * kGtRows, offset(e) + (int64_t)mt * kGtRows};
+    return GtTile{e, in / width, count(e) - mt * rows, offset(e) + (int64_t)mt * rows};
   };
+  const auto find4 = [&](int64_t t) __attribute__((always_inline)) { return find_tile(t, kGtRows, ntn); };
   const auto find_last = [&](const uint16_t* list, int64_t t) __attribute__((always_inline)) {
     const int e = __builtin_amdgcn_readfirstlane((int)list[t / ntn]);
     const int cnt = count(e), mt = cnt / kGtRows;
@@ -549,6 +794,10 @@ __global__ __launch_bounds__(kGtThreads, 1) void gt_kernel(GroupedArgs p) {
   // other, so that a workgroup that has one tile more of one list has one less of the next.
   const int64_t wg = (blockIdx.x % 8) * (kGtGrid / 8) + blockIdx.x / 8;
   const auto first = [&](int64_t before) { return (wg - before % kGtGrid + kGtGrid) % kGtGrid; };
+  if (fine) {
+    gt_fine_phase<kOp, kDtype>(p, wg, total4, [&](int64_t t) __attribute__((always_inline)) { return find_tile(t, 64, ntf); });
+    return;
+  }
   gt_phase<kOp, kDtype, 4>(p, wg, total4, find4);
   gt_phase<kOp, kDtype, 2>(p, first(total4), total2, [&](int64_t t) { return find_last(list2, t); });
   gt_phase<kOp, kDtype, 1>(p, first(total4 + total2), total1, [&](int64_t t) { return find_last(list1, t); });
@@ -788,7 +1037,7 @@ constexpr int kGsRows = 16, kGsWaves = 4, kGsChunk = 256, kGsMaxSlots = 8;
 constexpr int kGsWeights = 16 * kGsChunk;                                         // LDS bytes of a slot's weights
 constexpr int kGsRed = 2 * kGsWaves * kWave * 16;
 constexpr int kGsLists = (2 * MEGAMOE_MAX_EXPERTS + 4 * (MEGAMOE_MAX_EXPERTS + 1) + 4 + 15) / 16 * 16;  // experts, m-tile prefix
-constexpr int kGsSplitChunks = 8;  // K of so many chunks is split over the waves
+constexpr int kGsSplitChunks = 16;  // K of so many chunks is split over the waves
 constexpr int kGsScales = 256;                                                     // int8: of a slot
 
 __host__ __device__ constexpr int gs_slot_bytes(bool i8, int mrows) {
@@ -807,17 +1056,6 @@ __device__ __forceinline__ void gs_wait_slots(int after) {
   wait_vmcnt<5 * K>();
 }
 
-// Sum of a value over the lanes up to this one.
-__device__ __forceinline__ int gs_scan(int v) {
-  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);  // row_shr 1, 2, 4, 8
-  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false);
-  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false);
-  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false);
-  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);  // row_bcast 15 into rows 1 and 3
-  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);  // row_bcast 31 into rows 2 and 3
-  return v;
-}
-
 template <bool kL1, int kDtype, bool kSplit>
 __global__ __launch_bounds__(kGsWaves* kWave, 1) void gs_kernel(GroupedArgs p, int slots, int mrows) {
   extern __shared__ __attribute__((aligned(16))) uint8_t s_gt[];
@@ -832,15 +1070,15 @@ __global__ __launch_bounds__(kGsWaves* kWave, 1) void gs_kernel(GroupedArgs p, i
   const int64_t RB = (int64_t)p.K * T::kBytes;
   const int nch = (int)((RB + kGsChunk - 1) / kGsChunk), rest = (int)(RB / 16 - (int64_t)(nch - 1) * 16);  // pieces of the last
 
-  // The experts that this kernel takes and their m-tiles.
+  // The experts that have rows and their m-tiles.
   int listed = 1;
   if (p.counts != nullptr) {
     if (wave == 0) {
       int n = 0, tiles = 0;
       for (int c = 0; c < p.E; c += kWave) {
         const int cnt = c + lane < p.E ? p.counts[c + lane] : 0;
-        const int own = cnt > 0 && (cnt <= p.small_rows || p.small_all) ? (cnt + mrows - 1) / mrows : 0;
-        const int incl = gs_scan(own);
+        const int own = (cnt + mrows - 1) / mrows;
+        const int incl = g_scan(own);
         const uint64_t any = __ballot(own > 0);
         const int at = n + __popcll(any & (((uint64_t)1 << lane) - 1));
         if (own > 0) {
@@ -1091,7 +1329,12 @@ struct GsPlan {
 static GsPlan gs_plan(const GroupedArgs& a, int64_t rows) {
   GsPlan g;
   const int64_t chunks = ((int64_t)a.K * (a.dtype == kOperandI8 ? 1 : 2) + kGsChunk - 1) / kGsChunk;
-  g.split = chunks >= kGsSplitChunks;
+  // A group of 16 chunks and more is split (a wave of 8 alone streams 5.8 TB/s of 9 experts' int8 gate+up, 7168 long,
+  // that all four stream at 5.8 with half the groups' imbalance: 45.6 us, 49.9 unsplit).  A shorter one has too few
+  // chunks between two barriers (48 experts' int8 down projection, 2048 long: 137 us split, 104 unsplit), and is split
+  // only where a dense call has too few groups for the waves (8 x 7168 x 2048 int8: 6.9 us, 7.9 unsplit).
+  const int64_t groups = (a.N + 15) / 16;
+  g.split = chunks >= kGsSplitChunks || (chunks >= kGsSplitChunks / 2 && a.counts == nullptr && groups <= 2 * kGtGrid);
   g.mrows = rows > 0 && rows <= 4 ? 4 : rows > 0 && rows <= 8 ? 8 : kGsRows;
   const int slot = gs_slot_bytes(a.dtype == kOperandI8, g.mrows), fixed = kGsLists + (g.split ? kGsRed : 0);
   g.slots = (kGtLds - fixed) / (kGsWaves * slot);
@@ -1114,36 +1357,25 @@ static hipError_t launch_gs(const GroupedArgs& a, const GsPlan& plan, hipStream_
   return plan.split ? launch_gs_as<kL1, kDtype, true>(a, plan, stream) : launch_gs_as<kL1, kDtype, false>(a, plan, stream);
 }
 
-template <bool kL1, int kDtype>
-static hipError_t launch_both(const GroupedArgs& a, const GsPlan& plan, bool small, bool large, hipStream_t stream) {
-  if (small) {
-    const hipError_t err = launch_gs<kL1, kDtype>(a, plan, stream);
-    if (err != hipSuccess) return err;
-  }
-  return large ? launch_gt<kL1 ? kGtGateUp : kGtPlain, kDtype>(a, stream) : hipSuccess;
-}
-
-hipError_t launch_grouped(const GroupedArgs& a0, bool l1, int64_t max_rows, hipStream_t stream) {
-  GroupedArgs a = a0;
-  a.small_rows = 0;
+hipError_t launch_grouped(const GroupedArgs& a, bool l1, int64_t max_rows, hipStream_t stream) {
   if (a.across)
     return a.dtype == MEGAMOE_DTYPE_BF16 ? launch_gt<kGtAcross, MEGAMOE_DTYPE_BF16>(a, stream)
                                          : launch_gt<kGtAcross, MEGAMOE_DTYPE_F16>(a, stream);
-  // A dense call knows its rows.  A grouped one launches both kernels, which take their experts from the counts,
-  // unless the caller's bound says that no expert has more rows than the stream kernel's; that then covers every
-  // expert, should the bound be wrong.
+  // The stream kernel takes calls of at most 16 rows an expert, by the caller's bound (it covers every expert, should
+  // the bound be wrong), and dense calls of as many.  Without such a bound the tile kernel takes all experts: beside
+  // 384 experts of 8 rows (int8, 2048 -> 7168) the stream kernel's 1010 us are its 880, 8 experts of 3 rows (bf16, 7168 ->
+  // 4096) take 74 us and 80, and 16 small experts 10.5 us in two launches and 8.7 in one.
   const bool dense = a.counts == nullptr;
   const int64_t rows = dense ? a.M : max_rows;
-  const bool only_small = rows > 0 && rows <= kGsRows;
+  if (!(rows > 0 && rows <= kGsRows)) {
+    if (a.dtype == kOperandI8) return l1 ? launch_gt<kGtGateUp, kOperandI8>(a, stream) : launch_gt<kGtPlain, kOperandI8>(a, stream);
+    return a.dtype == MEGAMOE_DTYPE_BF16 ? launch_gt<kGtPlain, MEGAMOE_DTYPE_BF16>(a, stream)
+                                         : launch_gt<kGtPlain, MEGAMOE_DTYPE_F16>(a, stream);
+  }
   const GsPlan plan = gs_plan(a, rows);
-  a.small_rows = kGsRows;
-  a.small_all = only_small;
-  const bool small = dense ? only_small : true, large = !only_small;
-  if (a.dtype == kOperandI8)
-    return l1 ? launch_both<true, kOperandI8>(a, plan, small, large, stream)
-              : launch_both<false, kOperandI8>(a, plan, small, large, stream);
-  return a.dtype == MEGAMOE_DTYPE_BF16 ? launch_both<false, MEGAMOE_DTYPE_BF16>(a, plan, small, large, stream)
-                                       : launch_both<false, MEGAMOE_DTYPE_F16>(a, plan, small, large, stream);
+  if (a.dtype == kOperandI8) return l1 ? launch_gs<true, kOperandI8>(a, plan, stream) : launch_gs<false, kOperandI8>(a, plan, stream);
+  return a.dtype == MEGAMOE_DTYPE_BF16 ? launch_gs<false, MEGAMOE_DTYPE_BF16>(a, plan, stream)
+                                       : launch_gs<false, MEGAMOE_DTYPE_F16>(a, plan, stream);
 }
 
 hipError_t launch_grouped_wgrad(const GroupedWgradArgs& a, hipStream_t stream) {

@@ -186,8 +186,6 @@ struct GroupedArgs {
   void* out;                      // [*, N]
   int32_t dtype, out_dtype;
   bool across;                    // the rows' gradient: weights are read across their rows
-  int32_t small_rows = 0;         // experts of at most so many rows are the stream kernel's
-  bool small_all = false;         // the tile kernel is not launched: the stream kernel takes every expert
 };
 // max_rows: the caller's bound on an expert's rows, 0 = none.
 hipError_t launch_grouped(const GroupedArgs& a, bool l1, int64_t max_rows, hipStream_t stream);
