@@ -33,6 +33,7 @@ constexpr int kGtSide = kGtCols * kGtStage;         // LDS bytes of a stage's A 
 constexpr int kGtLds = 160 * 1024;
 // ns of a tile, by its rows (of 256 columns, and of the tiles of 64 x 64): a stage of 128 bytes of K, and the rest.
 constexpr int64_t kGtNs4[2] = {1300, 4000}, kGtNs2[2] = {1150, 5000}, kGtNs1[2] = {1050, 5000}, kGtNsFine[2] = {250, 1500};
+constexpr int kGwTile = 60, kGwFineTile = 20;  // the weights' gradient's tiles, beside their stages, in tenths of a us
 constexpr int64_t kGtNsFineAlone = 330;  // of a stage where no two tiles of 64 rows share weights
 constexpr int kGtBand = 8;                          // m-tiles walked together, for L2 reuse of the weights
 // The kernels have no static LDS: addresses start at 0.  At the end: two list lengths, m-tile prefix int32 [E + 1],
@@ -834,10 +835,211 @@ __global__ __launch_bounds__(kGtThreads, 1) void gt_kernel(GroupedArgs p) {
 // ============================================================================================
 constexpr int kGwSlot = 2 * kGtSide;
 constexpr int kGwTokens = 2 * kGwSlot;               // LDS: the waves' tokens of two stages' rows
-constexpr int kGwLds = kGwTokens + kGtWaves * 2 * 64 * 4;
+static_assert(kGwTokens + kGtWaves * 2 * 64 * 4 <= kGtLds, "the LDS layout fits");
+
+// Old values added to four consecutive gradients, at `out` (accumulate).
+__device__ __forceinline__ f32x4 gw_add(f32x4 z, const uint8_t* out, int dtype) {
+  if (dtype == MEGAMOE_DTYPE_F32) return z + *reinterpret_cast<const f32x4*>(out);
+  const u32x2 old = *reinterpret_cast<const u32x2*>(out);
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const uint32_t bits = (old[q / 2] >> (16 * (q & 1))) & 0xFFFFu;
+    const uint16_t b16 = (uint16_t)bits;
+    z[q] += dtype == MEGAMOE_DTYPE_F16 ? (float)__builtin_bit_cast(_Float16, b16) : bf16_bits_to_f32(bits);
+  }
+  return z;
+}
+
+// Small matrices: 64 columns of x by 64 of dy a tile, 128 of the expert's rows a stage, as the tiles of 64 x 64 above:
+// a ring of four slots, one barrier a stage, half of the waves on either half of its rows.  Gathered rows: the
+// expert's tokens lie in LDS (at most kGwMaxTokens; longer experts are left to the large tiles).
+constexpr int kGwFineStage = 128, kGwMaxTokens = 3584, kGwFineTokens = kGfRedAt + 4 * kWave * 64;
+static_assert(kGwFineTokens + 4 * kGwMaxTokens <= kGtLds, "the LDS layout fits");
+
+template <int kDtype, bool kGather>
+__device__ __forceinline__ void gw_fine_phase(const GroupedWgradArgs& p) {
+  typedef GType<kDtype> T;
+  constexpr int D = kGfD, L = 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), lane = lane_id(), ww = wave & 3;
+  const bool dy = wave >= 4;  // whose columns this wave loads: 32 of a stage's rows
+  const int64_t KB = (int64_t)p.K * 2, NB = (int64_t)p.N * 2, own_bytes = dy ? NB : KB;
+  const int ntk = (p.K + 63) / 64, ntn = (p.N + 63) / 64, per = ntk * ntn;
+  const int64_t total = (int64_t)p.E * per;
+  struct Tile {
+    int e, kt, nt, cnt;
+    int64_t row0;
+  };
+  const auto find = [&](int64_t t) __attribute__((always_inline)) {
+    Tile x;
+    x.e = (int)(t / per);
+    const int in = (int)(t % per);
+    x.nt = in % ntn;
+    x.kt = in / ntn;
+    x.cnt = g_scalar(p.counts + x.e);
+    x.row0 = g_scalar(p.padded_offsets + x.e);
+    return x;
+  };
+  const auto stages = [&](const Tile& x) { return x.cnt > 0 ? (x.cnt + kGwFineStage - 1) / kGwFineStage : 1; };
+  const int64_t t0 = (blockIdx.x % 8) * (kGtGrid / 8) + blockIdx.x / 8;
+  if (t0 >= total) return;
+
+  Tile ld;
+  int64_t lt = t0;
+  int lks = 0, lnks = 0, l_expert = -1;
+  bool done = false;
+  uint64_t base[L];
+  const auto row = [&](int j) { return 8 * (4 * ww + j) + lane / 8; };  // of a stage's 128, of load instruction j
+  const auto load = [&](int slot) __attribute__((always_inline)) {
+    if (!done && lks == 0) {
+      ld = find(lt);
+      lnks = stages(ld);
+      if (kGather && ld.e != l_expert && ld.cnt > 0) {
+        g_wait_lds();
+        g_barrier();  // the tokens before have been read
+        for (int at = 64 * wave; at < ld.cnt; at += 64 * kGtWaves)
+          dma4(reinterpret_cast<const uint8_t*>(p.row_token + ld.row0 + (at + lane < ld.cnt ? at + lane : ld.cnt - 1)),
+               kGwFineTokens + 4 * at);
+        wait_vmcnt<0>();
+        g_barrier();
+        l_expert = ld.e;
+      }
+#pragma unroll
+      for (int j = 0; j < L; ++j) {
+        const int R = row(j), c = (lane & 7) ^ ((((R >> 1) & 1) | ((R >> 3) & 1) << 1) << 1);
+        const int last = (int)(own_bytes / 16) - 1 - (dy ? ld.nt : ld.kt) * 8;
+        base[j] = reinterpret_cast<uint64_t>(dy ? p.dy : p.x) + 128 * (uint64_t)(dy ? ld.nt : ld.kt) + 16 * (c < last ? c : last) +
+                  (kGather && !dy ? 0 : (uint64_t)(ld.row0 * own_bytes));
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < L; ++j) {
+      const int at = kGwFineStage * lks + row(j), r = at < ld.cnt ? at : ld.cnt - 1;  // behind the last row: that; cleared later
+      const uint32_t src = kGather && !dy ? lds_read<uint32_t>(kGwFineTokens + 4 * (r < 0 ? 0 : r)) : (uint32_t)r;
+      const uint64_t from = base[j] + (uint64_t)src * (uint64_t)(uint32_t)own_bytes;
+      dma16(ld.cnt > 0 ? reinterpret_cast<const uint8_t*>(from) : reinterpret_cast<const uint8_t*>(g_zeros),
+            slot * kGfSlot + (dy ? kGfSide : 0) + 1024 * (4 * ww + j));
+    }
+    if (done) return;
+    if (lks + 1 == lnks && lt + kGtGrid >= total) {
+      done = true;  // with nothing left the last stage is loaded again, and not used
+    } else if (++lks == lnks) {
+      lks = 0;
+      lt += kGtGrid;
+    }
+  };
+#pragma unroll 1
+  for (int i = 0; i < D - 1; ++i) load(i);
+
+  const int half = wave >> 2, wm = ww >> 1, wn = ww & 1, r = lane & 15, g = lane >> 4, jj = r >> 2;
+  const uint32_t across = (64 * half + 8 * g + jj) * 128 + (lane & 3) * 8, v = (jj >> 1) | (g & 1) << 1;
+  const uint32_t a_at = across + ((2 * wn) ^ v) * 32, b_at = kGfSide + across + ((2 * wm) ^ v) * 32;
+  const auto read = [&](uint32_t from) __attribute__((always_inline)) {
+    typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+    const u32x2 l = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(reinterpret_cast<lds_s16x4*>(from)));
+    const u32x2 h = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(reinterpret_cast<lds_s16x4*>(from + 4 * 128)));
+    return u32x4{l[0], l[1], h[0], h[1]};
+  };
+  int slot = 0;
+  for (int64_t t = t0; t < total; t += kGtGrid) {
+    const Tile cur = find(t);
+    const int nks = stages(cur);
+    f32x4 acc[2][2];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) acc[i / 2][i % 2][q] = 0.0f;
+    for (int ks = 0; ks < nks; ++ks) {
+      wait_vmcnt<(D - 2) * L>();
+      if (cur.cnt - kGwFineStage * ks < kGwFineStage) {
+#pragma unroll
+        for (int j = 0; j < L; ++j)
+          if (kGwFineStage * ks + row(j) >= cur.cnt)
+            lds_write16(slot * kGfSlot + (dy ? kGfSide : 0) + 1024 * (4 * ww + j) + 16 * lane, u32x4{0u, 0u, 0u, 0u});
+      }
+      g_wait_lds();
+      g_barrier();
+      u32x4 a[2][2], b[2][2];
+#pragma unroll
+      for (int st = 0; st < 2; ++st)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          a[st][i] = read(slot * kGfSlot + (a_at ^ (i * 32)) + st * 32 * 128);
+          b[st][i] = read(slot * kGfSlot + (b_at ^ (i * 32)) + st * 32 * 128);
+        }
+      load(slot == 0 ? D - 1 : slot - 1);
+#pragma unroll
+      for (int st = 0; st < 2; ++st)
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+          for (int f = 0; f < 2; ++f) acc[m][f] = T::product(a[st][f], b[st][m], acc[m][f]);
+      slot = slot + 1 == D ? 0 : slot + 1;
+    }
+    const uint32_t red = kGfRedAt + (ww * kWave + lane) * 16;
+    if (half == 1) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) lds_write16(red + i * 4 * kWave * 16, __builtin_bit_cast(u32x4, acc[i / 2][i % 2]));
+    }
+    g_wait_lds();
+    g_barrier();
+    if (half == 1 || (cur.cnt == 0 && p.accumulate)) continue;
+    const bool f32 = p.dw_dtype == MEGAMOE_DTYPE_F32, f16 = p.dw_dtype == MEGAMOE_DTYPE_F16;
+    const int64_t bytes = f32 ? 4 : 2;
+    const auto place = [&](int n, int k) __attribute__((always_inline)) {
+      return static_cast<uint8_t*>(p.dw) + (((int64_t)cur.e * p.N + n) * p.K + k) * bytes;
+    };
+    const int k0 = cur.kt * 64 + wn * 32;
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+      const int n0 = cur.nt * 64 + wm * 32 + 16 * m, n = n0 + r;
+      f32x4 z[2];
+#pragma unroll
+      for (int f = 0; f < 2; ++f) {
+        z[f] = acc[m][f] + __builtin_bit_cast(f32x4, lds_read16(red + (2 * m + f) * 4 * kWave * 16));
+        const int k = k0 + 16 * f + 4 * g;
+        if (p.accumulate && n < p.N && k < p.K) z[f] = gw_add(z[f], place(n, k), p.dw_dtype);
+      }
+      const auto put = [&](int n, int k, u32x4 v) __attribute__((always_inline)) {
+        if (n < p.N && k < p.K) *reinterpret_cast<u32x4*>(place(n, k)) = v;
+      };
+      if (f32) {
+        u32x4 lo = __builtin_bit_cast(u32x4, z[0]), hi = __builtin_bit_cast(u32x4, z[1]);
+        g_whole_lines(lo, hi);
+        put(n0 + (r & 7), k0 + 16 * (r >> 3) + 4 * g, lo);
+        put(n0 + 8 + (r & 7), k0 + 16 * (r >> 3) + 4 * g, hi);
+      } else {
+        put(n, k0 + 16 * (g & 1) + 8 * (g >> 1),
+            g_gather8(u32x2{g_pack2(z[0][0], z[0][1], f16), g_pack2(z[0][2], z[0][3], f16)},
+                      u32x2{g_pack2(z[1][0], z[1][1], f16), g_pack2(z[1][2], z[1][3], f16)}));
+      }
+    }
+  }
+  wait_vmcnt<0>();
+}
+
+// Whether the tiles of 64 x 64 take the call: the time of the fullest workgroup either way, from the counts.
+__device__ __forceinline__ bool gw_fine(const GroupedWgradArgs& p, bool gather) {
+  const int64_t per = (int64_t)((p.K + 255) / 256) * ((p.N + 255) / 256), perf = (int64_t)((p.K + 63) / 64) * ((p.N + 63) / 64);
+  int coarse = 0, fine = 0, most = 0;  // a tile of every expert, in tenths of a us; the largest count
+  for (int e = lane_id(); e < p.E; e += kWave) {
+    const int cnt = p.counts[e];
+    coarse += 14 * ((cnt + 63) / 64) + kGwTile;
+    fine += 5 * ((cnt + 127) / 128) + kGwFineTile;
+    most = most > cnt ? most : cnt;
+  }
+  const int64_t all = (int64_t)wave_sum_i32(coarse) * per, all_fine = (int64_t)wave_sum_i32(fine) * perf;
+  most = (int)wave_max_u32((uint32_t)most);
+  if (gather && most > kGwMaxTokens) return false;
+  const int64_t one = 14 * (int64_t)((most + 63) / 64) + kGwTile, one_fine = 5 * (int64_t)((most + 127) / 128) + kGwFineTile;
+  return (all_fine / kGtGrid > one_fine ? all_fine / kGtGrid : one_fine) < (all / kGtGrid > one ? all / kGtGrid : one);
+}
 
 template <int kDtype, bool kGather>
 __global__ __launch_bounds__(kGtThreads, 1) void gt_weights_kernel(GroupedWgradArgs p) {
+  if (gw_fine(p, kGather)) {
+    gw_fine_phase<kDtype, kGather>(p);
+    return;
+  }
   extern __shared__ __attribute__((aligned(16))) uint8_t s_gt[];
   typedef GType<kDtype> T;
   constexpr int MF = 4, NF = 8, L = 8;
@@ -1017,17 +1219,7 @@ __global__ __launch_bounds__(kGtThreads, 1) void gt_weights_kernel(GroupedWgradA
           for (int h = 0; h < 2; ++h) {
             const int k = k0 + 16 * (f + h) + 4 * g;
             if (n >= p.N || k >= p.K) continue;
-            if (f32) {
-              z[h] += *reinterpret_cast<const f32x4*>(out + at(n, k));
-            } else {
-              const u32x2 old = *reinterpret_cast<const u32x2*>(out + at(n, k));
-#pragma unroll
-              for (int q = 0; q < 4; ++q) {
-                const uint32_t bits = (old[q / 2] >> (16 * (q & 1))) & 0xFFFFu;
-                const uint16_t b16 = (uint16_t)bits;
-                z[h][q] += f16 ? (float)__builtin_bit_cast(_Float16, b16) : bf16_bits_to_f32(bits);
-              }
-            }
+            z[h] = gw_add(z[h], out + at(n, k), p.dw_dtype);
           }
         }
         if (f32) {
@@ -1350,7 +1542,7 @@ static hipError_t launch_gt_weights(const GroupedWgradArgs& a, hipStream_t strea
   static std::atomic<bool> done[kGtDevices];
   const hipError_t err = gt_allow_lds(gt_weights_kernel<kDtype, kGather>, done);
   if (err != hipSuccess) return err;
-  hipLaunchKernelGGL((gt_weights_kernel<kDtype, kGather>), dim3(kGtGrid), dim3(kGtThreads), kGwLds, stream, a);
+  hipLaunchKernelGGL((gt_weights_kernel<kDtype, kGather>), dim3(kGtGrid), dim3(kGtThreads), kGtLds, stream, a);
   return hipGetLastError();
 }
 
