@@ -239,7 +239,8 @@ struct GtShape {
   // LDS behind the slots: the tokens of two tiles' rows, the scales of kBufs tiles
   static constexpr int kRowsAt = D * kSlot, kScalesAt = kRowsAt + 2 * 64 * WB * 4;
   static constexpr int kScaleBuf = 4 * (kGtCols + 64 * WB);
-  static_assert(kScalesAt + kBufs * kScaleBuf <= kGtLists, "the LDS layout fits");
+  static constexpr int kTilesAt = kScalesAt + kBufs * kScaleBuf;  // and what the epilogue needs of as many tiles
+  static_assert(kTilesAt + kBufs * 16 <= kGtLists, "the LDS layout fits");
 };
 
 struct GtTile {
@@ -248,7 +249,7 @@ struct GtTile {
 };
 
 template <int kOp, int kDtype, int WB, typename Find>
-__device__ __forceinline__ void gt_phase(const GroupedArgs& p, int64_t t0, int64_t total, const Find& find) {
+__device__ __forceinline__ void gt_phase(const GroupedArgs& p, int t0, int total, const Find& find) {
   typedef GtShape<WB> S;
   typedef GType<kDtype> T;
   constexpr bool kL1 = kOp == kGtGateUp, kAcross = kOp == kGtAcross, kI8 = kDtype == kOperandI8;
@@ -262,17 +263,16 @@ __device__ __forceinline__ void gt_phase(const GroupedArgs& p, int64_t t0, int64
   const int piece = (lane & 7) ^ (lane >> 4);  // of 8 rows of an even load instruction (odd: ^ 4)
 
   // ---- loads -------------------------------------------------------------------------------------
-  GtTile ld;
-  int64_t lt = t0;
+  GtTile ld, nx = find(t0);  // of the loads, and the next
+  int lt = t0;
   int lks = 0, lseq = 0;
   const uint8_t* w_at = nullptr;                   // of the stage to request
   uint32_t w_off[kAcross ? 2 : 4];                 // across: of even and odd load instructions
   uint64_t a_at[WB];
-  const auto fetch_rows = [&](int64_t t, int buf) __attribute__((always_inline)) {  // tokens of tile t's rows
-    if (!kAcross && p.row_token != nullptr && wave < WB && t < total) {
-      const GtTile x = find(t);
+  const auto fetch_rows = [&](int buf) __attribute__((always_inline)) {  // tokens of the next tile's rows
+    if (!kAcross && p.row_token != nullptr && wave < WB) {
       const int R = 64 * wave + g_here(lane);
-      dma4(reinterpret_cast<const uint8_t*>(p.row_token + x.row0 + (R < x.left ? R : x.left - 1)),
+      dma4(reinterpret_cast<const uint8_t*>(p.row_token + nx.row0 + (R < nx.left ? R : nx.left - 1)),
            S::kRowsAt + 4 * (64 * WB * buf + 64 * wave));
     }
   };
@@ -294,7 +294,10 @@ __device__ __forceinline__ void gt_phase(const GroupedArgs& p, int64_t t0, int64
   };
   const auto enter = [&]() __attribute__((always_inline)) {  // tile lt
     const int ln = g_here(lane);
-    ld = find(lt);
+    ld = nx;
+    if (wave == 0 && lane == 0)
+      lds_write16(S::kTilesAt + 16 * (lseq % S::kBufs),
+                  u32x4{(uint32_t)ld.nt, (uint32_t)ld.left, (uint32_t)ld.row0, (uint32_t)(ld.row0 >> 32)});
 #pragma unroll
     for (int i = 0; i < WB; ++i)
       a_at[i] = reinterpret_cast<uint64_t>(p.a) + (uint64_t)a_row(8 * (WB * wave + i) + ln / 8) * (uint64_t)(uint32_t)RB +
@@ -323,7 +326,10 @@ __device__ __forceinline__ void gt_phase(const GroupedArgs& p, int64_t t0, int64
       else if (wave - 4 < WB)
         dma4(reinterpret_cast<const uint8_t*>(p.a_scales + a_row(R)), to + 4 * kGtCols + 256 * (wave - 4));
     }
-    fetch_rows(lt + kGtGrid, (lseq + 1) & 1);
+    if (lt + kGtGrid < total) {  // (its table entries are on their way while the tile's stages are multiplied)
+      nx = find(lt + kGtGrid);
+      fetch_rows((lseq + 1) & 1);
+    }
     ++lseq;
   };
   bool done = false;  // with nothing left the last stage is loaded again, and not used
@@ -403,7 +409,7 @@ __device__ __forceinline__ void gt_phase(const GroupedArgs& p, int64_t t0, int64
 
   g_wait_lds();
   g_barrier();  // the phase before is done with LDS
-  fetch_rows(lt, 0);
+  fetch_rows(0);
   wait_vmcnt<0>();
   g_barrier();
   int issued = 0;
@@ -431,7 +437,7 @@ __device__ __forceinline__ void gt_phase(const GroupedArgs& p, int64_t t0, int64
   for (int i = 0; i < MF + NF; ++i) read_one(0, i);
 
   int slot = 0, seq = 0;
-  for (int64_t t = t0; t < total; t += kGtGrid) {
+  for (int t = t0; t < total; t += kGtGrid) {
     typename T::acc acc[MF][NF];
 #pragma unroll
     for (int m = 0; m < MF; ++m)
@@ -460,7 +466,15 @@ __device__ __forceinline__ void gt_phase(const GroupedArgs& p, int64_t t0, int64
     }
 
     // Output: row 16 m + r of the wave, columns 16 f + 4 g ..+3 of block f.
-    const GtTile cur = find(t);
+    const u32x4 info = lds_read16(S::kTilesAt + 16 * (seq % S::kBufs));  // of the tile, as its loads left it
+    struct {
+      int nt, left;
+      int64_t row0;
+    } cur;
+    cur.nt = __builtin_amdgcn_readfirstlane((int)info[0]);
+    cur.left = __builtin_amdgcn_readfirstlane((int)info[1]);
+    cur.row0 = (int64_t)((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)info[2]) |
+                         (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)info[3]) << 32);
     const uint32_t sc = S::kScalesAt + (seq % S::kBufs) * S::kScaleBuf;
     ++seq;
     const bool f16 = p.out_dtype == MEGAMOE_DTYPE_F16;
@@ -536,7 +550,7 @@ constexpr int kGfScaleBuf = 4 * (64 + 64);
 static_assert(kGfScalesAt + (kGfD + 1) * kGfScaleBuf <= kGtLists, "the LDS layout fits");
 
 template <int kOp, int kDtype, typename Find>
-__device__ __forceinline__ void gt_fine_phase(const GroupedArgs& p, int64_t t0, int64_t total, const Find& find) {
+__device__ __forceinline__ void gt_fine_phase(const GroupedArgs& p, int t0, int total, const Find& find) {
   typedef GType<kDtype> T;
   constexpr bool kL1 = kOp == kGtGateUp, kAcross = kOp == kGtAcross, kI8 = kDtype == kOperandI8;
   constexpr int cols = kL1 ? 32 : 64, D = kGfD, L = 4;
@@ -549,17 +563,14 @@ __device__ __forceinline__ void gt_fine_phase(const GroupedArgs& p, int64_t t0, 
   const auto piece = [&](int j) { return (lane & 15) ^ (4 * j + (lane >> 4)); };  // of load instruction j: 4 rows by 16
 
   // ---- loads -------------------------------------------------------------------------------------
-  GtTile ld;
-  int64_t lt = t0;
+  GtTile ld, nx = find(t0);
+  int lt = t0;
   int lks = 0, lseq = 0;
   bool done = false;
   uint64_t at[L];
-  const auto fetch_rows = [&](int64_t t, int buf) __attribute__((always_inline)) {
-    if (!kAcross && p.row_token != nullptr && wave == 0 && t < total) {
-      const GtTile x = find(t);
-      dma4(reinterpret_cast<const uint8_t*>(p.row_token + x.row0 + (lane < x.left ? lane : x.left - 1)),
-           kGfRowsAt + 4 * 64 * buf);
-    }
+  const auto fetch_rows = [&](int buf) __attribute__((always_inline)) {
+    if (!kAcross && p.row_token != nullptr && wave == 0)
+      dma4(reinterpret_cast<const uint8_t*>(p.row_token + nx.row0 + (lane < nx.left ? lane : nx.left - 1)), kGfRowsAt + 4 * 64 * buf);
   };
   const auto a_row = [&](int R) __attribute__((always_inline)) -> uint32_t {
     if (!kAcross && p.row_token != nullptr) return lds_read<uint32_t>(kGfRowsAt + 4 * (64 * (lseq & 1) + R));
@@ -571,7 +582,7 @@ __device__ __forceinline__ void gt_fine_phase(const GroupedArgs& p, int64_t t0, 
     return (int64_t)ld.e * (kL1 ? 2 : 1) * p.N + (c < p.N ? c : p.N - 1) + (kL1 && (R & 16) ? p.N : 0);
   };
   const auto enter = [&]() __attribute__((always_inline)) {
-    ld = find(lt);
+    ld = nx;
 #pragma unroll
     for (int j = 0; j < L; ++j) {
       const int R = 16 * ww + 4 * j + lane / 16;
@@ -591,7 +602,10 @@ __device__ __forceinline__ void gt_fine_phase(const GroupedArgs& p, int64_t t0, 
       if (wave == 1) dma4(reinterpret_cast<const uint8_t*>(p.w_scales + w_row(lane)), to);
       if (wave == 2) dma4(reinterpret_cast<const uint8_t*>(p.a_scales + a_row(lane)), to + 256);
     }
-    fetch_rows(lt + kGtGrid, (lseq + 1) & 1);
+    if (lt + kGtGrid < total) {
+      nx = find(lt + kGtGrid);
+      fetch_rows((lseq + 1) & 1);
+    }
     ++lseq;
   };
   const bool ragged = (RB & (kGfStage - 1)) != 0;
@@ -636,7 +650,7 @@ __device__ __forceinline__ void gt_fine_phase(const GroupedArgs& p, int64_t t0, 
 
   g_wait_lds();
   g_barrier();  // the phase before is done with LDS
-  fetch_rows(lt, 0);
+  fetch_rows(0);
   wait_vmcnt<0>();
   g_barrier();
 #pragma unroll 1
@@ -649,7 +663,7 @@ __device__ __forceinline__ void gt_fine_phase(const GroupedArgs& p, int64_t t0, 
   const uint32_t a_at = kAcross ? (64 * half + 8 * g + jj) * 128 + (((2 * wn) ^ ((jj >> 1) | (g & 1) << 1)) * 32) + (lane & 3) * 8
                                 : wn * 32 * kGfStage + along;
   int slot = 0, seq = 0;
-  for (int64_t t = t0; t < total; t += kGtGrid) {
+  for (int t = t0; t < total; t += kGtGrid) {
     typename T::acc acc[2][2];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
@@ -789,44 +803,45 @@ __global__ __launch_bounds__(kGtThreads, 1) void gt_kernel(GroupedArgs p) {
   }
   __syncthreads();
   const bool fine = __builtin_amdgcn_readfirstlane(s_n[0]) < 0;
-  const int64_t total4 = (int64_t)__builtin_amdgcn_readfirstlane(pref[E]) * (fine ? ntf : ntn);
-  const int64_t total2 = (int64_t)__builtin_amdgcn_readfirstlane(s_n[0]) * ntn;
-  const int64_t total1 = (int64_t)__builtin_amdgcn_readfirstlane(s_n[1]) * ntn;
+  const int total4 = __builtin_amdgcn_readfirstlane(pref[E]) * (fine ? ntf : ntn);
+  const int total2 = __builtin_amdgcn_readfirstlane(s_n[0]) * ntn;
+  const int total1 = __builtin_amdgcn_readfirstlane(s_n[1]) * ntn;
   const auto count = [&](int e) { return p.counts ? g_scalar(p.counts + e) : (int)p.M; };
   const auto offset = [&](int e) { return (int64_t)(p.padded_offsets ? g_scalar(p.padded_offsets + e) : 0); };
+  // (Tile numbers fit 32 bits: a tile has 4096 outputs and more, and 2^31 of them would not fit the GPU.)
   // Tile t of those of 256 (or 64) rows: its expert by two steps of 64 comparisons (at most 1024 experts).
-  const auto find_tile = [&](int64_t t, int rows, int ntn) __attribute__((always_inline)) {
+  const auto find_tile = [&](int t, int rows, int ntn) __attribute__((always_inline)) {
     const int step = (E + kWave - 1) / kWave;
     const int at = lane * step;
-    const int chunk = __popcll(__ballot(at < E && (int64_t)pref[at < E ? at : 0] * ntn <= t)) - 1;
+    const int chunk = __popcll(__ballot(at < E && pref[at < E ? at : 0] * ntn <= t)) - 1;
     const int at2 = chunk * step + lane;
     const int e = __builtin_amdgcn_readfirstlane(
-        chunk * step - 1 + __popcll(__ballot(lane < step && at2 < E && (int64_t)pref[at2 < E ? at2 : 0] * ntn <= t)));
+        chunk * step - 1 + __popcll(__ballot(lane < step && at2 < E && pref[at2 < E ? at2 : 0] * ntn <= t)));
     const int first = __builtin_amdgcn_readfirstlane(pref[e]);
     const int mts = __builtin_amdgcn_readfirstlane(pref[e + 1]) - first;
-    const int64_t local = t - (int64_t)first * ntn;
-    const int band = (int)(local / ((int64_t)kGtBand * ntn)), in = (int)(local % ((int64_t)kGtBand * ntn));
+    const int local = t - first * ntn;
+    const int band = local / (kGtBand * ntn), in = local % (kGtBand * ntn);
     const int width = min(kGtBand, mts - band * kGtBand);
     const int mt = band * kGtBand + in % width;
     return GtTile{e, in / width, count(e) - mt * rows, offset(e) + (int64_t)mt * rows};
   };
-  const auto find4 = [&](int64_t t) __attribute__((always_inline)) { return find_tile(t, kGtRows, ntn); };
-  const auto find_last = [&](const uint16_t* list, int64_t t) __attribute__((always_inline)) {
+  const auto find4 = [&](int t) __attribute__((always_inline)) { return find_tile(t, kGtRows, ntn); };
+  const auto find_last = [&](const uint16_t* list, int t) __attribute__((always_inline)) {
     const int e = __builtin_amdgcn_readfirstlane((int)list[t / ntn]);
     const int cnt = count(e), mt = cnt / kGtRows;
-    return GtTile{e, (int)(t % ntn), cnt - mt * kGtRows, offset(e) + (int64_t)mt * kGtRows};
+    return GtTile{e, t % ntn, cnt - mt * kGtRows, offset(e) + (int64_t)mt * kGtRows};
   };
   // XCD b % 8 takes 32 tiles in a row of every 256: they share rows and weights in its L2.  The lists follow each
   // other, so that a workgroup that has one tile more of one list has one less of the next.
-  const int64_t wg = (blockIdx.x % 8) * (kGtGrid / 8) + blockIdx.x / 8;
-  const auto first = [&](int64_t before) { return (wg - before % kGtGrid + kGtGrid) % kGtGrid; };
+  const int wg = (blockIdx.x % 8) * (kGtGrid / 8) + blockIdx.x / 8;
+  const auto first = [&](int before) { return (wg - before % kGtGrid + kGtGrid) % kGtGrid; };
   if (fine) {
-    gt_fine_phase<kOp, kDtype>(p, wg, total4, [&](int64_t t) __attribute__((always_inline)) { return find_tile(t, 64, ntf); });
+    gt_fine_phase<kOp, kDtype>(p, wg, total4, [&](int t) __attribute__((always_inline)) { return find_tile(t, 64, ntf); });
     return;
   }
   gt_phase<kOp, kDtype, 4>(p, wg, total4, find4);
-  gt_phase<kOp, kDtype, 2>(p, first(total4), total2, [&](int64_t t) { return find_last(list2, t); });
-  gt_phase<kOp, kDtype, 1>(p, first(total4 + total2), total1, [&](int64_t t) { return find_last(list1, t); });
+  gt_phase<kOp, kDtype, 2>(p, first(total4), total2, [&](int t) { return find_last(list2, t); });
+  gt_phase<kOp, kDtype, 1>(p, first(total4 + total2), total1, [&](int t) { return find_last(list1, t); });
 }
 
 // ============================================================================================
