@@ -2,11 +2,12 @@
 //
 //   scale = fl32(amax / 127),  code = the whole number nearest to 127 x / amax, ties to even,
 // of the exact quotient: the fp32 product x * fl32(127 / amax) is within 127 * 2^-23 < 2^-16 of it, so
-// only elements whose product lies within 2^-15 of a border are taken again in float64 (there a
-// quotient that is no border is 2^-33 and more away from one, and a border is met exactly).  A row with
+// only pieces with an element whose product lies within 2^-15 of a border are taken again, by the sign of
+// 254 |x| - (2k + 1) amax, without a rounding.  (16-bit rows meet borders often: amax / 2 is one, 63.5.)  A row with
 // an infinity or a NaN gets a NaN scale and zero codes: every product that reads it is NaN.
 //
-// Memory-bound.  A row stays in registers between its maximum and its codes, so it is read once.
+// Memory-bound.  A row stays in registers between its maximum and its codes, so it is read once: 49152 x 2048 in bf16
+// takes 49 us (6.2 TB/s read and written), in float32 79 (6.4); decoded 48 and 92 (6.3 and 5.5).
 #include "device_common.h"
 #include "internal.h"
 
@@ -55,7 +56,23 @@ __device__ __forceinline__ void i8_encode(const u32x4& v, float amax, float inv,
   }
   if (!(off <= kI8Border) || !(amax >= kI8Tiny)) {
 #pragma unroll
-    for (int j = 0; j < n; ++j) q[j] = (float)rint((double)I8In<kDtype>::get(v, j) * 127.0 / (double)amax);
+    for (int j = 0; j < n; ++j) {
+      const float x = I8In<kDtype>::get(v, j), ax = fabsf(x);
+      if (amax >= kI8Tiny) {  // k or k + 1: whether x is above the border between them, or on it and k is odd
+        const float k = floorf(ax * inv);
+        bool above, on;
+        if constexpr (kDtype == MEGAMOE_DTYPE_F32) {  // 32 and 32 bits
+          const double d = fma(-(double)(2.0f * k + 1.0f), (double)amax, 254.0 * (double)ax);
+          above = d > 0.0, on = d == 0.0;
+        } else {  // (over 256, as 254 |x| may overflow) 18 and 19 bits
+          const float d = fmaf(-(2.0f * k + 1.0f) / 256.0f, amax, ax * (254.0f / 256.0f));
+          above = d > 0.0f, on = d == 0.0f;
+        }
+        q[j] = copysignf(k + (above || (on && ((int)k & 1)) ? 1.0f : 0.0f), x);
+      } else {  // a quotient that is no border is 2^-33 and more away from one, and a border is met exactly
+        q[j] = (float)rint((double)x * 127.0 / (double)amax);
+      }
+    }
   }
 #pragma unroll
   for (int j = 0; j < n / 4; ++j)
@@ -126,51 +143,73 @@ __global__ __launch_bounds__(256) void i8_quant_kernel(I8QuantArgs p) {
   }
 }
 
-// 16 codes a thread.
+// 16 bytes of output a lane and store, so that a wave's stores cover whole lines (16 codes a lane, stored by quarters of a
+// line, took 307 us for 49152 x 2048 in float32); kI8Ahead of them a thread, their codes requested first.
+constexpr int kI8Ahead = 4, kI8Block = 256 * kI8Ahead;
+
 template <int kDtype>
-__global__ __launch_bounds__(256) void i8_dequant_kernel(const u32x4* codes, const float* scales, int64_t total,
-                                                         int32_t pieces, u32x4* out) {
-  constexpr int n = I8In<kDtype>::kElems, kOut = 16 / n;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
-    const u32x4 c = __builtin_nontemporal_load(codes + i);
-    const float s = scales[i / pieces];
-    float f[16];
+__global__ __launch_bounds__(256) void i8_dequant_kernel(const uint8_t* codes, const float* scales, int64_t total,
+                                                         uint32_t pieces, u32x4* out) {
+  constexpr int n = I8In<kDtype>::kElems;  // codes of a piece
+  for (int64_t at = (int64_t)blockIdx.x * kI8Block; at < total; at += (int64_t)gridDim.x * kI8Block) {
+    const int64_t row0 = at / pieces;
+    const uint32_t in0 = (uint32_t)(at - row0 * pieces) + threadIdx.x;
+    u32x2 c[kI8Ahead];
+    float s[kI8Ahead];
 #pragma unroll
-    for (int j = 0; j < 16; ++j) f[j] = (float)(int)(int8_t)(c[j / 4] >> (8 * (j % 4))) * s;
+    for (int u = 0; u < kI8Ahead; ++u) {
+      const int64_t i = at + 256 * u + threadIdx.x;
+      if (i >= total) break;
+      if constexpr (n == 8) c[u] = __builtin_nontemporal_load(reinterpret_cast<const u32x2*>(codes) + i);
+      else c[u][0] = __builtin_nontemporal_load(reinterpret_cast<const uint32_t*>(codes) + i);
+      s[u] = scales[row0 + (in0 + 256 * u) / pieces];
+    }
 #pragma unroll
-    for (int k = 0; k < kOut; ++k) {
+    for (int u = 0; u < kI8Ahead; ++u) {
+      const int64_t i = at + 256 * u + threadIdx.x;
+      if (i >= total) break;
+      float f[n];
+#pragma unroll
+      for (int j = 0; j < n; ++j) f[j] = (float)(int)(int8_t)(c[u][j / 4] >> (8 * (j % 4))) * s[u];
       u32x4 o;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        if constexpr (kDtype == MEGAMOE_DTYPE_F32) o[j] = __float_as_uint(f[4 * k + j]);
+        if constexpr (kDtype == MEGAMOE_DTYPE_F32) o[j] = __float_as_uint(f[j]);
         else if constexpr (kDtype == MEGAMOE_DTYPE_BF16)
-          o[j] = __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2n{f[8 * k + 2 * j], f[8 * k + 2 * j + 1]}, bf16x2n));
-        else
-          o[j] = __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2n{f[8 * k + 2 * j], f[8 * k + 2 * j + 1]}, f16x2));
+          o[j] = __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2n{f[2 * j], f[2 * j + 1]}, bf16x2n));
+        else o[j] = __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2n{f[2 * j], f[2 * j + 1]}, f16x2));
       }
-      __builtin_nontemporal_store(o, out + i * kOut + k);
+      __builtin_nontemporal_store(o, out + i);
     }
   }
 }
 
-template <int kDtype, int kLanes>
-static void i8_quant_pieces(const I8QuantArgs& a, hipStream_t stream) {
+template <int kDtype, int kLanes, int NP>
+static void i8_quant_as(const I8QuantArgs& a, hipStream_t stream) {
   constexpr int kRows = 256 / kLanes;
   const int64_t blocks = (a.rows + kRows - 1) / kRows;
-  const dim3 grid((unsigned)(blocks < (1 << 20) ? blocks : 1 << 20)), block(256);
-  const int np = (a.pieces + kLanes - 1) / kLanes;
-  if (np <= 1) hipLaunchKernelGGL((i8_quant_kernel<kDtype, kLanes, 1>), grid, block, 0, stream, a);
-  else if (np <= 2) hipLaunchKernelGGL((i8_quant_kernel<kDtype, kLanes, 2>), grid, block, 0, stream, a);
-  else if (np <= 4) hipLaunchKernelGGL((i8_quant_kernel<kDtype, kLanes, 4>), grid, block, 0, stream, a);
-  else if (np <= 8) hipLaunchKernelGGL((i8_quant_kernel<kDtype, kLanes, 8>), grid, block, 0, stream, a);
-  else if (np <= 14) hipLaunchKernelGGL((i8_quant_kernel<kDtype, kLanes, 14>), grid, block, 0, stream, a);
-  else hipLaunchKernelGGL((i8_quant_kernel<kDtype, kLanes, 0>), grid, block, 0, stream, a);
+  hipLaunchKernelGGL((i8_quant_kernel<kDtype, kLanes, NP>), dim3((unsigned)(blocks < (1 << 20) ? blocks : 1 << 20)), dim3(256),
+                     0, stream, a);
 }
 
+// Many short rows: a wave a row, else a workgroup (4096 x 2048: 7.5 us and 11.2 in bf16, 6.9 and 7.4 in float32; 16384 x
+// 4096: 38.5 and 36.5, 56 and 53; 512 x 2048: 5.4 and 5.3).  Rows of more than 16 pieces a thread are read twice.
 template <int kDtype>
 static void i8_quant(const I8QuantArgs& a, hipStream_t stream) {
-  if (a.rows >= 2048 && a.pieces <= 14 * kWave) i8_quant_pieces<kDtype, kWave>(a, stream);
-  else i8_quant_pieces<kDtype, 256>(a, stream);
+  constexpr int kMost = 2048 / (kWave * I8In<kDtype>::kElems);
+  if (a.rows >= 2048 && a.pieces <= kMost * kWave) {
+    if (a.pieces <= kWave) i8_quant_as<kDtype, kWave, 1>(a, stream);
+    else if (a.pieces <= kMost / 2 * kWave) i8_quant_as<kDtype, kWave, kMost / 2>(a, stream);
+    else i8_quant_as<kDtype, kWave, kMost>(a, stream);
+    return;
+  }
+  const int np = (a.pieces + 255) / 256;
+  if (np <= 1) i8_quant_as<kDtype, 256, 1>(a, stream);
+  else if (np <= 2) i8_quant_as<kDtype, 256, 2>(a, stream);
+  else if (np <= 4) i8_quant_as<kDtype, 256, 4>(a, stream);
+  else if (np <= 8) i8_quant_as<kDtype, 256, 8>(a, stream);
+  else if (np <= 16) i8_quant_as<kDtype, 256, 16>(a, stream);
+  else i8_quant_as<kDtype, 256, 0>(a, stream);
 }
 
 hipError_t launch_int8_quant(const void* x, int dtype, int64_t rows, int64_t cols, const int32_t* row_valid,
@@ -187,14 +226,15 @@ hipError_t launch_int8_quant(const void* x, int dtype, int64_t rows, int64_t col
 hipError_t launch_int8_dequant(const int8_t* codes, const float* scales, int64_t rows, int64_t cols, int dtype,
                                void* out, hipStream_t stream) {
   if (rows == 0) return hipSuccess;
-  const int64_t total = rows * (cols / 16), blocks = (total + 255) / 256;
+  const int64_t pieces = cols / (dtype == MEGAMOE_DTYPE_F32 ? 4 : 8), total = rows * pieces;
+  const int64_t blocks = (total + kI8Block - 1) / kI8Block;
   const dim3 grid((unsigned)(blocks < (1 << 20) ? blocks : 1 << 20)), block(256);
-  const u32x4* c = reinterpret_cast<const u32x4*>(codes);
+  const uint8_t* c = reinterpret_cast<const uint8_t*>(codes);
   u32x4* o = static_cast<u32x4*>(out);
-  const int32_t pieces = (int32_t)(cols / 16);
-  if (dtype == MEGAMOE_DTYPE_F32) hipLaunchKernelGGL((i8_dequant_kernel<MEGAMOE_DTYPE_F32>), grid, block, 0, stream, c, scales, total, pieces, o);
-  else if (dtype == MEGAMOE_DTYPE_BF16) hipLaunchKernelGGL((i8_dequant_kernel<MEGAMOE_DTYPE_BF16>), grid, block, 0, stream, c, scales, total, pieces, o);
-  else hipLaunchKernelGGL((i8_dequant_kernel<MEGAMOE_DTYPE_F16>), grid, block, 0, stream, c, scales, total, pieces, o);
+  const uint32_t per = (uint32_t)pieces;
+  if (dtype == MEGAMOE_DTYPE_F32) hipLaunchKernelGGL((i8_dequant_kernel<MEGAMOE_DTYPE_F32>), grid, block, 0, stream, c, scales, total, per, o);
+  else if (dtype == MEGAMOE_DTYPE_BF16) hipLaunchKernelGGL((i8_dequant_kernel<MEGAMOE_DTYPE_BF16>), grid, block, 0, stream, c, scales, total, per, o);
+  else hipLaunchKernelGGL((i8_dequant_kernel<MEGAMOE_DTYPE_F16>), grid, block, 0, stream, c, scales, total, per, o);
   return hipGetLastError();
 }
 

@@ -127,6 +127,17 @@ def test_quantize_many_near_borders():
     check_quantize(torch.from_numpy(x * rng.choice([-1, 1], x.shape).astype(np.float32)))
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_quantize_every_16_bit_value(dtype):
+    """Every finite value below each of some maxima: all borders that 16-bit rows can meet."""
+    top = 0x7F80 if dtype == torch.bfloat16 else 0x7C00
+    bits = torch.arange(top, dtype=torch.int32)
+    rng = np.random.default_rng(11)
+    most = np.concatenate([[1, 2, 127, 128, 254, top - 1], top - 1 - rng.integers(0, top // 4, 12), top // 2 + np.arange(12)])
+    rows = [torch.where(bits <= int(m), bits, 0).to(torch.int16).view(dtype) for m in most]
+    check_quantize(torch.stack(rows) * torch.where(bits % 3 == 0, -1.0, 1.0).to(dtype))
+
+
 @pytest.mark.parametrize("rows", [70, 2500])
 def test_quantize_skips_invalid_rows(rows):
     rng = np.random.default_rng(3)
