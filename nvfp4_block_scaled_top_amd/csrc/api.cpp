@@ -764,7 +764,7 @@ static int32_t grouped_gemm(const GroupedArgs& a, bool l1, int64_t rows, int32_t
     return MEGAMOE_ERR_SHAPE;
   // int8: sums of K products of at most 2^14 stay below 2^31
   if (i8 && (a.K % 16 != 0 || a.K >= (1 << 17))) return MEGAMOE_ERR_SHAPE;
-  // row offsets are 32-bit counts of 16 bytes
+  // (as the MXFP4 products)
   if (rows * ((int64_t)a.K * (i8 ? 1 : 2)) >= (int64_t)1 << 36) return MEGAMOE_ERR_SHAPE;
   if (!a.w || (i8 && !a.w_scales)) return MEGAMOE_ERR_NULL;
   if (rows > 0 && (!a.a || !a.out || (i8 && !a.a_scales))) return MEGAMOE_ERR_NULL;

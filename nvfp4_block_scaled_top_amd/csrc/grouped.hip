@@ -84,10 +84,11 @@ __device__ __forceinline__ int g_here(int v) {
 }
 
 // Operand types: the accumulator and the 16x16 matrix instruction over 64 bytes of K (16x16x32 or 16x16x64).  Inline
-// assembly keeps the accumulators in accumulation registers, all 256 of them in the largest tile: left to itself the
-// compiler moves them to and fro (408 moves beside 64 products).  What it does not know of these instructions is
-// kept by hand: an accumulator is met again after at least 7 others, and g_settle stands between the products
-// and any other write or read of it.
+// assembly keeps the accumulators in accumulation registers, 128 of them in the largest tile: left to itself the
+// compiler moves them to and fro (408 moves beside 64 products, when there were 256).  What it does not know of these
+// instructions is kept by hand: an accumulator is met again after at least 7 others, and g_settle stands between the
+// products and any other write or read of it.  From registers the instructions reach 2025 TFLOP/s (bf16) and 4121 TOPS
+// (int8) on random numbers, 2468 and 4926 on zeros: the clock falls with the power.
 template <int kDtype>
 struct GType {
   typedef f32x4 acc;
@@ -118,10 +119,8 @@ struct GType<kOperandI8> {
 // instruction, and is read by the next one 2 after a write.
 template <typename A, int n>
 __device__ __forceinline__ void g_settle(A (&c)[n]) {
-  static_assert(n == 2 || n == 4 || n == 8, "fragments of a wave");
-  if constexpr (n == 2)
-    asm volatile("s_nop 15\n\ts_nop 7" : "+a"(c[0]), "+a"(c[1]));
-  else if constexpr (n == 8)
+  static_assert(n == 4 || n == 8, "fragments of a wave");
+  if constexpr (n == 8)
     asm volatile("s_nop 15\n\ts_nop 7" : "+a"(c[0]), "+a"(c[1]), "+a"(c[2]), "+a"(c[3]), "+a"(c[4]), "+a"(c[5]), "+a"(c[6]), "+a"(c[7]));
   else
     asm volatile("s_nop 15\n\ts_nop 7" : "+a"(c[0]), "+a"(c[1]), "+a"(c[2]), "+a"(c[3]));
@@ -169,9 +168,9 @@ __device__ __forceinline__ u32x4 g_gather8(u32x2 lo, u32x2 hi) {
 }
 
 // A step: the products of one 64-byte piece of K, with the next step's operands read from LDS (read(i)) and a
-// stage's loads requested (load(j)) between them, each behind a product of its own: a wave has its SIMD to itself and
-// issues in order, so what stands between two products is free only within the first one's 16 cycles.  Reads and
-// loads are out after three quarters of the products.
+// stage's loads requested (load(j)) between them, each behind a product of its own: a wave issues in order, and a load
+// holds it for some 70 cycles, which only the SIMD's other wave's products fill.  Reads and loads are out after three
+// quarters of the products (half, or all of them: the same times).
 template <int V>
 struct GTag {
   static constexpr int value = V;
@@ -219,7 +218,7 @@ __device__ __forceinline__ void g_whole_lines(u32x4& lo, u32x4& hi) {
 
 // ============================================================================================
 // rows, gate+up and across: 256 weight rows x BM token rows a tile, BM = 64 WB = 256, or 128 or 64 for an
-// expert's last rows when they fit; one persistent workgroup of 4 waves a CU takes all tiles of 256 rows, then
+// expert's last rows when they fit; one persistent workgroup of 8 waves a CU takes all tiles of 256 rows, then
 // those of 128, then those of 64.
 //
 // A stage is 128 bytes of K of every row.  Stages go from global memory straight into a ring of LDS slots (2 of
@@ -227,6 +226,12 @@ __device__ __forceinline__ void g_whole_lines(u32x4& lo, u32x4& hi) {
 // operands are read from LDS while the step before is multiplied.  Between the two steps of stage s a wave has
 // read all of s: it waits for its loads of stage s + 1, and one barrier makes everyone's visible and says that
 // s's slot is free, into which the second step requests the stage after the ring's last.
+//
+// Many rows: matrix instructions, memory's latency and the power.  int8 16384 x 4096 x 7168 takes 350 us (2750 TOPS; 275
+// on zeros), bf16 16384 x 7168 x 4096 727 (1320 TFLOP/s), 16384 x 2048 x 7168 362, 24 experts of 1024 rows across, 7168 to 4096, 1150.  Few rows: the weights' bytes, 48
+// experts of 40 rows, 7168 to 4096, 404 us (7.1 TB/s).  4 waves of 128 x 128 read a third less from LDS: 657 us for the bf16 product,
+// the same for int8, 942 where 8 waves take 789 for the weights' gradient.  Operands staged through registers: 379 where these
+// loads took 358.  Touching the next stages in the L2 first: 3 to 10% slower.
 // ============================================================================================
 template <int WB>
 struct GtShape {
@@ -746,6 +751,9 @@ __device__ __forceinline__ void gt_fine_phase(const GroupedArgs& p, int t0, int 
 }
 
 // Whether the tiles of 64 take the call: the time of the fullest workgroup either way, of tiles of nks stages.
+// (Large and small tiles, us: int8 256 x 4096 x 7168 71 and 16, 1024 rows 86 and 51, 2048 rows 88 and 99; bf16 16 experts of 288 rows, 3640 to
+// 176, 118 and 19; 64 of 94 rows, 2048 to 7168, 402 and 534; 48 of 40 rows, 7168 to 4096, 404 and 479; 8 of 32, 512 to 1024, 10.7
+// and 7.2; across, 24 of 100 rows, 2048 to 1024, 39 and 28.)
 __device__ __forceinline__ bool gt_fine(int64_t n4, int64_t n2, int64_t n1, int64_t fine, int nks) {
   const int64_t t4 = nks * kGtNs4[0] + kGtNs4[1], t2 = nks * kGtNs2[0] + kGtNs2[1], t1 = nks * kGtNs1[0] + kGtNs1[1];
   const int64_t one = n4 ? t4 : n2 ? t2 : t1;
@@ -847,6 +855,11 @@ __global__ __launch_bounds__(kGtThreads, 1) void gt_kernel(GroupedArgs p) {
 // ============================================================================================
 // weights: 256 columns of x by 256 columns of dy a tile, both read across: the expert's rows are the reduced
 // dimension, 64 a stage.  The ring, the barrier and the steps are those above.
+//
+// Long experts: as the rows (16384 x 7168 x 4096: 789 us, 1220 TFLOP/s).  Short ones: the gradients' stores, which
+// no products run beside, since all workgroups store at about the same time (48 experts of 512 rows, float32 7168 x
+// 4096: 2080 us, 1250 without the stores; of 64 experts of 32 rows 1440, 5.3 TB/s).  Tiles of another order for each XCD, so
+// that they store at other times: slower.
 // ============================================================================================
 constexpr int kGwSlot = 2 * kGtSide;
 constexpr int kGwTokens = 2 * kGwSlot;               // LDS: the waves' tokens of two stages' rows
@@ -1032,7 +1045,9 @@ __device__ __forceinline__ void gw_fine_phase(const GroupedWgradArgs& p) {
   wait_vmcnt<0>();
 }
 
-// Whether the tiles of 64 x 64 take the call: the time of the fullest workgroup either way, from the counts.
+// Whether the tiles of 64 x 64 take the call: the time of the fullest workgroup either way, from the counts.  (Large and
+// small tiles, us: 4 experts of 945 rows, 40 x 696, 25.8 and 8.2; 4 of 2233, 160 x 816, 57 and 16; 1 of 469, 3496 x 456, 22 and 11;
+// 8 of 15, 520 x 1032, 12.3 and 13.3; 48 of 100, 1024 x 1024, 42 and 91.)
 __device__ __forceinline__ bool gw_fine(const GroupedWgradArgs& p, bool gather) {
   const int64_t per = (int64_t)((p.K + 255) / 256) * ((p.N + 255) / 256), perf = (int64_t)((p.K + 63) / 64) * ((p.N + 63) / 64);
   int coarse = 0, fine = 0, most = 0;  // a tile of every expert, in tenths of a us; the largest count
@@ -1269,7 +1284,8 @@ __global__ __launch_bounds__(kGtThreads, 1) void gt_weights_kernel(GroupedWgradA
 // part of the weight rows through an LDS ring of its own, 16 rows by 256 bytes a slot with the m-tile's token rows
 // beside them (they come from the L2), by direct loads: no barrier, no registers, and the ring runs on across groups,
 // m-tiles and experts.  kSplit: the 4 waves split K; at a group's end they leave their sums in LDS and one of them
-// adds the four in wave order.  Otherwise every wave takes groups of its own.
+// adds the four in wave order.  Otherwise every wave takes groups of its own.  8 x 7168 x 2048 int8 takes 7.0 us, of which
+// 5.3 are a launch and its call; int8 gate+up of 8 tokens, 147 MB of weights, 28.8 (5.1 TB/s); bf16, 294 MB, 53.5 (5.5).
 //
 // Both operands keep 16-byte piece c of row R at place c ^ R of the row's 256 bytes: the 16 rows of one piece are
 // read from 16 different places.

@@ -579,7 +579,7 @@ def int8_linear_gate_up_silu(a_codes, a_scales, w13_codes, w13_scales, h, stream
 
 
 def _gathered_bytes(name, t):
-    """Row offsets are 32-bit counts of 16 bytes; the library is not told how many rows a gathered tensor has."""
+    """The products' limit on their rows; the library is not told how many a gathered tensor has."""
     if _nbytes(t) >= 1 << 36:
         raise MegaMoEError(f"{name} has {_nbytes(t)} bytes, expected less than 2^36")
 

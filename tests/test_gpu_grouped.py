@@ -148,6 +148,56 @@ def test_weights_gradient(i, dtype, dwt, gather):
     assert torch.equal(acc[none], old[none])
 
 
+@pytest.mark.parametrize("gather", [False, True])
+@pytest.mark.parametrize("dtype,dwt", [(BF, F32), (HF, HF)])
+@pytest.mark.parametrize("counts,K,N", [
+    ([3584, 1, 0, 3583, 127, 129], 40, 696),   # an expert's tokens fill what is kept of them,
+    ([5, 3585, 0, 128, 4], 40, 696),           # or are one too many
+    ("ragged", 64, 64),                        # several experts a workgroup
+    ("ragged", 8, 72),
+])
+def test_weights_gradient_of_small_matrices(counts, K, N, dtype, dwt, gather):
+    if counts == "ragged":
+        counts = np.random.default_rng(5).integers(0, 300, 1024).tolist()
+    T = max(counts) + 9
+    counts, poff, rt = tables(counts, 1, T, 3)
+    gen = torch.Generator(device=DEV).manual_seed(K)
+    x, dy = normal(gen, T if gather else len(rt), K, dtype=dtype), normal(gen, len(rt), N, std=0.1, dtype=dtype)
+    old = normal(gen, len(counts), N, K, dtype=dwt)
+    dw, acc = torch.full_like(old, float("nan")), old.clone()
+    kw = dict(row_token=on(rt) if gather else None)
+    mm.moe_grouped_gemm_wgrad(dy, x, on(poff), on(counts), dw, **kw)
+    mm.moe_grouped_gemm_wgrad(dy, x, on(poff), on(counts), acc, accumulate=True, **kw)
+    torch.cuda.synchronize()
+    for e, at, src in spans(counts, poff, rt, gather):
+        g, a = dy[at].double().t(), x[src].double()
+        accept(dw[e], g @ a, g.abs() @ a.abs(), int(counts[e]))
+        accept(acc[e], g @ a + old[e].double(), g.abs() @ a.abs() + old[e].double().abs(), int(counts[e]) + 1)
+    none = on(counts == 0)
+    assert not dw[none].any() and torch.equal(acc[none], old[none])
+
+
+@pytest.mark.parametrize("gather", [False, True])
+@pytest.mark.parametrize("bound", [0, 3])
+def test_all_the_experts_there_can_be(bound, gather):
+    """1024 experts of 0 to 3 rows, a few of more, and with them the last lists' places."""
+    counts = np.random.default_rng(6).integers(0, 4, 1024)
+    counts[[0, 500, 1023]] = 300, 70, 140
+    counts, poff, rt = tables(counts, 1, 310, 4)
+    gen = torch.Generator(device=DEV).manual_seed(7)
+    K, N, cap = 136, 72, len(rt)
+    x, w, dy = normal(gen, 310 if gather else cap, K), normal(gen, 1024, N, K), normal(gen, cap, N)
+    y, dx = torch.full((cap, N), 7.0, dtype=BF, device=DEV), torch.full((cap, K), 7.0, dtype=BF, device=DEV)
+    mm.moe_grouped_gemm(x, w, on(poff), on(counts), y, row_token=on(rt) if gather else None, max_rows_per_expert=bound)
+    mm.moe_grouped_gemm_dgrad(dy, w, on(poff), on(counts), dx)
+    torch.cuda.synchronize()
+    for e, at, src in spans(counts, poff, rt, gather):
+        a, b, g = x[src].double(), w[e].double(), dy[at].double()
+        accept(y[at], a @ b.t(), a.abs() @ b.t().abs(), K)
+        accept(dx[at], g @ b, g.abs() @ b.abs(), N)
+    assert torch.all(y[poff[-1]:] == 7.0) and torch.all(dx[poff[-1]:] == 7.0)
+
+
 def test_gradients_agree_with_differences():
     """A loss that is linear in each factor: halves of central differences of the product itself, in fp32 sums of
     values that bf16 holds exactly (small whole numbers)."""
