@@ -419,6 +419,44 @@ def test_calls_captured_and_on_two_streams(T):
             assert all(torch.equal(p[:cap - 5], q[:cap - 5]) for p, q in zip(o, want))
 
 
+def test_captured_calls_on_other_counts():
+    """One captured forward and backward, replayed on tables that each kernel's tiles and none would take."""
+    gen = torch.Generator(device=DEV).manual_seed(12)
+    K, N, T, E = 264, 136, 1400, 4
+    cap = 1408
+    x, w, dy = normal(gen, T, K), normal(gen, E, N, K), normal(gen, cap, N)
+    poff, counts = (torch.zeros(n, dtype=torch.int32, device=DEV) for n in (E + 1, E))
+    row = torch.zeros(cap, dtype=torch.int32, device=DEV)
+    y, dx, dw = (torch.zeros(n, dtype=BF, device=DEV) for n in ((cap, N), (cap, K), (E, N, K)))
+
+    def step():
+        mm.moe_grouped_gemm(x, w, poff, counts, y, row_token=row)
+        mm.moe_grouped_gemm_dgrad(dy, w, poff, counts, dx)
+        mm.moe_grouped_gemm_wgrad(dy, x, poff, counts, dw, row_token=row)
+    step()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    for case in ([1, 0, 2, 3], [700, 0, 60, 300], [0, 0, 0, 0], [1400, 1, 1, 1], [128, 256, 64, 65]):
+        cnt, po, rt = tables(case, 1, T, 5)
+        rt = rt[:cap]
+        counts.copy_(on(cnt))
+        poff.copy_(on(po))
+        row[:len(rt)].copy_(on(rt))
+        for t in (y, dx, dw):
+            t.fill_(7.0)
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        for e, at, src in spans(cnt, po, rt, True):
+            a, b, d = x[src].double(), w[e].double(), dy[at].double()
+            accept(y[at], a @ b.t(), a.abs() @ b.t().abs(), K)
+            accept(dx[at], d @ b, d.abs() @ b.abs(), N)
+            accept(dw[e], d.t() @ a, d.t().abs() @ a.abs(), case[e])
+        assert torch.all(y[po[-1]:] == 7.0) and torch.all(dx[po[-1]:] == 7.0) and not dw[on(cnt == 0)].any()
+
+
 def test_no_rows():
     """M_cap = 0: no product; weights' gradients become 0, or stay with accumulate."""
     bf = lambda *s: torch.zeros(*s, dtype=BF, device=DEV)  # noqa: E731
