@@ -32,9 +32,9 @@ constexpr int kGtStage = 128;                       // bytes of K a stage (64 or
 constexpr int kGtSide = kGtCols * kGtStage;         // LDS bytes of a stage's A side
 constexpr int kGtLds = 160 * 1024;
 // ns of a tile, by its rows (of 256 columns, and of the tiles of 64 x 64): a stage of 128 bytes of K, and the rest.
-constexpr int64_t kGtNs4[2] = {1300, 4000}, kGtNs2[2] = {1150, 5000}, kGtNs1[2] = {1050, 5000}, kGtNsFine[2] = {250, 1500};
+constexpr int kGtNs4[2] = {1300, 4000}, kGtNs2[2] = {1150, 5000}, kGtNs1[2] = {1050, 5000}, kGtNsFine[2] = {250, 1500};
 constexpr int kGwTile = 60, kGwFineTile = 20;  // the weights' gradient's tiles, beside their stages, in tenths of a us
-constexpr int64_t kGtNsFineAlone = 330;  // of a stage where no two tiles of 64 rows share weights
+constexpr int kGtNsFineAlone = 330;  // of a stage where no two tiles of 64 rows share weights
 constexpr int kGtBand = 8;                          // m-tiles walked together, for L2 reuse of the weights
 // The kernels have no static LDS: addresses start at 0.  At the end: two list lengths, m-tile prefix int32 [E + 1],
 // two lists uint16 [E].
@@ -76,6 +76,8 @@ __device__ __forceinline__ int g_scan(int v) {
   v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);  // row_bcast 31 into rows 2 and 3
   return v;
 }
+
+__device__ __forceinline__ int g_total(int v) { return __builtin_amdgcn_readlane(g_scan(v), kWave - 1); }
 
 // What follows from the lane is computed where it is used, not held in registers through a loop.
 __device__ __forceinline__ int g_here(int v) {
@@ -754,13 +756,15 @@ __device__ __forceinline__ void gt_fine_phase(const GroupedArgs& p, int t0, int 
 // (Large and small tiles, us: int8 256 x 4096 x 7168 71 and 16, 1024 rows 86 and 51, 2048 rows 88 and 99; bf16 16 experts of 288 rows, 3640 to
 // 176, 118 and 19; 64 of 94 rows, 2048 to 7168, 402 and 534; 48 of 40 rows, 7168 to 4096, 404 and 479; 8 of 32, 512 to 1024, 10.7
 // and 7.2; across, 24 of 100 rows, 2048 to 1024, 39 and 28.)
-__device__ __forceinline__ bool gt_fine(int64_t n4, int64_t n2, int64_t n1, int64_t fine, int nks) {
-  const int64_t t4 = nks * kGtNs4[0] + kGtNs4[1], t2 = nks * kGtNs2[0] + kGtNs2[1], t1 = nks * kGtNs1[0] + kGtNs1[1];
-  const int64_t one = n4 ? t4 : n2 ? t2 : t1;
-  const int64_t n = n4 + n2 + n1, rounds = (n + kGtGrid - 1) / kGtGrid;
-  int64_t all = n ? (n4 * t4 + n2 * t2 + n1 * t1) / n * rounds : 0;
-  if (all < one) all = one;
-  return (fine + kGtGrid - 1) / kGtGrid * (nks * (n4 || n2 ? kGtNsFine[0] : kGtNsFineAlone) + kGtNsFine[1]) < all;
+// In float32: a division of 64-bit integers lasts longer than all of the rest.
+__device__ __forceinline__ bool gt_fine(int m4, int m2, int m1, int mf, int ntn, int ntf, int nks) {
+  const float t4 = (float)(nks * kGtNs4[0] + kGtNs4[1]), t2 = (float)(nks * kGtNs2[0] + kGtNs2[1]);
+  const float t1 = (float)(nks * kGtNs1[0] + kGtNs1[1]);
+  const float tf = (float)(nks * (m4 || m2 ? kGtNsFine[0] : kGtNsFineAlone) + kGtNsFine[1]);
+  const float one = m4 ? t4 : m2 ? t2 : t1, n = (float)(m4 + m2 + m1), per = 1.0f / kGtGrid;
+  const float rounds = ceilf(n * (float)ntn * per);
+  const float all = n > 0.0f ? ((float)m4 * t4 + (float)m2 * t2 + (float)m1 * t1) * __builtin_amdgcn_rcpf(n) * rounds : 0.0f;
+  return ceilf((float)mf * (float)ntf * per) * tf < (all < one ? one : all);
 }
 
 template <int kOp, int kDtype>
@@ -786,8 +790,7 @@ __global__ __launch_bounds__(kGtThreads, 1) void gt_kernel(GroupedArgs p) {
       own1 += l == 1;
       ownf += (cnt + 63) / 64;
     }
-    const bool fine = gt_fine((int64_t)wave_sum_i32(own4) * ntn, (int64_t)wave_sum_i32(own2) * ntn,
-                              (int64_t)wave_sum_i32(own1) * ntn, (int64_t)wave_sum_i32(ownf) * ntf,
+    const bool fine = gt_fine(g_total(own4), g_total(own2), g_total(own1), g_total(ownf), ntn, ntf,
                               (int)(((int64_t)p.K * GType<kDtype>::kBytes + kGtStage - 1) / kGtStage));
     int carry = 0, n2 = 0, n1 = 0;
     const uint64_t below = ((uint64_t)1 << lane) - 1;
@@ -1057,7 +1060,7 @@ __device__ __forceinline__ bool gw_fine(const GroupedWgradArgs& p, bool gather) 
     fine += 5 * ((cnt + 127) / 128) + kGwFineTile;
     most = most > cnt ? most : cnt;
   }
-  const int64_t all = (int64_t)wave_sum_i32(coarse) * per, all_fine = (int64_t)wave_sum_i32(fine) * perf;
+  const int64_t all = (int64_t)g_total(coarse) * per, all_fine = (int64_t)g_total(fine) * perf;
   most = (int)wave_max_u32((uint32_t)most);
   if (gather && most > kGwMaxTokens) return false;
   const int64_t one = 14 * (int64_t)((most + 63) / 64) + kGwTile, one_fine = 5 * (int64_t)((most + 127) / 128) + kGwFineTile;
