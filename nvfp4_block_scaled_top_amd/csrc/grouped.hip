@@ -1288,7 +1288,8 @@ __global__ __launch_bounds__(kGtThreads, 1) void gt_weights_kernel(GroupedWgradA
 // beside them (they come from the L2), by direct loads: no barrier, no registers, and the ring runs on across groups,
 // m-tiles and experts.  kSplit: the 4 waves split K; at a group's end they leave their sums in LDS and one of them
 // adds the four in wave order.  Otherwise every wave takes groups of its own.  8 x 7168 x 2048 int8 takes 7.0 us, of which
-// 5.3 are a launch and its call; int8 gate+up of 8 tokens, 147 MB of weights, 28.8 (5.1 TB/s); bf16, 294 MB, 53.5 (5.5).
+// 5.3 are a launch and its call; int8 gate+up of 8 tokens, 7168 to
+// 2 x 2048, at 5 experts 25 (5.8 TB/s), at 11 51 (6.4); bf16, 7168 to 4096, 47 (6.3) and 98 (6.6).
 //
 // Both operands keep 16-byte piece c of row R at place c ^ R of the row's 256 bytes: the 16 rows of one piece are
 // read from 16 different places.
