@@ -765,7 +765,7 @@ int32_t moe_grouped_gemm_l2_int8(const int8_t* h_codes, const float* h_scales, c
  * s = row_token[r], or r without row_token:
  *   y[r, n]     = sum_k x[s, k] * W[e, n, k]
  *   dx[r, k]    = sum_n dy[r, n] * W[e, n, k]          (by row r: a token's gradient is the sum over its
- *                 rows, e.g. moe_combine of dx with weights of 1)
+ *                 rows; in bf16 moe_combine of dx with weights of 1.  moe_combine takes no fp16 rows)
  *   dw[e, n, k] = sum over the expert's rows r of dy[r, n] * x[s, k], added to what dw holds with accumulate
  * with FP32 accumulation and one rounding to the output's type (accumulate: of the float32 sum of the
  * old value and the FP32 total).  Results do not change from call to call.  Rows of y and dx that hold no

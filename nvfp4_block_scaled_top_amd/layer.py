@@ -78,7 +78,7 @@ def quantize_matrix(w_bf16: torch.Tensor, codes: torch.Tensor, scales: torch.Ten
                     stream=None) -> None:
     """NVFP4-quantize one bf16 matrix on the GPU (rows = output features, K contiguous)."""
     ws = torch.empty(mm.megamoe_quant_workspace_bytes(*w_bf16.shape), dtype=torch.uint8, device=w_bf16.device)
-    mm.nvfp4_quantize_act(w_bf16.view(torch.int16), codes, scales, gs, workspace=ws, stream=stream)
+    mm.nvfp4_quantize_act(w_bf16, codes, scales, gs, workspace=ws, stream=stream)
 
 
 def quantize_expert_into(weights: MoEWeights, e: int, w13_bf16: torch.Tensor, w2_bf16: torch.Tensor) -> None:

@@ -147,6 +147,17 @@ def _ptr(t: Optional[torch.Tensor]):
     return t.data_ptr()
 
 
+#: bf16 tensors; their 16 bits may be viewed as integers.
+_BF16_BITS = (torch.bfloat16, torch.int16, torch.uint16)
+
+
+def _bf16(name: str, t: Optional[torch.Tensor]):
+    """_ptr of a bf16 tensor: a tensor of another type (float16 among them) would be taken for bf16 bits."""
+    if t is not None and t.dtype not in _BF16_BITS:
+        raise MegaMoEError(f"{name} is {t.dtype}, expected one of {list(_BF16_BITS)}")
+    return _ptr(t)
+
+
 def _stream(stream) -> int:
     if stream is None:
         stream = torch.cuda.current_stream()
@@ -222,7 +233,7 @@ def moe_route_quantize(topk_ids, expert_begin, num_experts, pad_multiple, counts
     _check("moe_route_quantize", lib().moe_route_quantize(
         _ptr(topk_ids), T, k, expert_begin, num_experts, pad_multiple, block_m_override, _ptr(counts),
         _ptr(expert_offsets), _ptr(padded_offsets), _ptr(row_token), _ptr(token_rows), _ptr(sched),
-        _ptr(route_workspace), _nbytes(route_workspace), _ptr(x_bf16), H, _ptr(x_gs_in), _ptr(x_codes),
+        _ptr(route_workspace), _nbytes(route_workspace), _bf16("x_bf16", x_bf16), H, _ptr(x_gs_in), _ptr(x_codes),
         _ptr(x_scales), _ptr(x_global_scale), _ptr(quant_workspace), _nbytes(quant_workspace), _stream(stream)))
 
 
@@ -231,14 +242,15 @@ def nvfp4_quantize_act(x_bf16, codes, scales, global_scale, workspace=None, row_
     rows, cols = x_bf16.shape
     n_amax = 0 if amax_in is None else amax_in.numel()
     _check("nvfp4_quantize_act", lib().nvfp4_quantize_act(
-        _ptr(x_bf16), rows, cols, _ptr(row_valid), _ptr(amax_in), n_amax, _ptr(codes), _ptr(scales), _ptr(global_scale),
-        _ptr(workspace), _nbytes(workspace), _stream(stream)))
+        _bf16("x_bf16", x_bf16), rows, cols, _ptr(row_valid), _ptr(amax_in), n_amax, _ptr(codes), _ptr(scales),
+        _ptr(global_scale), _ptr(workspace), _nbytes(workspace), _stream(stream)))
 
 
 def nvfp4_quantize_act_gs(x_bf16, global_scale_in, codes, scales, row_valid=None, stream=None):
     rows, cols = x_bf16.shape
     _check("nvfp4_quantize_act_gs", lib().nvfp4_quantize_act_gs(
-        _ptr(x_bf16), rows, cols, _ptr(row_valid), _ptr(global_scale_in), _ptr(codes), _ptr(scales), _stream(stream)))
+        _bf16("x_bf16", x_bf16), rows, cols, _ptr(row_valid), _ptr(global_scale_in), _ptr(codes), _ptr(scales),
+        _stream(stream)))
 
 
 def nvfp4_pack_weight_codes(codes, packed, stream=None):
@@ -260,8 +272,8 @@ def moe_grouped_gemm_l1_silu(x_codes, x_scales, x_gs, row_token, padded_offsets,
         raise MegaMoEError(f"h_amax_parts needs {L1_AMAX_PARTS} floats")
     head = (_ptr(x_codes), _ptr(x_scales), _ptr(x_gs), _ptr(row_token), _ptr(padded_offsets), _ptr(counts),
             _ptr(sched), _ptr(w13_codes), _ptr(w13_scales), _ptr(w13_gs))
-    tail = (E, 2 * Hh, I2 // 2, M_cap, block_m_override, max_rows_per_expert, _ptr(h_bf16), _ptr(h_amax_parts),
-            _stream(stream))
+    tail = (E, 2 * Hh, I2 // 2, M_cap, block_m_override, max_rows_per_expert, _bf16("h_bf16", h_bf16),
+            _ptr(h_amax_parts), _stream(stream))
     if w13_packed is None:
         _check("moe_grouped_gemm_l1_silu", lib().moe_grouped_gemm_l1_silu(*head, *tail))
     else:
@@ -292,7 +304,7 @@ def moe_grouped_gemm_l2(h_codes, h_scales, h_gs, padded_offsets, counts, sched, 
     M_cap = y_bf16.shape[0]
     head = (_ptr(h_codes), _ptr(h_scales), _ptr(h_gs), _ptr(padded_offsets), _ptr(counts), _ptr(sched),
             _ptr(w2_codes), _ptr(w2_scales), _ptr(w2_gs))
-    tail = (E, H, 2 * Ih, M_cap, block_m_override, max_rows_per_expert, _ptr(y_bf16), _stream(stream))
+    tail = (E, H, 2 * Ih, M_cap, block_m_override, max_rows_per_expert, _bf16("y_bf16", y_bf16), _stream(stream))
     if w2_packed is None:
         _check("moe_grouped_gemm_l2", lib().moe_grouped_gemm_l2(*head, *tail))
     else:
@@ -314,8 +326,8 @@ def moe_grouped_ffn_fused(x_codes, x_scales, x_gs, row_token, padded_offsets, co
     head = (_ptr(x_codes), _ptr(x_scales), _ptr(x_gs), _ptr(row_token), _ptr(padded_offsets), _ptr(counts),
             _ptr(sched), _ptr(w13_codes), _ptr(w13_scales), _ptr(w13_gs), _ptr(w2_codes), _ptr(w2_scales),
             _ptr(w2_gs))
-    tail = (E, 2 * Hh, I2 // 2, M_cap, _ptr(h_gs_in), _ptr(h_bf16), _ptr(h_amax_parts), _ptr(h_codes),
-            _ptr(h_scales), _ptr(h_gs_out), _ptr(y_bf16), _ptr(sync), _nbytes(sync), _stream(stream))
+    tail = (E, 2 * Hh, I2 // 2, M_cap, _ptr(h_gs_in), _bf16("h_bf16", h_bf16), _ptr(h_amax_parts), _ptr(h_codes),
+            _ptr(h_scales), _ptr(h_gs_out), _bf16("y_bf16", y_bf16), _ptr(sync), _nbytes(sync), _stream(stream))
     if w13_packed is None or w2_packed is None:
         _check("moe_grouped_ffn_fused", lib().moe_grouped_ffn_fused(*head, *tail))
     else:
@@ -323,19 +335,39 @@ def moe_grouped_ffn_fused(x_codes, x_scales, x_gs, row_token, padded_offsets, co
                lib().moe_grouped_ffn_fused_packed(*head, _ptr(w13_packed), _ptr(w2_packed), *tail))
 
 
-def moe_combine(y_bf16, token_rows, topk_weights, out_bf16, stream=None):
+def _combine_extents(y_bf16, token_rows, topk_weights, out_bf16):
+    """T, k and H of a combine, whose tensors must hold as much as the kernel reads and writes (buffers made for
+    more tokens may be longer)."""
     T, k = topk_weights.shape
     H = out_bf16.shape[1]
+    if topk_weights.dtype != torch.float32 or token_rows.dtype != torch.int32:
+        raise MegaMoEError(f"topk_weights is {topk_weights.dtype} and token_rows {token_rows.dtype}, "
+                           "expected torch.float32 and torch.int32")
+    if y_bf16.dim() != 2 or y_bf16.shape[1] != H:
+        raise MegaMoEError(f"y_bf16 has shape {tuple(y_bf16.shape)}, expected (rows, {H})")
+    if out_bf16.shape[0] < T or token_rows.numel() < T * k:
+        raise MegaMoEError(f"out_bf16 has {out_bf16.shape[0]} rows and token_rows {token_rows.numel()} entries, "
+                           f"expected {T} and {T * k}")
+    return T, k, H
+
+
+def moe_combine(y_bf16, token_rows, topk_weights, out_bf16, stream=None):
+    """y_bf16 [rows, H] and out_bf16 [T, H] bf16 (also viewed as 16-bit integers; float16 is refused), token_rows
+    int32 [T * k], topk_weights float32 [T, k]."""
+    T, k, H = _combine_extents(y_bf16, token_rows, topk_weights, out_bf16)
     _check("moe_combine", lib().moe_combine(
-        _ptr(y_bf16), _ptr(token_rows), _ptr(topk_weights), T, k, H, _ptr(out_bf16), _stream(stream)))
+        _bf16("y_bf16", y_bf16), _ptr(token_rows), _ptr(topk_weights), T, k, H, _bf16("out_bf16", out_bf16),
+        _stream(stream)))
 
 
 def moe_combine_shared(y_bf16, token_rows, topk_weights, y_shared_bf16, out_bf16, stream=None):
-    T, k = topk_weights.shape
-    H = out_bf16.shape[1]
+    """moe_combine with y_shared_bf16 [T, H] added to each token's sum."""
+    T, k, H = _combine_extents(y_bf16, token_rows, topk_weights, out_bf16)
+    if y_shared_bf16.dim() != 2 or y_shared_bf16.shape[0] < T or y_shared_bf16.shape[1] != H:
+        raise MegaMoEError(f"y_shared_bf16 has shape {tuple(y_shared_bf16.shape)}, expected {(T, H)}")
     _check("moe_combine_shared", lib().moe_combine_shared(
-        _ptr(y_bf16), _ptr(token_rows), _ptr(topk_weights), T, k, H, _ptr(y_shared_bf16), _ptr(out_bf16),
-        _stream(stream)))
+        _bf16("y_bf16", y_bf16), _ptr(token_rows), _ptr(topk_weights), T, k, H,
+        _bf16("y_shared_bf16", y_shared_bf16), _bf16("out_bf16", out_bf16), _stream(stream)))
 
 
 # ---- dense layers ------------------------------------------------------------------------------
@@ -349,7 +381,7 @@ def nvfp4_linear(a_codes, a_scales, a_gs, w_codes, w_scales, w_gs, out_bf16, wor
     N = w_codes.shape[0]
     _check("nvfp4_linear", lib().nvfp4_linear(
         _ptr(a_codes), _ptr(a_scales), _ptr(a_gs), M, 2 * Kh, _ptr(w_codes), _ptr(w_scales), _ptr(w_gs), N,
-        _ptr(out_bf16), _ptr(workspace), _nbytes(workspace), _stream(stream)))
+        _bf16("out_bf16", out_bf16), _ptr(workspace), _nbytes(workspace), _stream(stream)))
 
 
 def nvfp4_linear_gate_up_silu(a_codes, a_scales, a_gs, w13_codes, w13_scales, w13_gs, h_bf16, h_amax_parts,
@@ -360,7 +392,7 @@ def nvfp4_linear_gate_up_silu(a_codes, a_scales, a_gs, w13_codes, w13_scales, w1
         raise MegaMoEError(f"h_amax_parts needs {L1_AMAX_PARTS} floats")
     _check("nvfp4_linear_gate_up_silu", lib().nvfp4_linear_gate_up_silu(
         _ptr(a_codes), _ptr(a_scales), _ptr(a_gs), M, 2 * Kh, _ptr(w13_codes), _ptr(w13_scales), _ptr(w13_gs), I,
-        _ptr(h_bf16), _ptr(h_amax_parts), _ptr(workspace), _nbytes(workspace), _stream(stream)))
+        _bf16("h_bf16", h_bf16), _ptr(h_amax_parts), _ptr(workspace), _nbytes(workspace), _stream(stream)))
 
 
 def nvfp4_linear_gate_up_silu_nvfp4(a_codes, a_scales, a_gs, w13_codes, w13_scales, w13_gs, h_gs, h_codes, h_scales,

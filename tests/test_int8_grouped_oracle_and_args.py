@@ -178,3 +178,50 @@ def test_int8_layer_weight_shapes():
     assert (w.num_experts, w.hidden, w.intermediate) == (4, 256, 128)
     assert w.w13_scales.shape == (4, 256) and w.w2_scales.shape == (4, 256)
     assert w.nbytes_expert() == 256 * 256 + 256 * 4 + 256 * 128 + 256 * 4
+
+
+@pytest.mark.parametrize("other", [torch.float16, torch.float32])
+def test_calls_on_bf16_refuse_other_types(other, monkeypatch):
+    """The products, their gradients and the decoder write float16 too; a call that knows only bf16 has to refuse it
+    (it would take the bits for bf16).  Every other argument is taken as it is here, CPU tensors too: each call ends at
+    the refusal."""
+    monkeypatch.setattr(mm, "_ptr", lambda t: None if t is None else t.data_ptr())
+    bf = lambda *s: torch.zeros(*s, dtype=torch.bfloat16)  # noqa: E731
+    bad = lambda *s: torch.zeros(*s, dtype=other)  # noqa: E731
+    i32, u8, f32 = (lambda *s, d=d: torch.zeros(*s, dtype=d) for d in (torch.int32, torch.uint8, torch.float32))
+    rows, w, parts = i32(8), f32(4, 2), f32(mm.L1_AMAX_PARTS)
+    dense = u8(4, 32), u8(4, 4), f32(1), u8(64, 32), u8(64, 4), f32(1)
+    routed = u8(4, 32), u8(4, 4), f32(1)
+    w13, w2 = (u8(2, 128, 32), u8(2, 128, 4), f32(2)), (u8(2, 64, 32), u8(2, 64, 4), f32(2))
+    tabs = [i32(3)] * 3
+    calls = {
+        "y_bf16": [lambda: mm.moe_combine(bad(8, 64), rows, w, bf(4, 64)),
+                   lambda: mm.moe_combine_shared(bad(8, 64), rows, w, bf(4, 64), bf(4, 64)),
+                   lambda: mm.moe_grouped_gemm_l2(*routed, *tabs, *w2, bad(8, 64))],
+        "out_bf16": [lambda: mm.moe_combine(bf(8, 64), rows, w, bad(4, 64)),
+                     lambda: mm.moe_combine_shared(bf(8, 64), rows, w, bf(4, 64), bad(4, 64)),
+                     lambda: mm.nvfp4_linear(*dense, bad(4, 64), u8(64))],
+        "y_shared_bf16": [lambda: mm.moe_combine_shared(bf(8, 64), rows, w, bad(4, 64), bf(4, 64))],
+        "x_bf16": [lambda: mm.nvfp4_quantize_act(bad(4, 64), u8(4, 32), u8(4, 4), f32(1)),
+                   lambda: mm.nvfp4_quantize_act_gs(bad(4, 64), f32(1), u8(4, 32), u8(4, 4)),
+                   lambda: layer.quantize_matrix(bad(4, 64), u8(4, 32), u8(4, 4), f32(1))],
+        "h_bf16": [lambda: mm.nvfp4_linear_gate_up_silu(*dense, bad(4, 32), parts, u8(64)),
+                   lambda: mm.moe_grouped_gemm_l1_silu(*routed, i32(8), *tabs, *w13, bad(8, 64), parts)],
+    }
+    for name, fs in calls.items():
+        for f in fs:
+            with pytest.raises(mm.MegaMoEError, match=f"{name} is {other}"):
+                f()
+
+
+def test_combine_refuses_tensors_that_hold_too_little():
+    bf = lambda *s: torch.zeros(*s, dtype=torch.bfloat16)  # noqa: E731
+    rows, w = torch.zeros(8, dtype=torch.int32), torch.zeros(4, 2)
+    for y, r, wt, out, match in ((bf(8, 32), rows, w, bf(4, 64), "y_bf16 has"), (bf(8, 64), rows, w, bf(3, 64), "out_bf16 has"),
+                                 (bf(8, 64), rows[:7], w, bf(4, 64), "token_rows 7"), (bf(8, 64), rows.long(), w, bf(4, 64), "int64"),
+                                 (bf(8, 64), rows, w.double(), bf(4, 64), "float64"), (bf(8, 64), rows, w, bf(4, 64), "GPU")):
+        with pytest.raises(mm.MegaMoEError, match=match):
+            mm.moe_combine(y, r, wt, out)
+    for sh in (bf(3, 64), bf(4, 32)):
+        with pytest.raises(mm.MegaMoEError, match="y_shared_bf16 has"):
+            mm.moe_combine_shared(bf(8, 64), rows, w, sh, bf(4, 64))
