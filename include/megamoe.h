@@ -671,7 +671,8 @@ int32_t mxfp4_linear_gate_up_silu(const uint8_t* a_codes, const uint8_t* a_scale
  * Limits: E as for moe_route_permute; the reduced dimension (H for L1, I for L2) a multiple of 128,
  * the output dimension a multiple of 16, both below 2^30; M_cap rows of codes, x_codes (T is not an
  * argument: T <= M_cap with M_cap as above) and one expert's codes below 2^36 bytes each; alignment as for
- * mxfp4_linear.  With M_cap == 0 the row arrays may be NULL and the call enqueues nothing.
+ * mxfp4_linear.  With M_cap == 0 the row arrays may be NULL and the call enqueues nothing; pass 0 when T is
+ * 0, whatever the padding leaves room for.
  * ---------------------------------------------------------------------------------------- */
 int32_t moe_grouped_gemm_l1_silu_mxfp4(const uint8_t* x_codes, const uint8_t* x_scales,
                                        const int32_t* row_token, const int32_t* padded_offsets,
@@ -745,7 +746,7 @@ int32_t int8_linear_gate_up_silu(const int8_t* a_codes, const float* a_scales, i
  * h_bf16 bf16 [M_cap, I];  y_bf16 bf16 [M_cap, H].
  * Limits: E as for moe_route_permute; H, I and alignment as K, N and alignment of int8_linear; x and h below
  * 2^36 bytes (T is not an argument: T <= M_cap with M_cap as above).  With M_cap == 0 the row arrays may be
- * NULL and the call enqueues nothing.
+ * NULL and the call enqueues nothing; pass 0 when T is 0, whatever the padding leaves room for.
  * ---------------------------------------------------------------------------------------- */
 int32_t moe_grouped_gemm_l1_silu_int8(const int8_t* x_codes, const float* x_scales, const int32_t* row_token,
                                       const int32_t* padded_offsets, const int32_t* counts,
@@ -781,6 +782,7 @@ int32_t moe_grouped_gemm_l2_int8(const int8_t* h_codes, const float* h_scales, c
  * Limits: E as for moe_route_permute; K and N >= 8, multiples of 8 and below 2^22; 0 <= M_cap < 2^31,
  * x and dy below 2^36 bytes each (T <= M_cap); pointers aligned to 16 bytes, the tables to 4; no output
  * overlaps an input.  With M_cap == 0 the row arrays may be NULL; y and dx are then not written, dw as above.
+ * Pass 0 when T is 0, whatever the padding leaves room for.
  * ---------------------------------------------------------------------------------------- */
 int32_t moe_grouped_gemm(const void* x, int32_t dtype, const int32_t* row_token, const int32_t* padded_offsets,
                          const int32_t* counts, const void* w, int32_t E, int32_t K, int32_t N, int64_t M_cap,

@@ -494,6 +494,12 @@ def moe_router_scores_bwd(logits, topk_ids, grad_weights, grad_logits, score="si
 
 # ---- MXFP4 -------------------------------------------------------------------------------------
 
+def _rows_of(tokens: int, M_cap: int) -> int:
+    """Rows of a call that gathers from `tokens` rows: without a token none, although the padding leaves room for some
+    (an empty tensor has no address, which the library would refuse beside M_cap > 0)."""
+    return M_cap if tokens else 0
+
+
 def mxfp4_quantize_act(x, codes, scales, row_valid=None, stream=None):
     """x [rows, cols] bf16 (also viewed as int16) or float32 -> codes [rows, cols/2], scales [rows, cols/32]."""
     rows, cols = x.shape
@@ -547,7 +553,8 @@ def moe_grouped_gemm_l1_silu_mxfp4(x_codes, x_scales, row_token, padded_offsets,
         _arg("x_codes", x_codes, _U8, (T, Hh), dev), _arg("x_scales", x_scales, _U8, (T, Hh // 16), dev),
         _arg("row_token", row_token, _INT, (M_cap,), dev), _arg("padded_offsets", padded_offsets, _INT, (E + 1,), dev),
         _arg("counts", counts, _INT, (E,), dev), _arg("w13_codes", w13_codes, _U8, (E, 2 * I, Hh), dev),
-        _arg("w13_scales", w13_scales, _U8, (E, 2 * I, Hh // 16), dev), E, 2 * Hh, I, M_cap, max_rows_per_expert,
+        _arg("w13_scales", w13_scales, _U8, (E, 2 * I, Hh // 16), dev), E, 2 * Hh, I, _rows_of(T, M_cap),
+        max_rows_per_expert,
         _arg("h_bf16", h_bf16, _BF16, (M_cap, I), dev), st))
 
 
@@ -629,7 +636,7 @@ def moe_grouped_gemm_l1_silu_int8(x_codes, x_scales, row_token, padded_offsets, 
         _arg("x_codes", x_codes, _I8, (T, H), dev), _arg("x_scales", x_scales, _F32, (T,), dev),
         _arg("row_token", row_token, _INT, (M_cap,), dev), _arg("padded_offsets", padded_offsets, _INT, (E + 1,), dev),
         _arg("counts", counts, _INT, (E,), dev), _arg("w13_codes", w13_codes, _I8, (E, 2 * I, H), dev),
-        _arg("w13_scales", w13_scales, _F32, (E, 2 * I), dev), E, H, I, M_cap, max_rows_per_expert,
+        _arg("w13_scales", w13_scales, _F32, (E, 2 * I), dev), E, H, I, _rows_of(T, M_cap), max_rows_per_expert,
         _arg("h_bf16", h_bf16, _BF16, (M_cap, I), dev), st))
 
 
@@ -660,7 +667,8 @@ def moe_grouped_gemm(x, w, padded_offsets, counts, y, row_token=None, max_rows_p
         _arg("x", x, HALF_DTYPES, (rows if row_token is not None else M_cap, K), dev), HALF_DTYPES[x.dtype],
         None if row_token is None else _arg("row_token", row_token, _INT, (M_cap,), dev),
         _arg("padded_offsets", padded_offsets, _INT, (E + 1,), dev), _arg("counts", counts, _INT, (E,), dev),
-        _arg("w", w, dt, (E, N, K), dev), E, K, N, M_cap, max_rows_per_expert, _arg("y", y, dt, (M_cap, N), dev), st))
+        _arg("w", w, dt, (E, N, K), dev), E, K, N, _rows_of(rows, M_cap), max_rows_per_expert,
+        _arg("y", y, dt, (M_cap, N), dev), st))
 
 
 def moe_grouped_gemm_dgrad(dy, w, padded_offsets, counts, dx, stream=None):
@@ -690,5 +698,5 @@ def moe_grouped_gemm_wgrad(dy, x, padded_offsets, counts, dw, row_token=None, ac
         _arg("x", x, dt, (rows if row_token is not None else M_cap, K), dev), HALF_DTYPES[dy.dtype],
         None if row_token is None else _arg("row_token", row_token, _INT, (M_cap,), dev),
         _arg("padded_offsets", padded_offsets, _INT, (E + 1,), dev), _arg("counts", counts, _INT, (E,), dev), E, K, N,
-        M_cap, ANY_DTYPES.get(dw.dtype, -1), int(accumulate), _arg("dw", dw, (dy.dtype, torch.float32), (E, N, K), dev),
+        _rows_of(rows, M_cap), ANY_DTYPES.get(dw.dtype, -1), int(accumulate), _arg("dw", dw, (dy.dtype, torch.float32), (E, N, K), dev),
         st))

@@ -468,3 +468,16 @@ def test_no_rows():
     assert torch.all(dw == 3.0)
     mm.moe_grouped_gemm_wgrad(bf(0, 32), bf(0, 64), i32(5), i32(4), dw)
     assert not dw.any()
+
+
+def test_no_tokens_beside_padded_rows():
+    """Gathering from no tokens, with room for rows: no product; weights' gradients become 0, or stay with accumulate."""
+    counts, poff, rt = np.zeros(4, np.int32), np.zeros(5, np.int32), np.full(24, -1, np.int32)
+    x, w = torch.empty(0, 64, dtype=BF, device=DEV), torch.zeros(4, 32, 64, dtype=BF, device=DEV)
+    y, dw = torch.full((24, 32), 7.0, dtype=BF, device=DEV), torch.full((4, 32, 64), 3.0, device=DEV)
+    tab = on(poff), on(counts)
+    mm.moe_grouped_gemm(x, w, *tab, y, row_token=on(rt))
+    mm.moe_grouped_gemm_wgrad(y, x, *tab, dw, row_token=on(rt), accumulate=True)
+    assert torch.all(y == 7.0) and torch.all(dw == 3.0)
+    mm.moe_grouped_gemm_wgrad(y, x, *tab, dw, row_token=on(rt))
+    assert not dw.any()

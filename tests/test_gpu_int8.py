@@ -445,3 +445,20 @@ def test_layer_captured_and_two_layers_at_once(T):
         L2.forward_scores(x, z, W, stream=side, **kw)
         torch.cuda.synchronize()
         assert torch.equal(L.out, want) and torch.equal(L2.out, want)
+
+
+@pytest.mark.parametrize("P", [1, 16])
+@pytest.mark.parametrize("kind", ["int8", "mxfp4"])
+def test_layer_without_tokens(kind, P):
+    """A rank that got no token: an empty output, and the rows that padding leaves room for are not written."""
+    cls, W = {"int8": (layer.Int8MoELayer, layer.Int8MoEWeights), "mxfp4": (layer.MXMoELayer, layer.MXMoEWeights)}[kind]
+    w = W.empty(8, 256, 128, device=DEV)
+    for t in (w.w13_codes, w.w13_scales, w.w2_codes, w.w2_scales):
+        t.zero_()
+    L = cls(0, 2, 8, 256, 128, P, device=DEV)
+    L.h.fill_(7.0)
+    x, z = torch.empty(0, 256, dtype=torch.bfloat16, device=DEV), torch.empty(0, 8, device=DEV)
+    ids, wts = torch.empty(0, 2, dtype=torch.int32, device=DEV), torch.empty(0, 2, device=DEV)
+    assert L.forward(x, ids, wts, w).shape == (0, 256) and L.forward_scores(x, z, w).shape == (0, 256)
+    torch.cuda.synchronize()
+    assert not L.counts.any() and torch.all(L.h == 7.0) and len(L.h) == (8 * (P - 1))
