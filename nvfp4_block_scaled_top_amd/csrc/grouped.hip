@@ -47,6 +47,9 @@ __device__ __forceinline__ float g_silu(float g) {
   return g * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-g * 1.4426950408889634f));
 }
 
+// Parts of at most `of` that n is cut into, for any n of 31 bits (n + of - 1 would not fit).
+__device__ __forceinline__ int g_parts(int n, int of) { return n / of + (n % of > 0 ? 1 : 0); }
+
 // Workgroup barrier that no LDS access is moved across.  Vector memory loads stay in flight.
 __device__ __forceinline__ void g_barrier() {
   asm volatile("" ::: "memory");
@@ -788,7 +791,7 @@ __global__ __launch_bounds__(kGtThreads, 1) void gt_kernel(GroupedArgs p) {
       own4 += cnt / kGtRows + (l == 4);
       own2 += l == 2;
       own1 += l == 1;
-      ownf += (cnt + 63) / 64;
+      ownf += g_parts(cnt, 64);
     }
     const bool fine = gt_fine(g_total(own4), g_total(own2), g_total(own1), g_total(ownf), ntn, ntf,
                               (int)(((int64_t)p.K * GType<kDtype>::kBytes + kGtStage - 1) / kGtStage));
@@ -796,7 +799,7 @@ __global__ __launch_bounds__(kGtThreads, 1) void gt_kernel(GroupedArgs p) {
     const uint64_t below = ((uint64_t)1 << lane) - 1;
     for (int c = 0; c < E; c += kWave) {
       const int cnt = rows_of(c + lane), l = last(cnt % kGtRows);
-      const int own = fine ? (cnt + 63) / 64 : cnt / kGtRows + (l == 4);
+      const int own = fine ? g_parts(cnt, 64) : cnt / kGtRows + (l == 4);
       const int incl = g_scan(own);
       if (c + lane < E) pref[c + lane] = carry + incl - own;
       carry += __builtin_amdgcn_readlane(incl, kWave - 1);
@@ -910,7 +913,7 @@ __device__ __forceinline__ void gw_fine_phase(const GroupedWgradArgs& p) {
     x.row0 = g_scalar(p.padded_offsets + x.e);
     return x;
   };
-  const auto stages = [&](const Tile& x) { return x.cnt > 0 ? (x.cnt + kGwFineStage - 1) / kGwFineStage : 1; };
+  const auto stages = [&](const Tile& x) { return x.cnt > 0 ? g_parts(x.cnt, kGwFineStage) : 1; };
   const int64_t t0 = (blockIdx.x % 8) * (kGtGrid / 8) + blockIdx.x / 8;
   if (t0 >= total) return;
 
@@ -1056,14 +1059,14 @@ __device__ __forceinline__ bool gw_fine(const GroupedWgradArgs& p, bool gather) 
   int coarse = 0, fine = 0, most = 0;  // a tile of every expert, in tenths of a us; the largest count
   for (int e = lane_id(); e < p.E; e += kWave) {
     const int cnt = p.counts[e];
-    coarse += 14 * ((cnt + 63) / 64) + kGwTile;
-    fine += 5 * ((cnt + 127) / 128) + kGwFineTile;
+    coarse += 14 * g_parts(cnt, 64) + kGwTile;
+    fine += 5 * g_parts(cnt, kGwFineStage) + kGwFineTile;
     most = most > cnt ? most : cnt;
   }
   const int64_t all = (int64_t)g_total(coarse) * per, all_fine = (int64_t)g_total(fine) * perf;
   most = (int)wave_max_u32((uint32_t)most);
   if (gather && most > kGwMaxTokens) return false;
-  const int64_t one = 14 * (int64_t)((most + 63) / 64) + kGwTile, one_fine = 5 * (int64_t)((most + 127) / 128) + kGwFineTile;
+  const int64_t one = 14 * (int64_t)g_parts(most, 64) + kGwTile, one_fine = 5 * (int64_t)g_parts(most, kGwFineStage) + kGwFineTile;
   return (all_fine / kGtGrid > one_fine ? all_fine / kGtGrid : one_fine) < (all / kGtGrid > one ? all / kGtGrid : one);
 }
 
@@ -1098,7 +1101,7 @@ __global__ __launch_bounds__(kGtThreads, 1) void gt_weights_kernel(GroupedWgradA
     x.row0 = g_scalar(p.padded_offsets + x.e);
     return x;
   };
-  const auto stages = [&](const Tile& x) { return x.cnt > 0 ? (x.cnt + 63) / 64 : 1; };
+  const auto stages = [&](const Tile& x) { return x.cnt > 0 ? g_parts(x.cnt, 64) : 1; };
 
   const int64_t t0 = (blockIdx.x % 8) * (kGtGrid / 8) + blockIdx.x / 8;
   if (t0 >= total) return;
@@ -1338,7 +1341,7 @@ __global__ __launch_bounds__(kGsWaves* kWave, 1) void gs_kernel(GroupedArgs p, i
       int n = 0, tiles = 0;
       for (int c = 0; c < p.E; c += kWave) {
         const int cnt = c + lane < p.E ? p.counts[c + lane] : 0;
-        const int own = (cnt + mrows - 1) / mrows;
+        const int own = g_parts(cnt, mrows);
         const int incl = g_scan(own);
         const uint64_t any = __ballot(own > 0);
         const int at = n + __popcll(any & (((uint64_t)1 << lane) - 1));

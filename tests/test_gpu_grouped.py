@@ -481,3 +481,49 @@ def test_no_tokens_beside_padded_rows():
     assert torch.all(y == 7.0) and torch.all(dw == 3.0)
     mm.moe_grouped_gemm_wgrad(y, x, *tab, dw, row_token=on(rt))
     assert not dw.any()
+
+
+MOST = 2 ** 31 - 1  # rows that a call can have
+
+
+def repeated(block, rows):
+    """block again and again, cut at `rows`."""
+    t = torch.empty(rows, block.shape[1], dtype=block.dtype, device=DEV)
+    for a in range(0, rows, len(block)):
+        t[a:a + len(block)] = block[:rows - a]
+    return t
+
+
+def is_repeated(t, block):
+    return all(torch.equal(t[a:a + len(block)], block[:len(t) - a]) for a in range(0, len(t), len(block)))
+
+
+@pytest.mark.parametrize("bound", [0, 1])
+def test_as_many_rows_as_there_can_be(bound):
+    """One expert of 2^31 - 1 rows; whole numbers, whose sums bf16 holds exactly."""
+    gen = torch.Generator(device=DEV).manual_seed(1)
+    whole = lambda *s: torch.randint(-3, 4, s, generator=gen, device=DEV).to(BF)  # noqa: E731
+    block, w = whole(1000003, 8), whole(2, 8, 8)
+    tab = on(np.array([0, 0, MOST], np.int32)), on(np.array([0, MOST], np.int32))
+    x = repeated(block, MOST)
+    y = torch.full((MOST, 8), 7.5, dtype=BF, device=DEV)
+    mm.moe_grouped_gemm(x, w, *tab, y, max_rows_per_expert=bound)
+    assert is_repeated(y, (block.float() @ w[1].float().t()).to(BF))
+    if bound == 0:
+        y.fill_(7.5)
+        mm.moe_grouped_gemm_dgrad(x, w, *tab, y)
+        assert is_repeated(y, (block.float() @ w[1].float()).to(BF))
+
+
+def test_weights_gradient_of_as_many_rows_as_there_can_be():
+    """As above; all but a few rows of dy are 0, the last one not."""
+    gen = torch.Generator(device=DEV).manual_seed(2)
+    whole = lambda *s: torch.randint(-3, 4, s, generator=gen, device=DEV).to(BF)  # noqa: E731
+    block, few = whole(1000003, 8), whole(64, 8)
+    tab = on(np.array([0, MOST, MOST], np.int32)), on(np.array([MOST, 0], np.int32))
+    x, dy = repeated(block, MOST), torch.zeros(MOST, 8, dtype=BF, device=DEV)
+    at = torch.cat([torch.arange(0, MOST, MOST // 61, device=DEV)[:61], torch.tensor([MOST - 3, MOST - 2, MOST - 1], device=DEV)])
+    dy[at] = few
+    dw = torch.full((2, 8, 8), 7.5, device=DEV)
+    mm.moe_grouped_gemm_wgrad(dy, x, *tab, dw)
+    assert torch.equal(dw[0], few.float().t() @ block[at % len(block)].float()) and not dw[1].any()

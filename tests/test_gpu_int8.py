@@ -278,6 +278,19 @@ def test_linear_offsets_past_32_bits(M, N, K):
     assert not torch.isnan(out.view(-1)[:: 4099]).any() and not torch.isnan(out[:, -1]).any()
 
 
+@pytest.mark.parametrize("M", [2 ** 31 - 1, 2 ** 31 - 64])
+def test_linear_of_as_many_rows_as_there_can_be(M):
+    """The same rows again and again, whole sums that bf16 rounds once."""
+    gen = torch.Generator(device=DEV).manual_seed(3)
+    block, w = (torch.randint(-128, 128, (n, 16), dtype=torch.int8, device=DEV, generator=gen) for n in (1000003, 8))
+    a, out = torch.empty(M, 16, dtype=torch.int8, device=DEV), torch.full((M, 8), 7.5, dtype=torch.bfloat16, device=DEV)
+    for r in range(0, M, len(block)):
+        a[r:r + len(block)] = block[:M - r]
+    mm.int8_linear(a, torch.ones(M, device=DEV), w, torch.full((8,), 0.5, device=DEV), out)
+    want = (block.float() @ w.float().t() * 0.5).to(torch.bfloat16)  # sums below 2^24: exact in float32
+    assert all(torch.equal(out[r:r + len(block)], want[:M - r]) for r in range(0, M, len(block)))
+
+
 # ---- experts -------------------------------------------------------------------------------------
 
 def tables(counts, P, T, rng):
