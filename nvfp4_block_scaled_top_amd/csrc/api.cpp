@@ -725,7 +725,7 @@ static bool any_dtype_ok(int32_t d) { return dtype_ok(d) || d == MEGAMOE_DTYPE_F
 static bool half_dtype_ok(int32_t d) { return d == MEGAMOE_DTYPE_BF16 || d == MEGAMOE_DTYPE_F16; }
 
 static bool int8_matrix_ok(int64_t rows, int64_t cols) {
-  return rows >= 0 && cols > 0 && cols % 16 == 0 && cols < (1 << 30) && rows < ((int64_t)1 << 37) / cols;
+  return rows >= 0 && cols > 0 && cols % 16 == 0 && cols < (1 << 30) && rows <= (((int64_t)1 << 37) - 1) / cols;
 }
 
 int32_t int8_quantize_act(const void* x, int32_t dtype, int64_t rows, int64_t cols, const int32_t* row_valid,

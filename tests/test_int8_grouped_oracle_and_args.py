@@ -86,6 +86,15 @@ def test_int8_quantizer_refuses_bad_args(lib):
     assert d(FAKE, FAKE, 4, 64, 0, FAKE + 8, None) == -6
 
 
+@pytest.mark.parametrize("cols", [16, 48, 7168, (1 << 30) - 16])
+def test_int8_quantizer_takes_all_sizes_below_its_limit(lib, cols):
+    """The most rows that keep a tensor below 2^37 elements, and one more.  Without pointers the next check refuses."""
+    most = ((1 << 37) - 1) // cols
+    for rows, rc in ((most, -1), (most + 1, -2)):
+        assert lib.int8_quantize_act(None, 0, rows, cols, None, FAKE, FAKE, None) == rc
+        assert lib.int8_dequantize(None, FAKE, rows, cols, 0, FAKE, None) == rc
+
+
 @pytest.mark.parametrize("name", ["int8_linear", "int8_linear_gate_up_silu"])
 def test_int8_dense_products_refuse_bad_args(lib, name):
     def call(a=FAKE, sa=FAKE, M=4, K=256, w=FAKE, sw=FAKE, N=64, dtype=0, out=FAKE):
