@@ -475,3 +475,46 @@ def test_layer_without_tokens(kind, P):
     assert L.forward(x, ids, wts, w).shape == (0, 256) and L.forward_scores(x, z, w).shape == (0, 256)
     torch.cuda.synchronize()
     assert not L.counts.any() and torch.all(L.h == 7.0) and len(L.h) == (8 * (P - 1))
+
+
+# ---- one result whatever kernel runs -----------------------------------------------------------------
+
+@pytest.mark.parametrize("i", range(len(EXPERTS)))
+def test_experts_bits_do_not_depend_on_the_bound(i):
+    """The caller's bound changes which kernel runs (stream or tiles, m-tiles of 4, 8 or 16 rows), not a bit."""
+    counts, P, H, I = EXPERTS[i]
+    rng = np.random.default_rng(100 + i)
+    counts = np.array(counts, np.int32)
+    E, T = len(counts), max(int(counts.max()), 1) + 7
+    poff, row_token = tables(counts, P, T, rng)
+    M_cap, gen = len(row_token), torch.Generator(device=DEV).manual_seed(i)
+    code = lambda *s: torch.randint(-127, 128, s, dtype=torch.int8, device=DEV, generator=gen)  # noqa: E731
+    scale = lambda *s, m=1.0: (torch.rand(s, device=DEV, generator=gen) + 0.5) * m  # noqa: E731
+    x, xs, hc, hs = code(T, H), scale(T, m=0.01), code(M_cap, I), scale(M_cap, m=0.01)
+    w13, w13s, w2, w2s = code(E, 2 * I, H), scale(E, 2 * I, m=0.02 / H ** 0.5), code(E, H, I), scale(E, H, m=0.01)
+    rt, po, ct = dev(row_token), dev(poff), dev(counts)
+    first = None
+    for bound in (0, 1, 5, 16, 10 ** 6):
+        h, y = (torch.full((M_cap, n), 7.0, dtype=torch.bfloat16, device=DEV) for n in (I, H))
+        mm.moe_grouped_gemm_l1_silu_int8(x, xs, rt, po, ct, w13, w13s, h, max_rows_per_expert=bound)
+        mm.moe_grouped_gemm_l2_int8(hc, hs, po, ct, w2, w2s, y, max_rows_per_expert=bound)
+        first = first or (h, y)
+        assert torch.equal(h, first[0]) and torch.equal(y, first[1]), bound
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("N,K", [(48, 48), (528, 1040), (272, 7168), (4096, 2048)])
+def test_dense_bits_do_not_depend_on_the_rows(N, K, dtype):
+    """The first rows of a call of many as in a call of few: stream, tiles of 64 x 64, tiles of 256 columns."""
+    gen = torch.Generator(device=DEV).manual_seed(N)
+    M = 4200
+    a, w = (torch.randint(-127, 128, (n, K), dtype=torch.int8, device=DEV, generator=gen) for n in (M, N))
+    sa, sw = torch.rand(M, device=DEV, generator=gen) * 0.02, torch.rand(N, device=DEV, generator=gen) * 0.02 / K ** 0.5
+    whole, wide = torch.empty(M, N, dtype=dtype, device=DEV), torch.empty(M, N // 2, dtype=dtype, device=DEV)
+    mm.int8_linear(a, sa, w, sw, whole)
+    mm.int8_linear_gate_up_silu(a, sa, w, sw, wide)
+    for m in (1, 4, 7, 16, 17, 40, 200, 1500):
+        out, h = torch.empty(m, N, dtype=dtype, device=DEV), torch.empty(m, N // 2, dtype=dtype, device=DEV)
+        mm.int8_linear(a[:m], sa[:m], w, sw, out)
+        mm.int8_linear_gate_up_silu(a[:m], sa[:m], w, sw, h)
+        assert torch.equal(out, whole[:m]) and torch.equal(h, wide[:m]), m
