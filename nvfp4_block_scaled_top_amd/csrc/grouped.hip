@@ -99,8 +99,10 @@ struct GType {
   typedef f32x4 acc;
   static constexpr int kBytes = 2;
   static __device__ __forceinline__ void mfma(u32x4 a, u32x4 b, acc& c) {
-    if constexpr (kDtype == MEGAMOE_DTYPE_BF16) asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b));
-    else asm volatile("v_mfma_f32_16x16x32_f16 %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b));
+    if constexpr (kDtype == MEGAMOE_DTYPE_BF16)
+      asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b));
+    else
+      asm volatile("v_mfma_f32_16x16x32_f16 %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b));
   }
   static __device__ __forceinline__ acc product(u32x4 a, u32x4 b, acc c) {  // (the compiler's own, for chains)
     if constexpr (kDtype == MEGAMOE_DTYPE_BF16)
@@ -126,7 +128,8 @@ template <typename A, int n>
 __device__ __forceinline__ void g_settle(A (&c)[n]) {
   static_assert(n == 4 || n == 8, "fragments of a wave");
   if constexpr (n == 8)
-    asm volatile("s_nop 15\n\ts_nop 7" : "+a"(c[0]), "+a"(c[1]), "+a"(c[2]), "+a"(c[3]), "+a"(c[4]), "+a"(c[5]), "+a"(c[6]), "+a"(c[7]));
+    asm volatile("s_nop 15\n\ts_nop 7"
+                 : "+a"(c[0]), "+a"(c[1]), "+a"(c[2]), "+a"(c[3]), "+a"(c[4]), "+a"(c[5]), "+a"(c[6]), "+a"(c[7]));
   else
     asm volatile("s_nop 15\n\ts_nop 7" : "+a"(c[0]), "+a"(c[1]), "+a"(c[2]), "+a"(c[3]));
 }
@@ -137,25 +140,19 @@ __device__ __forceinline__ u32x4 lds_read16(uint32_t at) {
 __device__ __forceinline__ void lds_write16(uint32_t at, u32x4 v) {
   *reinterpret_cast<__attribute__((address_space(3))) u32x4*>(at) = v;
 }
-__device__ __forceinline__ u32x4 g_read16(uint64_t at) {
-  return *reinterpret_cast<const __attribute__((address_space(1))) u32x4*>(at);
-}
-__device__ __forceinline__ u32x4 g_read16(const uint8_t* base, uint32_t off) {  // wave-uniform base
-  return *reinterpret_cast<const __attribute__((address_space(1))) u32x4*>(
-      reinterpret_cast<const __attribute__((address_space(1))) uint8_t*>(scalar_addr(base)) + off);
-}
 template <typename T>
 __device__ __forceinline__ T lds_read(uint32_t at) {
   return *reinterpret_cast<const __attribute__((address_space(3))) T*>(at);
 }
 
-// A 16-row fragment of a side that lies across: LDS holds 64 rows of the reduced dimension, 512 bytes (256
-// columns) each.  The transposing read gives lane i of 16 lanes column i of the four rows by 16 columns whose
-// 8-byte pieces the lanes point at: two of them make the lane's eight values of K.
+// A 16-row fragment of a side that lies across: LDS holds rows of the reduced dimension, kRow bytes each (512: the
+// 256 columns of a large tile; 128: the 64 of a small one).  The transposing read gives lane i of 16 lanes column i of
+// the four rows by 16 columns whose 8-byte pieces the lanes point at: two of them make the lane's eight values of K.
+template <int kRow>
 __device__ __forceinline__ u32x4 lds_read_across(uint32_t at) {
   typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
   const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(reinterpret_cast<lds_s16x4*>(at));
-  const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(reinterpret_cast<lds_s16x4*>(at + 4 * 512));
+  const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(reinterpret_cast<lds_s16x4*>(at + 4 * kRow));
   const u32x2 l = __builtin_bit_cast(u32x2, lo), h = __builtin_bit_cast(u32x2, hi);
   return u32x4{l[0], l[1], h[0], h[1]};
 }
@@ -313,7 +310,8 @@ __device__ __forceinline__ void gt_phase(const GroupedArgs& p, int t0, int total
       a_at[i] = reinterpret_cast<uint64_t>(p.a) + (uint64_t)a_row(8 * (WB * wave + i) + ln / 8) * (uint64_t)(uint32_t)RB +
                 16 * a_piece(i);
     if constexpr (kAcross) {
-      w_at = uniform(static_cast<const uint8_t*>(p.w) + ((int64_t)ld.e * p.K + 8 * wave) * NB + (int64_t)ld.nt * cols * T::kBytes);
+      w_at = uniform(static_cast<const uint8_t*>(p.w) + ((int64_t)ld.e * p.K + 8 * wave) * NB +
+                     (int64_t)ld.nt * cols * T::kBytes);
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
         const int c = (ln & 31) ^ (((2 * q + (ln >> 5)) | ((wave & 1) << 2)) << 1);
@@ -331,7 +329,8 @@ __device__ __forceinline__ void gt_phase(const GroupedArgs& p, int t0, int total
       const uint32_t to = S::kScalesAt + (lseq % S::kBufs) * S::kScaleBuf;
       const int R = 64 * (wave & 3) + ln;
       if (wave < 4)
-        dma4(reinterpret_cast<const uint8_t*>(p.w_scales + (int64_t)ld.e * (kL1 ? 2 : 1) * p.N + (kL1 && is_up(R) ? p.N : 0) + w_col(R)),
+        dma4(reinterpret_cast<const uint8_t*>(p.w_scales + (int64_t)ld.e * (kL1 ? 2 : 1) * p.N +
+                                              (kL1 && is_up(R) ? p.N : 0) + w_col(R)),
              to + 256 * wave);
       else if (wave - 4 < WB)
         dma4(reinterpret_cast<const uint8_t*>(p.a_scales + a_row(R)), to + 4 * kGtCols + 256 * (wave - 4));
@@ -413,7 +412,7 @@ __device__ __forceinline__ void gt_phase(const GroupedArgs& p, int t0, int total
   };
   const auto read_one = [&](int st, int i) __attribute__((always_inline)) {
     if (i < MF) b[st][i] = lds_read16(rb + i * 16 * kGtStage);
-    else if constexpr (kAcross) a[st][i - MF] = lds_read_across((ra ^ ((i - MF) * 32)) + st * 32 * 512);
+    else if constexpr (kAcross) a[st][i - MF] = lds_read_across<512>((ra ^ ((i - MF) * 32)) + st * 32 * 512);
     else a[st][i - MF] = lds_read16(ra + (i - MF) * 16 * kGtStage);
   };
 
@@ -493,7 +492,8 @@ __device__ __forceinline__ void gt_phase(const GroupedArgs& p, int t0, int total
     const int c0 = cur.nt * cols + wn * 16 * kOutF + 16 * (g & 1) + 8 * (g >> 1);
     const auto put = [&](int R, int c, u32x4 v) __attribute__((always_inline)) {
       if (R < cur.left && c < p.N)
-        __builtin_nontemporal_store(v, reinterpret_cast<u32x4*>(static_cast<uint16_t*>(p.out) + (cur.row0 + R) * (int64_t)p.N + c));
+        __builtin_nontemporal_store(
+            v, reinterpret_cast<u32x4*>(static_cast<uint16_t*>(p.out) + (cur.row0 + R) * (int64_t)p.N + c));
     };
 #pragma unroll
     for (int m = 0; m < MF; ++m) {
@@ -580,7 +580,8 @@ __device__ __forceinline__ void gt_fine_phase(const GroupedArgs& p, int t0, int 
   uint64_t at[L];
   const auto fetch_rows = [&](int buf) __attribute__((always_inline)) {
     if (!kAcross && p.row_token != nullptr && wave == 0)
-      dma4(reinterpret_cast<const uint8_t*>(p.row_token + nx.row0 + (lane < nx.left ? lane : nx.left - 1)), kGfRowsAt + 4 * 64 * buf);
+      dma4(reinterpret_cast<const uint8_t*>(p.row_token + nx.row0 + (lane < nx.left ? lane : nx.left - 1)),
+           kGfRowsAt + 4 * 64 * buf);
   };
   const auto a_row = [&](int R) __attribute__((always_inline)) -> uint32_t {
     if (!kAcross && p.row_token != nullptr) return lds_read<uint32_t>(kGfRowsAt + 4 * (64 * (lseq & 1) + R));
@@ -691,11 +692,7 @@ __device__ __forceinline__ void gt_fine_phase(const GroupedArgs& p, int t0, int 
         for (int i = 0; i < 2; ++i) {
           b[st][i] = lds_read16(slot * kGfSlot + (b_at ^ (st * 64)) + i * 16 * kGfStage);
           if constexpr (kAcross) {
-            const uint32_t from = slot * kGfSlot + (a_at ^ (i * 32)) + st * 32 * 128;
-            typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
-            const u32x2 l = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(reinterpret_cast<lds_s16x4*>(from)));
-            const u32x2 h = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(reinterpret_cast<lds_s16x4*>(from + 4 * 128)));
-            a[st][i] = u32x4{l[0], l[1], h[0], h[1]};
+            a[st][i] = lds_read_across<128>(slot * kGfSlot + (a_at ^ (i * 32)) + st * 32 * 128);
           } else {
             a[st][i] = lds_read16(slot * kGfSlot + (a_at ^ (st * 64)) + i * 16 * kGfStage);
           }
@@ -727,7 +724,8 @@ __device__ __forceinline__ void gt_fine_phase(const GroupedArgs& p, int t0, int 
       f32x4 z[2];
 #pragma unroll
       for (int f = 0; f < 2; ++f) {
-        const typename T::acc sum = acc[m][f] + __builtin_bit_cast(typename T::acc, lds_read16(red + (2 * m + f) * 4 * kWave * 16));
+        const typename T::acc sum =
+            acc[m][f] + __builtin_bit_cast(typename T::acc, lds_read16(red + (2 * m + f) * 4 * kWave * 16));
         if constexpr (kI8) {
           const f32x4 sw = lds_read<f32x4>(sc + 4 * (wn * 32 + 16 * f + 4 * g));
           const float sa = lds_read<float>(sc + 256 + 4 * R);
@@ -941,8 +939,8 @@ __device__ __forceinline__ void gw_fine_phase(const GroupedWgradArgs& p) {
       for (int j = 0; j < L; ++j) {
         const int R = row(j), c = (lane & 7) ^ ((((R >> 1) & 1) | ((R >> 3) & 1) << 1) << 1);
         const int last = (int)(own_bytes / 16) - 1 - (dy ? ld.nt : ld.kt) * 8;
-        base[j] = reinterpret_cast<uint64_t>(dy ? p.dy : p.x) + 128 * (uint64_t)(dy ? ld.nt : ld.kt) + 16 * (c < last ? c : last) +
-                  (kGather && !dy ? 0 : (uint64_t)(ld.row0 * own_bytes));
+        base[j] = reinterpret_cast<uint64_t>(dy ? p.dy : p.x) + 128 * (uint64_t)(dy ? ld.nt : ld.kt) +
+                  16 * (c < last ? c : last) + (kGather && !dy ? 0 : (uint64_t)(ld.row0 * own_bytes));
       }
     }
 #pragma unroll
@@ -967,12 +965,6 @@ __device__ __forceinline__ void gw_fine_phase(const GroupedWgradArgs& p) {
   const int half = wave >> 2, wm = ww >> 1, wn = ww & 1, r = lane & 15, g = lane >> 4, jj = r >> 2;
   const uint32_t across = (64 * half + 8 * g + jj) * 128 + (lane & 3) * 8, v = (jj >> 1) | (g & 1) << 1;
   const uint32_t a_at = across + ((2 * wn) ^ v) * 32, b_at = kGfSide + across + ((2 * wm) ^ v) * 32;
-  const auto read = [&](uint32_t from) __attribute__((always_inline)) {
-    typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
-    const u32x2 l = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(reinterpret_cast<lds_s16x4*>(from)));
-    const u32x2 h = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(reinterpret_cast<lds_s16x4*>(from + 4 * 128)));
-    return u32x4{l[0], l[1], h[0], h[1]};
-  };
   int slot = 0;
   for (int64_t t = t0; t < total; t += kGtGrid) {
     const Tile cur = find(t);
@@ -997,8 +989,8 @@ __device__ __forceinline__ void gw_fine_phase(const GroupedWgradArgs& p) {
       for (int st = 0; st < 2; ++st)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          a[st][i] = read(slot * kGfSlot + (a_at ^ (i * 32)) + st * 32 * 128);
-          b[st][i] = read(slot * kGfSlot + (b_at ^ (i * 32)) + st * 32 * 128);
+          a[st][i] = lds_read_across<128>(slot * kGfSlot + (a_at ^ (i * 32)) + st * 32 * 128);
+          b[st][i] = lds_read_across<128>(slot * kGfSlot + (b_at ^ (i * 32)) + st * 32 * 128);
         }
       load(slot == 0 ? D - 1 : slot - 1);
 #pragma unroll
@@ -1066,7 +1058,8 @@ __device__ __forceinline__ bool gw_fine(const GroupedWgradArgs& p, bool gather) 
   const int64_t all = (int64_t)g_total(coarse) * per, all_fine = (int64_t)g_total(fine) * perf;
   most = (int)wave_max_u32((uint32_t)most);
   if (gather && most > kGwMaxTokens) return false;
-  const int64_t one = 14 * (int64_t)g_parts(most, 64) + kGwTile, one_fine = 5 * (int64_t)g_parts(most, kGwFineStage) + kGwFineTile;
+  const int64_t one = 14 * (int64_t)g_parts(most, 64) + kGwTile;
+  const int64_t one_fine = 5 * (int64_t)g_parts(most, kGwFineStage) + kGwFineTile;
   return (all_fine / kGtGrid > one_fine ? all_fine / kGtGrid : one_fine) < (all / kGtGrid > one ? all / kGtGrid : one);
 }
 
@@ -1133,7 +1126,7 @@ __global__ __launch_bounds__(kGtThreads, 1) void gt_weights_kernel(GroupedWgradA
     }
   };
   uint32_t tok[4];
-  bool done = false;  // with nothing left the last stage is loaded again, into registers that no one reads
+  bool done = false;  // with nothing left the last stage is loaded again, into a slot that no product reads
   const auto begin = [&]() __attribute__((always_inline)) {  // of the stage at (lt, lks)
     if (lks == 0) enter();
     if (kGather) {
@@ -1186,8 +1179,8 @@ __global__ __launch_bounds__(kGtThreads, 1) void gt_weights_kernel(GroupedWgradA
     asm volatile("" : "+v"(ra), "+v"(rb));
   };
   const auto read_one = [&](int st, int i) __attribute__((always_inline)) {
-    if (i < MF) b[st][i] = lds_read_across((rb ^ (i * 32)) + st * 32 * 512);
-    else a[st][i - MF] = lds_read_across((ra ^ ((i - MF) * 32)) + st * 32 * 512);
+    if (i < MF) b[st][i] = lds_read_across<512>((rb ^ (i * 32)) + st * 32 * 512);
+    else a[st][i - MF] = lds_read_across<512>((ra ^ ((i - MF) * 32)) + st * 32 * 512);
   };
 
   fetch(ld, 0, 0);
@@ -1632,12 +1625,14 @@ hipError_t launch_grouped(const GroupedArgs& a, bool l1, int64_t max_rows, hipSt
   const bool dense = a.counts == nullptr;
   const int64_t rows = dense ? a.M : max_rows;
   if (!(rows > 0 && rows <= kGsRows)) {
-    if (a.dtype == kOperandI8) return l1 ? launch_gt<kGtGateUp, kOperandI8>(a, stream) : launch_gt<kGtPlain, kOperandI8>(a, stream);
+    if (a.dtype == kOperandI8)
+      return l1 ? launch_gt<kGtGateUp, kOperandI8>(a, stream) : launch_gt<kGtPlain, kOperandI8>(a, stream);
     return a.dtype == MEGAMOE_DTYPE_BF16 ? launch_gt<kGtPlain, MEGAMOE_DTYPE_BF16>(a, stream)
                                          : launch_gt<kGtPlain, MEGAMOE_DTYPE_F16>(a, stream);
   }
   const GsPlan plan = gs_plan(a, rows);
-  if (a.dtype == kOperandI8) return l1 ? launch_gs<true, kOperandI8>(a, plan, stream) : launch_gs<false, kOperandI8>(a, plan, stream);
+  if (a.dtype == kOperandI8)
+    return l1 ? launch_gs<true, kOperandI8>(a, plan, stream) : launch_gs<false, kOperandI8>(a, plan, stream);
   return a.dtype == MEGAMOE_DTYPE_BF16 ? launch_gs<false, MEGAMOE_DTYPE_BF16>(a, plan, stream)
                                        : launch_gs<false, MEGAMOE_DTYPE_F16>(a, plan, stream);
 }

@@ -232,9 +232,10 @@ hipError_t launch_int8_dequant(const int8_t* codes, const float* scales, int64_t
   const uint8_t* c = reinterpret_cast<const uint8_t*>(codes);
   u32x4* o = static_cast<u32x4*>(out);
   const uint32_t per = (uint32_t)pieces;
-  if (dtype == MEGAMOE_DTYPE_F32) hipLaunchKernelGGL((i8_dequant_kernel<MEGAMOE_DTYPE_F32>), grid, block, 0, stream, c, scales, total, per, o);
-  else if (dtype == MEGAMOE_DTYPE_BF16) hipLaunchKernelGGL((i8_dequant_kernel<MEGAMOE_DTYPE_BF16>), grid, block, 0, stream, c, scales, total, per, o);
-  else hipLaunchKernelGGL((i8_dequant_kernel<MEGAMOE_DTYPE_F16>), grid, block, 0, stream, c, scales, total, per, o);
+  const auto kernel = dtype == MEGAMOE_DTYPE_F32    ? i8_dequant_kernel<MEGAMOE_DTYPE_F32>
+                      : dtype == MEGAMOE_DTYPE_BF16 ? i8_dequant_kernel<MEGAMOE_DTYPE_BF16>
+                                                    : i8_dequant_kernel<MEGAMOE_DTYPE_F16>;
+  hipLaunchKernelGGL(kernel, grid, block, 0, stream, c, scales, total, per, o);
   return hipGetLastError();
 }
 
