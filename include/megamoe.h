@@ -744,9 +744,10 @@ int32_t int8_linear_gate_up_silu(const int8_t* a_codes, const float* a_scales, i
  * max_rows_per_expert  a bound on counts[e] the caller expects, or 0 if none: it may change which
  *              kernels launch, never the results; a bound that is too low costs time only.
  * h_bf16 bf16 [M_cap, I];  y_bf16 bf16 [M_cap, H].
- * Limits: E as for moe_route_permute; H, I and alignment as K, N and alignment of int8_linear; x and h below
- * 2^36 bytes (T is not an argument: T <= M_cap with M_cap as above).  With M_cap == 0 the row arrays may be
- * NULL and the call enqueues nothing; pass 0 when T is 0, whatever the padding leaves room for.
+ * Limits: E as for moe_route_permute; H, I and alignment as K, N and alignment of int8_linear; M_cap rows of
+ * the call's codes below 2^36 bytes, x's too (T is not an argument: T <= M_cap with M_cap as above).  With
+ * M_cap == 0 the row arrays may be NULL and the call enqueues nothing; pass 0 when T is 0, whatever the padding
+ * leaves room for.
  * ---------------------------------------------------------------------------------------- */
 int32_t moe_grouped_gemm_l1_silu_int8(const int8_t* x_codes, const float* x_scales, const int32_t* row_token,
                                       const int32_t* padded_offsets, const int32_t* counts,
@@ -780,9 +781,10 @@ int32_t moe_grouped_gemm_l2_int8(const int8_t* h_codes, const float* h_scales, c
  *              sched is not read).
  * max_rows_per_expert  as for moe_grouped_gemm_l2_mxfp4.
  * Limits: E as for moe_route_permute; K and N >= 8, multiples of 8 and below 2^22; 0 <= M_cap < 2^31,
- * x and dy below 2^36 bytes each (T <= M_cap); pointers aligned to 16 bytes, the tables to 4; no output
- * overlaps an input.  With M_cap == 0 the row arrays may be NULL; y and dx are then not written, dw as above.
- * Pass 0 when T is 0, whatever the padding leaves room for.
+ * M_cap rows of x's, dy's or both, as the call reads them, below 2^36 bytes each (T is not an argument:
+ * T <= M_cap); pointers aligned to 16 bytes, the tables to 4; no output overlaps an input.  With M_cap == 0
+ * the row arrays may be NULL; y and dx are then not written, dw as above.  Pass 0 when T is 0, whatever the
+ * padding leaves room for.
  * ---------------------------------------------------------------------------------------- */
 int32_t moe_grouped_gemm(const void* x, int32_t dtype, const int32_t* row_token, const int32_t* padded_offsets,
                          const int32_t* counts, const void* w, int32_t E, int32_t K, int32_t N, int64_t M_cap,

@@ -229,11 +229,13 @@ __device__ __forceinline__ void g_whole_lines(u32x4& lo, u32x4& hi) {
 // read all of s: it waits for its loads of stage s + 1, and one barrier makes everyone's visible and says that
 // s's slot is free, into which the second step requests the stage after the ring's last.
 //
-// Many rows: matrix instructions, memory's latency and the power.  int8 16384 x 4096 x 7168 takes 350 us (2750 TOPS; 275
-// on zeros), bf16 16384 x 7168 x 4096 727 (1320 TFLOP/s), 16384 x 2048 x 7168 362, 24 experts of 1024 rows across, 7168 to 4096, 1150.  Few rows: the weights' bytes, 48
-// experts of 40 rows, 7168 to 4096, 404 us (7.1 TB/s).  4 waves of 128 x 128 read a third less from LDS: 657 us for the bf16 product,
-// the same for int8, 942 where 8 waves take 789 for the weights' gradient.  Operands staged through registers: 379 where these
-// loads took 358.  Touching the next stages in the L2 first: 3 to 10% slower.
+// Many rows: matrix instructions, memory's latency and the power.  int8 16384 x 4096 x 7168 takes 350 us in runs of
+// 50 ms (2750 TOPS; 275 us on zeros) and up to 400 in longer ones, as the clock falls; bf16 16384 x 7168 x 4096 727 (1320
+// TFLOP/s), 16384 x 2048 x 7168 362, 24 experts of 1024 rows across, 7168 to 4096, 1150.  Few rows: the weights' bytes,
+// 48 experts of 40 rows, 7168 to 4096, 404 us (7.1 TB/s), 8 experts of one row across 80 (5.9).  4 waves of 128 x 128
+// read a third less from LDS: 657 us for the bf16 product, the same for int8, 942 where 8 waves take 789 for the
+// weights' gradient.  Operands staged through registers: 379 where these loads took 358.  Touching the next stages in
+// the L2 first: 3 to 10% slower.
 // ============================================================================================
 template <int WB>
 struct GtShape {
@@ -754,9 +756,9 @@ __device__ __forceinline__ void gt_fine_phase(const GroupedArgs& p, int t0, int 
 }
 
 // Whether the tiles of 64 take the call: the time of the fullest workgroup either way, of tiles of nks stages.
-// (Large and small tiles, us: int8 256 x 4096 x 7168 71 and 16, 1024 rows 86 and 51, 2048 rows 88 and 99; bf16 16 experts of 288 rows, 3640 to
-// 176, 118 and 19; 64 of 94 rows, 2048 to 7168, 402 and 534; 48 of 40 rows, 7168 to 4096, 404 and 479; 8 of 32, 512 to 1024, 10.7
-// and 7.2; across, 24 of 100 rows, 2048 to 1024, 39 and 28.)
+// (Large and small tiles, us: int8 256 x 4096 x 7168 71 and 16, 1024 rows 86 and 51, 2048 rows 88 and 99; bf16 16
+// experts of 288 rows, 3640 to 176, 118 and 19; 64 of 94 rows, 2048 to 7168, 402 and 534; 48 of 40 rows, 7168 to 4096,
+// 404 and 479; 8 of 32, 512 to 1024, 10.7 and 7.2; across, 24 of 100 rows, 2048 to 1024, 39 and 28.)
 // In float32: a division of 64-bit integers lasts longer than all of the rest.
 __device__ __forceinline__ bool gt_fine(int m4, int m2, int m1, int mf, int ntn, int ntf, int nks) {
   const float t4 = (float)(nks * kGtNs4[0] + kGtNs4[1]), t2 = (float)(nks * kGtNs2[0] + kGtNs2[1]);
@@ -862,8 +864,9 @@ __global__ __launch_bounds__(kGtThreads, 1) void gt_kernel(GroupedArgs p) {
 //
 // Long experts: as the rows (16384 x 7168 x 4096: 789 us, 1220 TFLOP/s).  Short ones: the gradients' stores, which
 // no products run beside, since all workgroups store at about the same time (48 experts of 512 rows, float32 7168 x
-// 4096: 2080 us, 1250 without the stores; of 64 experts of 32 rows 1440, 5.3 TB/s).  Tiles of another order for each XCD, so
-// that they store at other times: slower.
+// 4096: 2080 us, 1250 without the stores; of 64 experts of 32 rows 1440, 5.3 TB/s; in 16 bits 1590 and 840).  With
+// accumulate the old values are read between the products and the stores, beside nothing else: 3470 and 3550 (3.4 and
+// 4.2 TB/s), in 16 bits 2640 and 2520.  Tiles of another order for each XCD, so that they store at other times: slower.
 // ============================================================================================
 constexpr int kGwSlot = 2 * kGtSide;
 constexpr int kGwTokens = 2 * kGwSlot;               // LDS: the waves' tokens of two stages' rows
@@ -1044,8 +1047,8 @@ __device__ __forceinline__ void gw_fine_phase(const GroupedWgradArgs& p) {
 }
 
 // Whether the tiles of 64 x 64 take the call: the time of the fullest workgroup either way, from the counts.  (Large and
-// small tiles, us: 4 experts of 945 rows, 40 x 696, 25.8 and 8.2; 4 of 2233, 160 x 816, 57 and 16; 1 of 469, 3496 x 456, 22 and 11;
-// 8 of 15, 520 x 1032, 12.3 and 13.3; 48 of 100, 1024 x 1024, 42 and 91.)
+// small tiles, us: 4 experts of 945 rows, 40 x 696, 25.8 and 8.2; 4 of 2233, 160 x 816, 57 and 16; 1 of 469, 3496 x 456,
+// 22 and 11; 8 of 15, 520 x 1032, 12.3 and 13.3; 48 of 100, 1024 x 1024, 42 and 91.)
 __device__ __forceinline__ bool gw_fine(const GroupedWgradArgs& p, bool gather) {
   const int64_t per = (int64_t)((p.K + 255) / 256) * ((p.N + 255) / 256), perf = (int64_t)((p.K + 63) / 64) * ((p.N + 63) / 64);
   int coarse = 0, fine = 0, most = 0;  // a tile of every expert, in tenths of a us; the largest count
@@ -1283,9 +1286,10 @@ __global__ __launch_bounds__(kGtThreads, 1) void gt_weights_kernel(GroupedWgradA
 // part of the weight rows through an LDS ring of its own, 16 rows by 256 bytes a slot with the m-tile's token rows
 // beside them (they come from the L2), by direct loads: no barrier, no registers, and the ring runs on across groups,
 // m-tiles and experts.  kSplit: the 4 waves split K; at a group's end they leave their sums in LDS and one of them
-// adds the four in wave order.  Otherwise every wave takes groups of its own.  8 x 7168 x 2048 int8 takes 7.0 us, of which
-// 5.3 are a launch and its call; int8 gate+up of 8 tokens, 7168 to
-// 2 x 2048, at 5 experts 25 (5.8 TB/s), at 11 51 (6.4); bf16, 7168 to 4096, 47 (6.3) and 98 (6.6).
+// adds the four in wave order.  Otherwise every wave takes groups of its own.  int8 gate+up of 8 tokens, 7168 to
+// 2 x 2048, takes 25 us at 5 experts (5.8 TB/s), 51 at 11 (6.4); bf16, 7168 to 4096, 47 (6.3) and 98 (6.6).  Small
+// calls are bound by the start and by groups taken in turn, on the GPU: 8 x 7168 x 2048 int8, whose bytes take 2.1 us,
+// takes 6.8 us a call and 7.2 to 7.5 in a kernel trace, as most workgroups take two groups with a barrier each.
 //
 // Both operands keep 16-byte piece c of row R at place c ^ R of the row's 256 bytes: the 16 rows of one piece are
 // read from 16 different places.
@@ -1586,10 +1590,11 @@ struct GsPlan {
 static GsPlan gs_plan(const GroupedArgs& a, int64_t rows) {
   GsPlan g;
   const int64_t chunks = ((int64_t)a.K * (a.dtype == kOperandI8 ? 1 : 2) + kGsChunk - 1) / kGsChunk;
-  // A group of 16 chunks and more is split (a wave of 8 alone streams 5.8 TB/s of 9 experts' int8 gate+up, 7168 long,
-  // that all four stream at 5.8 with half the groups' imbalance: 45.6 us, 49.9 unsplit).  A shorter one has too few
-  // chunks between two barriers (48 experts' int8 down projection, 2048 long: 137 us split, 104 unsplit), and is split
-  // only where a dense call has too few groups for the waves (8 x 7168 x 2048 int8: 6.9 us, 7.9 unsplit).
+  // Split and unsplit, us, int8.  Experts of one row, by chunks of K: 48 with 7168 outputs, 4 chunks 99 and 58, 8 137 and
+  // 105, 14 208 and 186, 16 219 and 217; 8 of them, 14 chunks 39 and 36, 16 40 and 49; so from 16 on.  Dense calls of 8
+  // rows, which have few groups for the waves, by groups: 300, 8 chunks 6.8 and 7.8, 16 9.0 and 11.6; 448, 4 chunks 6.5
+  // and 6.5, 6 6.7 and 6.8, 8 6.9 and 7.8; 512, 8 chunks 6.8 and 7.7; 600, 8 chunks 8.6 and 7.9, 14 11.4 and 10.9; 1024,
+  // 8 chunks 10.3 and 8.4, 16 14.5 and 14.1: from 8 chunks on, where no workgroup takes more than two groups.
   const int64_t groups = (a.N + 15) / 16;
   g.split = chunks >= kGsSplitChunks || (chunks >= kGsSplitChunks / 2 && a.counts == nullptr && groups <= 2 * kGtGrid);
   g.mrows = rows > 0 && rows <= 4 ? 4 : rows > 0 && rows <= 8 ? 8 : kGsRows;
