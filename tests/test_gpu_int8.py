@@ -518,3 +518,24 @@ def test_dense_bits_do_not_depend_on_the_rows(N, K, dtype):
         mm.int8_linear(a[:m], sa[:m], w, sw, out)
         mm.int8_linear_gate_up_silu(a[:m], sa[:m], w, sw, h)
         assert torch.equal(out, whole[:m]) and torch.equal(h, wide[:m]), m
+
+
+@pytest.mark.parametrize("rows,cols", [(5 * 2 ** 20 + 3, 2064), (5 * 2 ** 20 + 3, 64)])
+def test_quantize_and_decode_beyond_one_grid(rows, cols):
+    """More rows, and pieces of output, than a grid has places for: a workgroup a row, and a wave a row."""
+    gen = torch.Generator(device=DEV).manual_seed(9)
+    few = (torch.randn(10007, cols, generator=gen, device=DEV) * 0.3).to(torch.bfloat16)
+    x, row_valid = torch.empty(rows, cols, dtype=torch.bfloat16, device=DEV), torch.zeros(rows, dtype=torch.int32, device=DEV)
+    for a in range(0, rows, len(few)):
+        x[a:a + len(few)] = few[:rows - a]
+    row_valid[rows - 2] = -1
+    c, s = torch.full((rows, cols), 77, dtype=torch.int8, device=DEV), torch.full((rows,), 77.0, device=DEV)
+    mm.int8_quantize_act(x, c, s, row_valid=row_valid)
+    x.fill_(7.0)
+    mm.int8_dequantize(c, s, x)
+    fc, fs = Q.quantize(host(few))
+    small = dev(fc), dev(fs), torch.from_numpy(Q.dequantize(fc, fs)).to(torch.bfloat16).to(DEV)
+    for t, f in zip((c, s, x), small):
+        assert not t[rows - 2].any()
+        t[rows - 2] = f[(rows - 2) % len(few)]
+        assert all(torch.equal(t[a:a + len(few)], f[:rows - a]) for a in range(0, rows, len(few)))
